@@ -68,9 +68,12 @@ typedef enum {
   DG_F16 = 0,   /* IEEE binary16 */
   DG_I8 = 1,    /* two's-complement int8 */
   DG_E2M1 = 2,  /* 4-bit float: sign | 2-bit exponent (bias 1) | 1-bit mantissa */
-  DG_MXF4 = 3   /* block-scaled E2M1 (MXFP4): E2M1 codes packed as for DG_E2M1, plus one
+  DG_MXF4 = 3,  /* block-scaled E2M1 (MXFP4): E2M1 codes packed as for DG_E2M1, plus one
                    E8M0 scale byte (2^(e - 127); 255 = NaN) per 32 codes along K.  Taken by
                    dg_quantize_mxf4, dg_gemm_mxf4 and dg_plan_tiles (pair DG_MXF4 x DG_MXF4) */
+  /* taken by the FP8 and expert-routing entry points only */
+  DG_BF16 = 4,  /* bfloat16 */
+  DG_F32 = 5    /* IEEE binary32 */
 } dg_dtype;
 
 /* Fused epilogue applied to t = alpha*acc + beta*C:  bias adds bias[j] to t,
@@ -421,6 +424,158 @@ dg_status dg_gemm_thin_noalloc(int64_t M, int64_t N, int64_t K, dg_dtype dtype_a
                                dg_dtype dtype_b, const void *A, int64_t lda, const void *B,
                                int64_t ldb, void *C, const void *bias, float alpha, float beta,
                                dg_epilogue epilogue, dg_stream_t stream);
+
+/* ---------------------------------------------------------------- 8-bit float
+ * FP8 operands are E4M3 codes (sign | 4-bit exponent, bias 7 | 3-bit mantissa;
+ * largest finite value 448; 0x7F and 0xFF are NaN; no infinities), one byte
+ * each, with one FP32 scale for each block of 128 values along K: a code
+ * stands for e4m3(code) * scale.  A block is 1 x 128 (one row: activations,
+ * and both operands of a weight gradient) or 128 x 128 (weights).  The pages
+ * ask for precisions as triples {weight, activation, output} (discosf.com/
+ * news/5532976, section 2.2 layer 2) and name no 8-bit float; this is the
+ * format with block scales that models trained and served in 8 bits use.
+ */
+
+/* Block quantization of X (rows x K, FP16 or BF16, row pitch ldx elements).
+ *   A block's scale is s = max(amax, 448 * 2^-126) / 448 with amax its largest
+ *   magnitude, and a value's code is e4m3(v * (448 / max(amax, 448 * 2^-126)))
+ *   rounded to nearest, ties to even (both quotients and the product are
+ *   FP32).  A block that holds a NaN or an infinity gets codes 0 and the scale
+ *   NaN.  Blocks at the edges hold what is there.
+ *   block_rows: 1 (blocks of 1 x 128) or 128 (128 x 128).
+ *   codes (or NULL): rows x K, row pitch ldq bytes (>= K, a multiple of 16);
+ *     scales: ceil(rows / block_rows) x ceil(K / 128) FP32, row pitch lds
+ *     elements.  Blocks lie along K.
+ *   codes_t (or NULL): the transposed matrix, K x rows, row pitch ldqt bytes
+ *     (>= rows, a multiple of 16), quantized along ITS rows: scales_t is
+ *     ceil(K / block_rows) x ceil(rows / 128), row pitch ldst.  This is the
+ *     operand of the products that contract over the rows of X (weight
+ *     gradients: block_rows 1) or take the weights transposed (input
+ *     gradients: block_rows 128).
+ *   X, codes and codes_t are 16-byte aligned and ldx is a multiple of 8; bytes
+ *   of a row of codes past its length are not written.  With both outputs X
+ *   is read once.  One launch; rows == 0 or K == 0 is a no-op.
+ * Errors: DG_ERR_INVALID_ARG for sizes, pointers or pitches that break these
+ * rules or when both outputs are NULL; DG_ERR_UNSUPPORTED for another type. */
+dg_status dg_quantize_fp8(int64_t rows, int64_t K, dg_dtype dtype_x, const void *X, int64_t ldx,
+                          int block_rows, void *codes, int64_t ldq, float *scales, int64_t lds,
+                          void *codes_t, int64_t ldqt, float *scales_t, int64_t ldst,
+                          dg_stream_t stream);
+
+/* D = epilogue(alpha * A.B^T + beta * D) for FP8 A (M x K) and B (N x K):
+ *   t[i,j] = sum over blocks b of  scale_a[i,b] * scale_b[j,b] *
+ *            sum over k in block b of  e4m3(A[i,k]) * e4m3(B[j,k])
+ * with the inner sums and their scaled total in FP32.
+ *   A, B: codes, row pitches lda, ldb bytes (>= K, multiples of 16, 16-byte
+ *     aligned bases).  scale_a: M rows of lds_a >= ceil(K / 128) FP32.
+ *     scale_b: N rows (block_rows_b == 1) or ceil(N / 128) rows
+ *     (block_rows_b == 128) of lds_b FP32.
+ *   D: M x N of dtype_d (DG_F16, DG_BF16 or DG_F32), row pitch ldd >= N
+ *     elements, 16-byte aligned, read only when beta != 0 (in place; columns
+ *     N .. ldd - 1 are never touched).  bias: [N] of dtype_d, read only by the
+ *     bias epilogues.  Epilogues as dg_gemm.
+ *   M == 0 or N == 0 is a no-op; K == 0 gives epilogue(beta * D).
+ * Few rows (M <= 16) run a streaming kernel that reads each weight once; more
+ * run on tcgen05 with the block sums scaled and added in registers.  Nothing
+ * is allocated.
+ * Errors: as dg_gemm, with these rules. */
+dg_status dg_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
+                      const float *scale_a, int64_t lds_a, const void *B, int64_t ldb,
+                      const float *scale_b, int64_t lds_b, int block_rows_b, void *D,
+                      dg_dtype dtype_d, int64_t ldd, const void *bias, float alpha, float beta,
+                      dg_epilogue epilogue, dg_stream_t stream);
+
+/* The FP8 product of a mixture of experts, one for each expert e of `count`:
+ *   D[i,:] = epilogue(alpha * A[i,:].B_e^T + beta * D[i,:]),
+ *   offsets[e] <= i < offsets[e+1]
+ * over `rows` rows sorted by expert (dg_moe_sort).  offsets: DEVICE array of
+ * count + 1 int32, so the host waits for nothing.
+ *   B_e = B + e * stride_b codes, scale_b_e = scale_b + e * stride_sb (128 x
+ *   128 blocks: ceil(N / 128) rows of lds_b), bias_e = bias + e * stride_bias;
+ *   stride_b is a multiple of ldb and at least N * ldb.  Rows outside every
+ *   segment are neither read nor written.  Offsets are taken as clamped to
+ *   [0, rows]; an end before its start is an empty segment.
+ *   count is at most 1024.  Other rules as dg_gemm_fp8. */
+dg_status dg_gemm_fp8_grouped(int64_t count, int64_t rows, int64_t N, int64_t K, const void *A,
+                              int64_t lda, const float *scale_a, int64_t lds_a, const void *B,
+                              int64_t ldb, int64_t stride_b, const float *scale_b, int64_t lds_b,
+                              int64_t stride_sb, const int32_t *offsets, void *D,
+                              dg_dtype dtype_d, int64_t ldd, const void *bias,
+                              int64_t stride_bias, float alpha, float beta, dg_epilogue epilogue,
+                              dg_stream_t stream);
+
+/* Its weight gradients, one M x N product over each expert's rows:
+ *   D_e = alpha * sum over offsets[e] <= r < offsets[e+1] of A[:,r] B[:,r]^T
+ *         + beta * D_e,  D_e = D + e * stride_d
+ * A: M x rows and B: N x rows codes with 1 x 128 scales along the rows of the
+ * sorted batch (the transposed output of dg_quantize_fp8).  offsets: device
+ * array of count + 1 int32, each a multiple of 128 (dg_moe_sort with align
+ * 128; padding rows are zero): one that is not is rounded down to it and
+ * DG_ERR_INVALID_ARG is recorded in the status word.  An empty segment gives
+ * beta * D_e.  Other rules as dg_gemm_fp8. */
+dg_status dg_gemm_fp8_grouped_wgrad(int64_t count, int64_t M, int64_t N, int64_t rows,
+                                    const void *A, int64_t lda, const float *scale_a,
+                                    int64_t lds_a, const void *B, int64_t ldb,
+                                    const float *scale_b, int64_t lds_b, const int32_t *offsets,
+                                    void *D, dg_dtype dtype_d, int64_t ldd, int64_t stride_d,
+                                    float alpha, float beta, dg_stream_t stream);
+
+/* ------------------------------------------------- tokens and their experts */
+
+/* Sorts the tokens' choices by expert (stable: by expert, then by slot
+ * s = t * top_k + j).  ids: tokens x top_k int32, row pitch top_k; a choice
+ * outside [0, count) is dropped.
+ *   offsets: count + 1 int32; expert e's rows are offsets[e] .. offsets[e+1],
+ *     its segment rounded up to a multiple of `align` (a power of two up to
+ *     1024).
+ *   row_slot: `rows` int32: the slot that each sorted row holds, -1 for
+ *     padding and for rows past offsets[count].  rows is at least
+ *     dg_moe_rows(tokens, top_k, count, align).
+ *   slot_row: tokens x top_k int32: the row of each slot, -1 if dropped.
+ * One launch; nothing is allocated; count is at most 1024. */
+dg_status dg_moe_sort(int64_t tokens, int64_t top_k, int64_t count, const int32_t *ids,
+                      int64_t align, int64_t rows, int32_t *offsets, int32_t *row_slot,
+                      int32_t *slot_row, dg_stream_t stream);
+
+/* The most rows a sort can need: tokens * top_k plus the padding of every
+ * expert that can have a row, rounded up to `align`; -1 for invalid sizes. */
+int64_t dg_moe_rows(int64_t tokens, int64_t top_k, int64_t count, int64_t align);
+
+/* The tokens' rows in sorted order: D[r,:] = X[row_slot[r] / top_k,:], zeros
+ * where row_slot[r] is -1 (X: FP16 or BF16, D the same type; bases 16-byte
+ * aligned, pitches multiples of 8 elements).  Slots of tokens past `tokens`
+ * give zeros too.  Its gradient is dg_moe_combine without weights. */
+dg_status dg_moe_dispatch(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
+                          const void *X, int64_t ldx, int64_t rows, const int32_t *row_slot,
+                          void *D, int64_t ldd, dg_stream_t stream);
+
+/* The same, quantized on the way (dg_quantize_fp8 with 1 x 128 blocks): the
+ * operand of dg_gemm_fp8_grouped without a 16-bit copy in between. */
+dg_status dg_moe_dispatch_fp8(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
+                              const void *X, int64_t ldx, int64_t rows, const int32_t *row_slot,
+                              void *codes, int64_t ldq, float *scales, int64_t lds,
+                              dg_stream_t stream);
+
+/* The way back: D[t,:] = sum over j of weights[t,j] * Y[slot_row[t,j],:] in
+ * FP32, in the order of j, rounded once; dropped slots (and rows outside [0,
+ * rows)) add nothing, so a token without any gets zeros.  weights: tokens x
+ * top_k FP32, or NULL for ones.  Y, D: FP16 or BF16 as in dg_moe_dispatch. */
+dg_status dg_moe_combine(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
+                         const void *Y, int64_t ldy, int64_t rows, const int32_t *slot_row,
+                         const float *weights, void *D, int64_t ldd, dg_stream_t stream);
+
+/* Its gradient, from dD (tokens x width):
+ *   dY[r,:] = weights[s] * dD[s / top_k,:] for r = slot_row[s], zeros for the
+ *             rows whose row_slot is -1;
+ *   dweights[s] = sum over the columns of dD[s / top_k,:] * Y[r,:] (FP32; 0
+ *             for a dropped slot).
+ * row_slot and slot_row come from one dg_moe_sort.  weights may be NULL for
+ * ones, dweights (then Y too) NULL when not wanted. */
+dg_status dg_moe_combine_backward(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
+                                  const void *dD, int64_t lddd, const void *Y, int64_t ldy,
+                                  int64_t rows, const int32_t *row_slot, const int32_t *slot_row,
+                                  const float *weights, void *dY, int64_t lddy, float *dweights,
+                                  dg_stream_t stream);
 
 /* Message for the last failing call on this thread ("" if none).  Valid
  * until the next libdg call on the same thread. */

@@ -16,11 +16,13 @@ __all__ = [
     "gemm_strided_batched_raw", "prepare_grouped", "OPS", "MAX_EPILOGUE_OPS", "MXF4", "quantize_mxf4",
     "quantize_mxf4_raw", "gemm_mxf4", "gemm_mxf4_raw",
     "EpilogueOp", "EpilogueProgram", "make_program",
+    "quantize_fp8", "gemm_fp8", "gemm_fp8_grouped", "gemm_fp8_grouped_wgrad", "moe_rows",
+    "moe_sort", "moe_dispatch", "moe_dispatch_fp8", "moe_combine", "moe_combine_backward",
     "plan_tiles", "query_hw", "last_error", "check_status", "set_wait_timeout_ns",
     "selftest_wait_timeout", "launch_count", "shutdown", "HwDesc", "TilePlan", "EXPORTS",
 ]
 
-F16, I8, E2M1, MXF4 = 0, 1, 2, 3
+F16, I8, E2M1, MXF4, BF16, F32 = 0, 1, 2, 3, 4, 5
 DTYPES = {"f16": F16, "i8": I8, "e2m1": E2M1, "mxf4": MXF4}
 EPILOGUES = {"none": 0, "bias": 1, "gelu": 2, "bias_gelu": 3}
 OPS = {"bias": 1, "relu": 2, "gelu": 3, "scale": 4, "clamp": 5, "quant_i8": 6}
@@ -35,6 +37,9 @@ KERNELS = {0: "tc", 1: "gemv", 2: "tc_widened", 3: "skinny", 4: "gemv_mma", 5: "
 EXPORTS = ["dg_query_hw", "dg_plan_tiles", "dg_gemm", "dg_gemm_planned", "dg_gemm_host",
            "dg_gemm_ex", "dg_gemm_strided_batched", "dg_gemm_grouped",
            "dg_quantize_mxf4", "dg_gemm_mxf4", "dg_gemm_mxf4_planned",
+           "dg_quantize_fp8", "dg_gemm_fp8", "dg_gemm_fp8_grouped", "dg_gemm_fp8_grouped_wgrad",
+           "dg_moe_rows", "dg_moe_sort", "dg_moe_dispatch", "dg_moe_dispatch_fp8",
+           "dg_moe_combine", "dg_moe_combine_backward",
            "dg_gemm_thin_noalloc", "dg_last_error",
            "dg_check_status", "dg_set_wait_timeout_ns", "dg_selftest_wait_timeout",
            "dg_launch_count", "dg_shutdown"]
@@ -141,6 +146,22 @@ def lib():
                                f32, i32, vp]
     L.dg_gemm_mxf4_planned.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
                                        f32, f32, i32, ctypes.POINTER(TilePlan), vp]
+    L.dg_quantize_fp8.argtypes = [i64, i64, i32, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64,
+                                  vp]
+    L.dg_gemm_fp8.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i32, i64,
+                              vp, f32, f32, i32, vp]
+    L.dg_gemm_fp8_grouped.argtypes = [i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64,
+                                      i64, vp, vp, i32, i64, vp, i64, f32, f32, i32, vp]
+    L.dg_gemm_fp8_grouped_wgrad.argtypes = [i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                            vp, vp, i32, i64, i64, f32, f32, vp]
+    L.dg_moe_rows.argtypes = [i64, i64, i64, i64]
+    L.dg_moe_rows.restype = ctypes.c_int64
+    L.dg_moe_sort.argtypes = [i64, i64, i64, vp, i64, i64, vp, vp, vp, vp]
+    L.dg_moe_dispatch.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp]
+    L.dg_moe_dispatch_fp8.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, i64, vp]
+    L.dg_moe_combine.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, vp]
+    L.dg_moe_combine_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, vp, vp,
+                                          vp, i64, vp, vp]
     L.dg_last_error.restype = ctypes.c_char_p
     L.dg_last_error.argtypes = []
     L.dg_check_status.argtypes = [vp]
@@ -152,6 +173,9 @@ def lib():
     for name in ("dg_query_hw", "dg_plan_tiles", "dg_gemm", "dg_gemm_planned",
                  "dg_gemm_thin_noalloc", "dg_gemm_host", "dg_gemm_ex", "dg_gemm_strided_batched",
                  "dg_gemm_grouped", "dg_quantize_mxf4", "dg_gemm_mxf4", "dg_gemm_mxf4_planned",
+                 "dg_quantize_fp8", "dg_gemm_fp8", "dg_gemm_fp8_grouped",
+                 "dg_gemm_fp8_grouped_wgrad", "dg_moe_sort", "dg_moe_dispatch",
+                 "dg_moe_dispatch_fp8", "dg_moe_combine", "dg_moe_combine_backward",
                  "dg_check_status",
                  "dg_set_wait_timeout_ns", "dg_selftest_wait_timeout", "dg_shutdown"):
         getattr(L, name).restype = ctypes.c_int
@@ -573,6 +597,312 @@ def gemm_host(A, B, D, C=None, K=None, bias=None, alpha=1.0, beta=0.0, epilogue=
     gemm_host_raw(M, N, K, dtype_a, dtype_b, A, A.stride(0), B, ldb, C, D, bias, alpha, beta,
                   epilogue, stream=stream)
     return D
+
+
+# ------------------------------------------------- FP8 and expert routing
+
+_FP = None  # (torch, {16-bit and 32-bit float dtype: code}), built on first use
+
+
+def _fp():
+    global _FP
+    if _FP is None:
+        import torch
+        _FP = (torch, {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+    return _FP
+
+
+def _float_code(t, what, kinds=(F16, BF16)):
+    code = (_FP or _fp())[1].get(t.dtype, -1)
+    if code not in kinds:
+        raise TypeError("%s must be float16%s, got %s" % (
+            what, ", bfloat16 or float32" if F32 in kinds else " or bfloat16", t.dtype))
+    return code
+
+
+def _rows(t, dtype, what, shape=None, dim=2):
+    """Checks a tensor's type, dimensions, unit last stride and (where given) shape."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    s = t.stride()
+    if len(s) != dim or (s[-1] != 1 and t.shape[-1] > 1 and t.numel()):
+        raise ValueError("%s must be %d-D with unit last stride" % (what, dim))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU" % what)
+    return s
+
+
+def _fp8_operand(torch, codes, scales, what, dim=2):
+    s = _rows(codes, torch.float8_e4m3fn, what, None, dim)
+    z = _rows(scales, torch.float32, "the scales of " + what, None, dim)
+    return s, z
+
+
+def quantize_fp8(X, form="rows", block_rows=1, out=None, stream=None):
+    """E4M3 block quantization of X [rows, K] (float16 or bfloat16).
+
+    form "rows": (codes [rows, K] float8_e4m3fn, scales [ceil(rows /
+    block_rows), ceil(K / 128)] float32), blocks along K; "transposed": the
+    same of X's transpose (codes_t [K, rows], blocks along the rows of X);
+    "both": (codes, scales, codes_t, scales_t) from one read of X.
+    block_rows: 1 (activations) or 128 (weights).  out: such a tuple to write
+    into; codes rows start on 16-byte boundaries.
+    """
+    torch = (_FP or _fp())[0]
+    code = _float_code(X, "X")
+    sx = _rows(X, X.dtype, "X")
+    rows, K = X.shape
+    if form not in ("rows", "transposed", "both"):
+        raise ValueError("form must be rows, transposed or both")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    shapes = [(rows, K)] * (form != "transposed") + [(K, rows)] * (form != "rows")
+    if out is None:
+        out = ()
+        for r, c in shapes:
+            room = torch.empty((r, (c + 15) // 16 * 16), dtype=torch.float8_e4m3fn,
+                               device=X.device)
+            out += (room[:, :c], torch.empty((-(-r // block_rows), -(-c // 128)),
+                                             dtype=torch.float32, device=X.device))
+    if len(out) != 2 * len(shapes):
+        raise ValueError("form %r has %d outputs" % (form, 2 * len(shapes)))
+    args = []
+    for i, (r, c) in enumerate(shapes):
+        sq = _rows(out[2 * i], torch.float8_e4m3fn, "out[%d]" % (2 * i), (r, c))
+        ss = _rows(out[2 * i + 1], torch.float32, "out[%d]" % (2 * i + 1),
+                   (-(-r // block_rows), -(-c // 128)))
+        args += [out[2 * i].data_ptr(), sq[0], out[2 * i + 1].data_ptr(), ss[0]]
+    none = [None, 0, None, 0]
+    if form == "rows":
+        args += none
+    elif form == "transposed":
+        args = none + args
+    _check(lib().dg_quantize_fp8(rows, K, code, X.data_ptr(), sx[0], block_rows, *args,
+                                 _stream_handle(stream)))
+    return out
+
+
+def gemm_fp8(A, scale_a, B, scale_b, D, bias=None, alpha=1.0, beta=0.0, epilogue="none",
+             stream=None):
+    """D = epilogue(alpha * A.B^T + beta * D) for FP8 operands, written into D.
+
+    A: float8_e4m3fn [M, K] with scale_a float32 [M, ceil(K / 128)]; B: [N, K]
+    with scale_b [N, ...] or [ceil(N / 128), ...] (128 x 128 blocks); D: [M, N]
+    float16, bfloat16 or float32; bias: [N] of D's type.
+    """
+    torch, codes = _FP or _fp()
+    sa, za = _fp8_operand(torch, A, scale_a, "A")
+    sb, zb = _fp8_operand(torch, B, scale_b, "B")
+    dt = _float_code(D, "D", (F16, BF16, F32))
+    sd = _rows(D, D.dtype, "D")
+    M, N = D.shape
+    K = A.shape[1]
+    nb = scale_b.shape[0]
+    kb = (K + 127) // 128
+    if A.shape[0] != M or B.shape[0] != N or B.shape[1] != K or scale_a.shape[0] != M or \
+            scale_a.shape[1] < kb or scale_b.shape[1] < kb or nb not in (N, (N + 127) // 128):
+        raise ValueError("shape mismatch: A %s with %s, B %s with %s, D %s" % tuple(
+            tuple(t.shape) for t in (A, scale_a, B, scale_b, D)))
+    if bias is not None and (bias.dtype is not D.dtype or bias.shape != (N,) or
+                             (N > 1 and bias.stride(0) != 1)):
+        raise ValueError("bias must be [N] of D's type")
+    _check(lib().dg_gemm_fp8(
+        M, N, K, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[0],
+        scale_b.data_ptr(), zb[0], 1 if nb == N else 128, D.data_ptr(), dt, sd[0],
+        None if bias is None else bias.data_ptr(), alpha, beta, _epi_code(epilogue),
+        _stream_handle(stream)))
+    return D
+
+
+def gemm_fp8_grouped(A, scale_a, B, scale_b, offsets, D, bias=None, alpha=1.0, beta=0.0,
+                     epilogue="none", stream=None):
+    """D[i] = epilogue(alpha * A[i].B[e]^T + beta * D[i]) for the rows i of each
+    expert e, offsets[e] <= i < offsets[e + 1] (int32 [count + 1] on the device).
+
+    A: float8_e4m3fn [rows, K] with scale_a [rows, ceil(K / 128)]; B: [count, N,
+    K] with scale_b [count, ceil(N / 128), ceil(K / 128)]; D: [rows, N]; bias:
+    [count, N] of D's type.
+    """
+    torch, codes = _FP or _fp()
+    sa, za = _fp8_operand(torch, A, scale_a, "A")
+    sb, zb = _fp8_operand(torch, B, scale_b, "B", 3)
+    dt = _float_code(D, "D", (F16, BF16, F32))
+    sd = _rows(D, D.dtype, "D")
+    rows, N = D.shape
+    count, K = B.shape[0], A.shape[1]
+    kb = (K + 127) // 128
+    if A.shape[0] != rows or B.shape[1] != N or B.shape[2] != K or scale_a.shape[0] != rows or \
+            scale_a.shape[1] < kb or scale_b.shape[0] != count or \
+            scale_b.shape[1] != (N + 127) // 128 or scale_b.shape[2] < kb:
+        raise ValueError("shape mismatch: A %s with %s, B %s with %s, D %s" % tuple(
+            tuple(t.shape) for t in (A, scale_a, B, scale_b, D)))
+    _rows(offsets, torch.int32, "offsets", (count + 1,), 1)
+    stride_bias = 0
+    if bias is not None:
+        stride_bias = _rows(bias, D.dtype, "bias", (count, N))[0]
+    _check(lib().dg_gemm_fp8_grouped(
+        count, rows, N, K, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[1],
+        sb[0], scale_b.data_ptr(), zb[1], zb[0], offsets.data_ptr(), D.data_ptr(), dt, sd[0],
+        None if bias is None else bias.data_ptr(), stride_bias, alpha, beta, _epi_code(epilogue),
+        _stream_handle(stream)))
+    return D
+
+
+def gemm_fp8_grouped_wgrad(A, scale_a, B, scale_b, offsets, D, alpha=1.0, beta=0.0, stream=None):
+    """D[e] = alpha * A[:, e's rows].B[:, e's rows]^T + beta * D[e].
+
+    A: float8_e4m3fn [M, rows] with scale_a [M, ceil(rows / 128)]; B: [N, rows]
+    likewise (both the transposed form of quantize_fp8); offsets: int32 [count
+    + 1] on the device, multiples of 128; D: [count, M, N].
+    """
+    torch, codes = _FP or _fp()
+    sa, za = _fp8_operand(torch, A, scale_a, "A")
+    sb, zb = _fp8_operand(torch, B, scale_b, "B")
+    dt = _float_code(D, "D", (F16, BF16, F32))
+    sd = _rows(D, D.dtype, "D", None, 3)
+    count, M, N = D.shape
+    rows = A.shape[1]
+    kb = (rows + 127) // 128
+    if A.shape[0] != M or B.shape[0] != N or B.shape[1] != rows or scale_a.shape[0] != M or \
+            scale_b.shape[0] != N or scale_a.shape[1] < kb or scale_b.shape[1] < kb:
+        raise ValueError("shape mismatch: A %s with %s, B %s with %s, D %s" % tuple(
+            tuple(t.shape) for t in (A, scale_a, B, scale_b, D)))
+    _rows(offsets, torch.int32, "offsets", (count + 1,), 1)
+    _check(lib().dg_gemm_fp8_grouped_wgrad(
+        count, M, N, rows, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[0],
+        scale_b.data_ptr(), zb[0], offsets.data_ptr(), D.data_ptr(), dt, sd[1], sd[0], alpha, beta,
+        _stream_handle(stream)))
+    return D
+
+
+def moe_rows(tokens, top_k, count, align=1):
+    """The rows that moe_sort needs room for (dg_moe_rows)."""
+    n = lib().dg_moe_rows(int(tokens), int(top_k), int(count), int(align))
+    if n < 0:
+        raise ValueError("moe_rows: tokens %s, top_k %s, count %s, align %s" % (
+            tokens, top_k, count, align))
+    return n
+
+
+def moe_sort(ids, count, align=1, out=None, stream=None):
+    """Sorts the tokens' choices ids [tokens, top_k] (int32; outside [0, count):
+    dropped) by expert.  Returns (offsets [count + 1], row_slot [rows], slot_row
+    [tokens, top_k]), int32: each expert's rows, the slot t * top_k + j that a
+    row holds (-1: none) and the row of each slot (-1: dropped).  Segments
+    start at multiples of align.  out: such a tuple to write into.
+    """
+    torch = (_FP or _fp())[0]
+    _rows(ids, torch.int32, "ids")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    tokens, top_k = ids.shape
+    if out is None:
+        def room(*shape):
+            return torch.empty(shape, dtype=torch.int32, device=ids.device)
+        out = (room(count + 1), room(moe_rows(tokens, top_k, count, align)), room(tokens, top_k))
+    offsets, row_slot, slot_row = out
+    for t, what in ((offsets, "offsets"), (row_slot, "row_slot")):
+        _rows(t, torch.int32, what, None, 1)
+    _rows(slot_row, torch.int32, "slot_row", ids.shape)
+    if offsets.shape[0] != count + 1 or not slot_row.is_contiguous():
+        raise ValueError("offsets must be [count + 1], slot_row contiguous like ids")
+    _check(lib().dg_moe_sort(tokens, top_k, count, ids.data_ptr(), align, row_slot.shape[0],
+                             offsets.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
+                             _stream_handle(stream)))
+    return out
+
+
+def moe_dispatch(X, row_slot, top_k, D, stream=None):
+    """D[r] = X[row_slot[r] // top_k], zeros where row_slot[r] is -1.  X: [tokens,
+    width] float16 or bfloat16, D: [rows, width] of its type.  The gradient is
+    moe_combine without weights."""
+    torch = (_FP or _fp())[0]
+    code = _float_code(X, "X")
+    sx = _rows(X, X.dtype, "X")
+    rows = row_slot.shape[0]
+    tokens, width = X.shape
+    _rows(row_slot, torch.int32, "row_slot", None, 1)
+    sd = _rows(D, X.dtype, "D", (rows, width))
+    _check(lib().dg_moe_dispatch(tokens, top_k, width, code, X.data_ptr(), sx[0], rows,
+                                 row_slot.data_ptr(), D.data_ptr(), sd[0],
+                                 _stream_handle(stream)))
+    return D
+
+
+def moe_dispatch_fp8(X, row_slot, top_k, codes, scales, stream=None):
+    """moe_dispatch and quantize_fp8 in one: codes float8_e4m3fn [rows, width],
+    scales float32 [rows, ceil(width / 128)]."""
+    torch = (_FP or _fp())[0]
+    code = _float_code(X, "X")
+    sx = _rows(X, X.dtype, "X")
+    rows = row_slot.shape[0]
+    tokens, width = X.shape
+    _rows(row_slot, torch.int32, "row_slot", None, 1)
+    sq = _rows(codes, torch.float8_e4m3fn, "codes", (rows, width))
+    ss = _rows(scales, torch.float32, "scales", (rows, (width + 127) // 128))
+    _check(lib().dg_moe_dispatch_fp8(tokens, top_k, width, code, X.data_ptr(), sx[0], rows,
+                                     row_slot.data_ptr(), codes.data_ptr(), sq[0],
+                                     scales.data_ptr(), ss[0], _stream_handle(stream)))
+    return codes, scales
+
+
+def moe_combine(Y, slot_row, D, weights=None, stream=None):
+    """D[t] = sum over j of weights[t, j] * Y[slot_row[t, j]] (dropped slots add
+    nothing).  Y: [rows, width] float16 or bfloat16, D: [tokens, width] of its
+    type, weights: float32 [tokens, top_k] or None for ones."""
+    torch = (_FP or _fp())[0]
+    code = _float_code(Y, "Y")
+    sy = _rows(Y, Y.dtype, "Y")
+    _rows(slot_row, torch.int32, "slot_row")
+    tokens, top_k = slot_row.shape
+    width = Y.shape[1]
+    sd = _rows(D, Y.dtype, "D", (tokens, width))
+    if weights is not None:
+        _rows(weights, torch.float32, "weights", slot_row.shape)
+    if not slot_row.is_contiguous() or not (weights is None or weights.is_contiguous()):
+        raise ValueError("slot_row and weights must be contiguous")
+    _check(lib().dg_moe_combine(tokens, top_k, width, code, Y.data_ptr(), sy[0], Y.shape[0],
+                                slot_row.data_ptr(),
+                                None if weights is None else weights.data_ptr(), D.data_ptr(),
+                                sd[0], _stream_handle(stream)))
+    return D
+
+
+def moe_combine_backward(dD, Y, slot_row, row_slot, weights, dY, dweights=None, stream=None):
+    """The gradient of moe_combine: dY[r] = weights[s] * dD[s // top_k] for the
+    slot s of row r (zeros without one), dweights[s] = dD[s // top_k] . Y[r].
+    weights may be None for ones; without dweights Y may be None.  Returns
+    (dY, dweights)."""
+    torch = (_FP or _fp())[0]
+    code = _float_code(dD, "dD")
+    s_dd = _rows(dD, dD.dtype, "dD")
+    _rows(slot_row, torch.int32, "slot_row")
+    _rows(row_slot, torch.int32, "row_slot", None, 1)
+    tokens, top_k = slot_row.shape
+    width, rows = dD.shape[1], row_slot.shape[0]
+    if dD.shape[0] != tokens:
+        raise ValueError("dD must be [tokens, width]")
+    s_dy = _rows(dY, dD.dtype, "dY", (rows, width))
+    s_y = (0,)
+    if dweights is not None:
+        if Y is None:
+            raise ValueError("dweights needs Y")
+        s_y = _rows(Y, dD.dtype, "Y", (rows, width))
+    for t, what in ((weights, "weights"), (dweights, "dweights")):
+        if t is not None:
+            _rows(t, torch.float32, what, slot_row.shape)
+            if not t.is_contiguous():
+                raise ValueError("%s must be contiguous" % what)
+    if not slot_row.is_contiguous():
+        raise ValueError("slot_row must be contiguous")
+    _check(lib().dg_moe_combine_backward(
+        tokens, top_k, width, code, dD.data_ptr(), s_dd[0],
+        None if dweights is None else Y.data_ptr(), s_y[0], rows, row_slot.data_ptr(),
+        slot_row.data_ptr(), None if weights is None else weights.data_ptr(), dY.data_ptr(),
+        s_dy[0], None if dweights is None else dweights.data_ptr(), _stream_handle(stream)))
+    return dY, dweights
 
 
 def query_hw(device=0):

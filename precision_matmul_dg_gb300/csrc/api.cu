@@ -148,6 +148,8 @@ int elem_bits(dg_dtype t) {
     case DG_I8: return 8;
     case DG_E2M1: return 4;
     case DG_MXF4: return 4;  // codes; the scales are a separate array
+    case DG_BF16: return 16;
+    case DG_F32: return 32;
   }
   return 0;
 }
@@ -752,6 +754,27 @@ void count_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
 void clear_error() { g_last_error[0] = '\0'; }
 
 dg_status set_error(dg_status s, const char* msg) { return fail(s, "%s", msg); }
+
+dg_status set_errorf(dg_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+  va_end(ap);
+  return s;
+}
+
+dg_status set_cuda_error(cudaError_t e, const char* what) { return fail_cuda(e, what); }
+
+dg_status call_context(CallContext* out) {
+  DeviceState* st = nullptr;
+  const dg_status s = device_state(&st);
+  if (s != DG_OK) return s;
+  cudaGetDevice(&out->dev);
+  out->status = st->status;
+  out->timeout_ns = timeout_ns();
+  out->sm_count = st->hw.sm_count;
+  return DG_OK;
+}
 
 // Host-buffer GEMM (dg_gemm_host in dg.h).
 dg_status run_host(int64_t M, int64_t N, int64_t K, dg_dtype da, dg_dtype db, const void* A,

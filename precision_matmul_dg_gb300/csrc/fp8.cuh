@@ -1,0 +1,87 @@
+// Pieces shared by the FP8 (E4M3 with block scales) and expert-routing
+// kernels: 16-bit loads as FP32, block scales, conversions and stores.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace dg {
+namespace fp8 {
+
+constexpr int kBlock = 128;              // values per scale along K
+constexpr float kTop = 448.0f;           // largest finite E4M3 value
+constexpr float kFloor = 448.0f * 0x1p-126f;  // a block's amax is taken as at least this
+
+// The two 16-bit floating types behind one interface.
+struct F16 {
+  static constexpr uint32_t kInf = 0x7C00u;  // magnitudes from here on are infinite or NaN
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float one(uint32_t h) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+  }
+};
+struct BF16 {
+  static constexpr uint32_t kInf = 0x7F80u;
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float one(uint32_t h) { return __uint_as_float(h << 16); }
+};
+
+// Four FP32 values -> four E4M3 codes (v0 in the low byte), nearest, ties to
+// even, saturated to the largest finite value.
+__device__ __forceinline__ uint32_t e4m3x4(float v0, float v1, float v2, float v3) {
+  uint32_t out;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(out)
+      : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
+  return out;
+}
+
+// What quantizes a block: its scale and the factor that its values take.  A
+// block with an infinity or a NaN has the scale NaN and codes 0.
+struct BlockScale {
+  float scale, factor;
+  bool bad;
+};
+template <typename T>
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
+  BlockScale b;
+  b.bad = amax_bits >= T::kInf;
+  const float amax = fmaxf(T::one(b.bad ? 0u : amax_bits), kFloor);
+  b.factor = __fdiv_rn(kTop, amax);
+  b.scale = b.bad ? CUDART_NAN_F : __fdiv_rn(amax, kTop);
+  return b;
+}
+
+// Eight 16-bit values (four words) -> eight codes.
+template <typename T>
+__device__ __forceinline__ uint2 quantize8(const uint32_t (&w)[4], const BlockScale& b) {
+  if (b.bad) return make_uint2(0u, 0u);
+  const float2 x0 = T::unpack(w[0]), x1 = T::unpack(w[1]), x2 = T::unpack(w[2]),
+               x3 = T::unpack(w[3]);
+  const float f = b.factor;
+  return make_uint2(e4m3x4(x0.x * f, x0.y * f, x1.x * f, x1.y * f),
+                    e4m3x4(x2.x * f, x2.y * f, x3.x * f, x3.y * f));
+}
+
+}  // namespace fp8
+}  // namespace dg

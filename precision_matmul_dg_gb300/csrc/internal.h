@@ -236,6 +236,97 @@ struct MxWidenJob {
 };
 cudaError_t launch_widen_mxf4(const MxWidenJob* jobs, int njobs, int64_t K, cudaStream_t stream,
                               int sm_count);
+// FP8 (fp8_quant.cu): E4M3 block quantization of FP16 / BF16 rows.  Row form
+// with 1 x 128 blocks, of X's rows or (row_slot) of rows gathered by expert;
+// tile form: row and / or transposed codes, with 1 x 128 blocks or (whole)
+// one block per 128 x 128 tile.
+struct Fp8RowsJob {
+  bool bf16;
+  const void* X;
+  int64_t ldx, rows, K;
+  void* codes;
+  int64_t ldq;
+  float* scales;
+  int64_t lds;
+  const int32_t* row_slot = nullptr;
+  int64_t top_k = 1, tokens = 0;
+};
+cudaError_t launch_quantize_fp8_rows(const Fp8RowsJob& j, cudaStream_t stream, int sm_count);
+struct Fp8TilesJob {
+  bool bf16;
+  const void* X;
+  int64_t ldx, rows, K;
+  bool whole;
+  void* codes;  // or NULL
+  int64_t ldq;
+  float* scales;
+  int64_t lds;
+  void* codes_t;  // or NULL
+  int64_t ldqt;
+  float* scales_t;
+  int64_t ldst;
+};
+cudaError_t launch_quantize_fp8_tiles(const Fp8TilesJob& j, cudaStream_t stream);
+
+// FP8 products.  Fp8Args: one dense product, a grouped one (offsets: rows of
+// A by expert) or grouped weight gradients (offsets: K by expert).
+enum class Fp8Mode : int { kDense = 0, kRows = 1, kK = 2 };
+struct Fp8Args {
+  Fp8Mode mode;
+  int64_t M, N, K;  // kRows: M rows in all; kK: K rows of the sorted batch in all
+  const void* A;
+  int64_t lda;
+  const float* sa;
+  int64_t lds_a;
+  const void* B;
+  int64_t ldb, stride_b;
+  const float* sb;
+  int64_t lds_b, stride_sb;
+  int block_rows_b;
+  int64_t count;
+  const int32_t* offsets;
+  void* D;
+  dg_dtype dtype_d;
+  int64_t ldd, stride_d;
+  const void* bias;
+  int64_t stride_bias;
+  float alpha, beta;
+  int epi;  // kEpiBias | kEpiGelu
+  cudaStream_t stream;
+  int* status;
+  uint64_t timeout_ns;
+  int sm_count;
+};
+cudaError_t launch_fp8_tc(const Fp8Args& a);      // fp8_gemm.cu: tcgen05
+cudaError_t launch_fp8_skinny(const Fp8Args& a);  // fp8_skinny.cu: few rows (dense or kRows)
+constexpr int64_t kFp8SkinnyRows = 16;
+constexpr int64_t kMaxExperts = 1024;
+
+// Expert routing (moe.cu).
+struct MoeSortJob {
+  int64_t tokens, top_k, count;
+  const int32_t* ids;
+  int64_t align, rows;
+  int32_t *offsets, *row_slot, *slot_row;
+};
+cudaError_t launch_moe_sort(const MoeSortJob& j, cudaStream_t stream);
+struct MoeRowsJob {
+  bool bf16;
+  int64_t tokens, top_k, width;
+  int64_t rows;  // of the sorted side
+  const void* X;
+  int64_t ldx;
+  const void* Y;
+  int64_t ldy;
+  const int32_t *row_slot, *slot_row;
+  const float* weights;
+  void* D;
+  int64_t ldd;
+  float* dweights;
+};
+cudaError_t launch_moe_dispatch(const MoeRowsJob& j, cudaStream_t stream, int sm_count);
+cudaError_t launch_moe_combine(const MoeRowsJob& j, cudaStream_t stream);
+cudaError_t launch_moe_combine_backward(const MoeRowsJob& j, cudaStream_t stream);
 cudaError_t launch_wait_selftest(cudaStream_t stream, int* status, uint64_t timeout_ns);
 
 // Whether the split-K GEMV reduces `split` splits inside a thread-block
@@ -245,10 +336,22 @@ bool gemv_split_in_cluster(int split);
 int64_t gemv_partial_elems(const dg_tile_plan& plan, int64_t M, int64_t N, int64_t batch);
 int64_t gemv_counter_elems(const dg_tile_plan& plan, int64_t N, int64_t batch);
 
+// What a launcher outside api.cu needs of the current device: its status word,
+// the wait limit in force and its SM count.
+struct CallContext {
+  int dev;
+  int* status;
+  uint64_t timeout_ns;
+  int sm_count;
+};
+dg_status call_context(CallContext* out);
+
 // Kernel-launch counter and error state (api.cu).  None of these allocate.
 void count_launches(int n);
 void clear_error();
 dg_status set_error(dg_status s, const char* msg);
+dg_status set_errorf(dg_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+dg_status set_cuda_error(cudaError_t e, const char* what);
 dg_status fill_hw_desc(int device, dg_hw_desc* out);
 dg_status validate_gemm_args(int64_t M, int64_t N, int64_t K, dg_dtype da, dg_dtype db,
                              const void* A, int64_t lda, const void* B, int64_t ldb, void* C,
