@@ -495,7 +495,7 @@ dg_status dg_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
  *   stride_b is a multiple of ldb and at least N * ldb.  Rows outside every
  *   segment are neither read nor written.  Offsets are taken as clamped to
  *   [0, rows]; an end before its start is an empty segment.
- *   count is at most 1024.  Other rules as dg_gemm_fp8. */
+ *   count is at most 512.  Other rules as dg_gemm_fp8. */
 dg_status dg_gemm_fp8_grouped(int64_t count, int64_t rows, int64_t N, int64_t K, const void *A,
                               int64_t lda, const float *scale_a, int64_t lds_a, const void *B,
                               int64_t ldb, int64_t stride_b, const float *scale_b, int64_t lds_b,

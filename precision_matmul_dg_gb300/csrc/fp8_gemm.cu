@@ -7,8 +7,8 @@
 //
 // The tensor core adds within a block; scales change from block to block, so
 // each block's P_b (one pipeline stage: 128 bytes of K) lands in a tensor
-// memory buffer of its own and the epilogue warps add s * P_b to sums that
-// stay in registers:
+// memory buffer of its own and the sum warps add s * P_b to sums that stay in
+// registers:
 //
 //   warps 0-7   sums and epilogue: warps w and w + 4 own TMEM lanes
 //               32 * (w % 4) .. +31 (rows of D) and one half of the columns
@@ -16,24 +16,34 @@
 //               columns with s = sa[i,b] * sb[b] (128 x 128 weight blocks: one
 //               factor for the thread's row and half), or a multiplication by
 //               the column's scale first (1 x 128 blocks in B);
-//   warp 8      TMA producer of a ring of stages (A: 128 rows, B: BN rows, 128
-//               bytes each, 128-byte swizzle);
+//   warp 8      TMA producer of a ring of stages (128 rows of A, BN rows of B,
+//               128 bytes each, 128-byte swizzle);
 //   warp 9      tensor memory allocation; MMA issuer, 4 x tcgen05.mma
-//               (kind::f8f6f4, K = 32) per stage.
-//
+//               (kind::f8f6f4, K = 32) per stage;
 //   warp 10     with 1 x 128 blocks in B: brings the columns' scales of four K
 //               blocks at a time to shared memory, two such groups ahead;
 //   warp 11     nothing: it completes the third warpgroup.
 //
-// A sum thread holds 128 sums beside a 32-column load, more than the 168
-// registers that 384 threads can have each: the third warpgroup keeps 72 and
-// the two of the sum warps take 216 (2 x 216 + 72 = 3 x 168).
+// CG = 2: a cluster of two CTAs computes a tile of 256 rows with cta_group::2
+// MMAs, each CTA holding 128 rows of A and half of B's rows: 32 KB instead of
+// 48 KB come in per 128 x 256 x 128 block.  (A CTA alone is held by those
+// copies: at 1/4 of the MMAs and 1/4 of the TMEM loads it still took 660 clocks
+// per block, 72 bytes per clock and SM, where the MMAs take 512.)
 //
-// The kernel is persistent: CTA u takes tiles u, u + grid, ...  Experts'
-// segments are read from the device's offsets: every CTA counts the segments'
-// 128-row blocks into shared memory, and every role walks the same tile list.
-// A row tile may run into the next expert's rows (they are loaded, never
-// stored).  Weight gradients walk (expert, tile) with K = the segment.
+// A sum thread holds up to 128 sums beside two 32-column loads, more than the
+// 168 registers that 384 threads can have each: the third warpgroup keeps 72
+// and the two of the sum warps take 216 (2 x 216 + 72 = 3 x 168).
+//
+// The kernel is persistent: unit u (CTA or pair) takes tiles u, u + units, ...
+// Experts' segments are read from the device's offsets: every CTA counts the
+// segments' row blocks into shared memory, and every role walks the same tile
+// list.  A row tile may run into the next expert's rows (they are loaded,
+// never stored).  Weight gradients walk (expert, tile) with K = the segment.
+//
+// D leaves through shared memory: a warp's 32 rows x 64 bytes at a time, by
+// TMA, or (a segment's last rows, layouts that TMA does not take) by the warp
+// in runs of whole rows.  Straight from registers a store touches 32 rows, one
+// line each: 5500 clocks per 128 x 256 tile.
 #include <algorithm>
 
 #include "epilogue.cuh"
@@ -48,10 +58,13 @@ using namespace fp8;
 constexpr int kTcThreads = 384;
 constexpr int kLaunchRegs = 168, kSumRegs = 216, kOtherRegs = 72;  // per thread
 static_assert(2 * kSumRegs + kOtherRegs == 3 * kLaunchRegs, "shares of the launch's registers");
-constexpr int kColGroup = 4;  // K blocks whose column scales are staged together
+constexpr int kScaleGroup = 4;  // K blocks (of one number / 4) whose scales are staged together
 constexpr int kSumWarps = 8;
-constexpr int kRowsPerTile = 128;  // TMEM lanes
-constexpr int kStageA = kRowsPerTile * 128;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10;
+constexpr int kRowsPerCta = 128;  // TMEM lanes
+constexpr int kStageA = kRowsPerCta * 128;
+constexpr int kRowScaleBytes = kRowsPerCta * kScaleGroup * 4;
+constexpr int kBoxBytes = 32 * 64;  // 32 rows of 64 bytes, 64-byte swizzle
 
 struct F8Params {
   int M, N;  // kRows: M rows in all
@@ -69,7 +82,9 @@ struct F8Params {
   const void* bias;
   int64_t stride_bias;
   float alpha, beta;
-  int flags, dtype_d, vec;  // vec: bytes per store that D's layout allows (32, 16 or 0)
+  int flags, dtype_d;
+  int tma_d, vec_d;  // D's layout: TMA can store it; rows are 16-byte aligned
+  int vec_a, vec_b;  // rows of scales are too
   uint32_t stage_tx;
   int k_rows;  // kK: rows of the sorted batch
   int* status;
@@ -81,19 +96,26 @@ struct F8Smem {
   static constexpr int kTileB = BN * 128;
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + Stages * kStageA;
-  static constexpr int kOffCol = kOffB + Stages * kTileB;  // column scales: [2][4][BN]
-  static constexpr int kOffBar = kOffCol + (ColScale ? 2 * kColGroup * BN * 4 : 0);
-  static constexpr int kBufs = 512 / BN < 4 ? 512 / BN : 4;
+  static constexpr int kOffBox = kOffB + Stages * kTileB;
+  static constexpr int kOffRow = kOffBox + kSumWarps * kBoxBytes;  // row scales [2][128][4]
+  static constexpr int kOffCol = kOffRow + 2 * kRowScaleBytes;
+  // column scales [2][4][BN]
+  static constexpr int kOffBar = kOffCol + (ColScale ? 2 * kScaleGroup * BN * 4 : 0);
+  static constexpr int kBufs = 512 / BN;
   static constexpr int kBars = 2 * Stages + 2 * kBufs + 1 + 4;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffAbort = kOffSlot + 4;
   static constexpr int kOffGroups = (kOffAbort + 4 + 15) / 16 * 16;
   static constexpr int kFixed = kOffGroups + 1024;  // base alignment
-  // row offsets and block counts of the experts, count + 1 each
-  static int bytes(int64_t count) { return kFixed + static_cast<int>(2 * (count + 1) * 4); }
+  // count + 1 row offsets of the experts, and without column scales (kRows) as
+  // many row block counts
+  static constexpr int bytes(int64_t count) {
+    return kFixed + static_cast<int>(count > 0 ? (ColScale ? 1 : 2) * (count + 1) * 4 : 0);
+  }
+  static_assert(bytes(kMaxFp8Experts) <= 227 * 1024, "shared memory of a CTA");
 };
 
-// One tile: rows row0 .. row0 + rows - 1 of A and D, columns from n0, K blocks
+// A tile: rows row0 .. row0 + rows - 1 of A and D, columns from n0, K blocks
 // [kb0, kb1).
 struct F8Tile {
   int row0, rows, n0, expert, kb0, kb1;
@@ -104,7 +126,7 @@ struct F8Walk {
 };
 
 // The CTA's next tile; false past its last.  `off` and `pre` are the experts'
-// row offsets and running 128-row block counts (kRows), off the K blocks (kK).
+// row offsets and running row block counts (kRows), off the K blocks (kK).
 template <Fp8Mode Mode, int BN>
 __device__ __forceinline__ bool next_tile(F8Walk& w, const F8Params& p, const int* off,
                                           const int* pre, F8Tile& o) {
@@ -115,8 +137,8 @@ __device__ __forceinline__ bool next_tile(F8Walk& w, const F8Params& p, const in
     const int local = w.t - pre[w.expert] * p.n_blocks;
     const int nb = local / mb, m = local - nb * mb;  // rows first: concurrent tiles share weights
     o.expert = w.expert;
-    o.row0 = off[w.expert] + m * kRowsPerTile;
-    o.rows = min(kRowsPerTile, off[w.expert + 1] - o.row0);
+    o.row0 = off[w.expert] + m * kRowsPerCta;
+    o.rows = min(kRowsPerCta, off[w.expert + 1] - o.row0);
     o.n0 = nb * BN;
     o.kb0 = 0;
     o.kb1 = p.k_blocks;
@@ -134,22 +156,94 @@ __device__ __forceinline__ bool next_tile(F8Walk& w, const F8Params& p, const in
       o.kb1 = max(off[o.expert + 1], o.kb0);
     }
     tc::tile_coords(local, p.m_blocks, p.n_blocks, p.group_m, m, nb);
-    o.row0 = m * kRowsPerTile;
-    o.rows = min(kRowsPerTile, p.M - o.row0);
+    o.row0 = m * kRowsPerCta;
+    o.rows = min(kRowsPerCta, p.M - o.row0);
     o.n0 = nb * BN;
   }
   w.t += static_cast<int>(gridDim.x);
   return true;
 }
 
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
+// One K block: four MMAs (K = 32 each, 32 bytes further into the swizzled rows:
+// +2 in the descriptors' 16-byte address field) into d_tmem, whose end arrives
+// on done_bar (the buffer is full) and free_bar (the stage is free).  Issued by
+// the lane with `issue` set, without a branch.
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t done_bar, uint32_t free_bar,
+                                          uint32_t issue) {
+    asm volatile(
+        "{\n\t.reg .pred i, f, t;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.u32 i, %6, 0;\n\t"
+        "setp.ne.u32 f, 0, 0;\n\t"
+        "setp.eq.u32 t, 0, 0;\n\t"
+        "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+        "add.s64 a, %1, 2;\n\t"
+        "add.s64 b, %2, 2;\n\t"
+        "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 4;\n\t"
+        "add.s64 b, %2, 4;\n\t"
+        "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 6;\n\t"
+        "add.s64 b, %2, 6;\n\t"
+        "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "@i tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+        "@i tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(done_bar), "r"(free_bar), "r"(issue)
+        : "memory");
+}
+
+// A wait of a whole warp, all lanes polling together so that the warp stays
+// converged: one lane polling for the others costs 240 clocks a time, this 50.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const F8Params& p,
+                                          volatile int* abort) {
+  const uint32_t a = smem_addr(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort != 0)) return false;
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > p.timeout_ns)) {
+      atomicExch(p.status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
+// Lane 0's arrival, predicated instead of branched around.
+__device__ __forceinline__ void lane0_arrive(uint32_t bar, int lane) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(lane)
       : "memory");
+}
+// tcgen05.wait::ld that names the registers it makes readable, so that no use
+// of them is moved above it.
+__device__ __forceinline__ void tc_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// The scales of K blocks kb .. kb + 3 (kb a multiple of 4, vec: rows of scales
+// are 16-byte aligned) of a row of nk; past its end, whatever is read instead
+// is not used.  Nothing is done with the values here: a select after the load
+// would wait for it.
+__device__ __forceinline__ void load_group(float4& v, const float* s, int kb, int nk, int vec) {
+  if (vec) {
+    v = __ldg(reinterpret_cast<const float4*>(s + min(kb, (nk - 1) & ~(kScaleGroup - 1))));
+  } else {
+    v.x = __ldg(s + min(kb, nk - 1));
+    v.y = __ldg(s + min(kb + 1, nk - 1));
+    v.z = __ldg(s + min(kb + 2, nk - 1));
+    v.w = __ldg(s + min(kb + 3, nk - 1));
+  }
 }
 
 // Two FP32 operations in one instruction.
@@ -175,12 +269,11 @@ __device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int dtype
   return dtype == DG_BF16 ? BF16::one(h) : F16::one(h);
 }
 
-// epilogue(alpha * t + beta * D) of 16 columns from col0 on, stored at D's row
-// `drow` (element offset) for the columns < N.
+// alpha * t + beta * D, bias and GELU of 16 columns from col0 on, row `drow`
+// (element offset of D).  Columns >= N read nothing.
 __device__ __forceinline__ void finish16(float (&v)[16], const F8Params& p, int64_t drow, int col0,
-                                         const void* bias, int64_t bias0) {
+                                         int64_t bias0) {
   const int n = p.N - col0;
-  if (n <= 0) return;
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] *= p.alpha;
   if (p.beta != 0.0f) {
@@ -191,40 +284,66 @@ __device__ __forceinline__ void finish16(float (&v)[16], const F8Params& p, int6
   if (p.flags & kEpiBias) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i < n) v[i] += load_as_f32(bias, bias0 + col0 + i, p.dtype_d);
+      if (i < n) v[i] += load_as_f32(p.bias, bias0 + col0 + i, p.dtype_d);
   }
   if (p.flags & kEpiGelu) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = gelu_erf(v[i]);
   }
-  const bool full = n >= 16;
-  if (p.dtype_d == DG_F32) {
-    float* d = static_cast<float*>(p.D) + drow + col0;
-    if (full && p.vec >= 16) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        reinterpret_cast<float4*>(d)[q] =
-            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) d[i] = v[i];
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t x,
+                                             int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Sends a box (this warp's 32 rows, 64 bytes from column col0 on) to D (of the
+// stack's matrix z): by TMA where all 32 rows are D's, else four lanes per
+// row.  Either way lane 0 closes one bulk group.
+__device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_t* box,
+                                         const F8Params& p, const F8Tile& tile, int row_in_tile,
+                                         int col0, int matrix, int lane) {
+  const int left = tile.rows - row_in_tile;  // rows of the box that are D's
+  if (p.tma_d && left >= 32) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(tmap_d, box, col0, tile.row0 + row_in_tile, matrix);
+      bulk_commit_group();
     }
     return;
   }
-  uint32_t w[8];
+  if (lane == 0) bulk_commit_group();
+  __syncwarp();
+  const int z = p.dtype_d == DG_F32 ? 4 : 2;
+  const int per = 16 / z;  // columns in 16 bytes
+  const int col = col0 + (lane & 3) * per;
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
-    w[q] = p.dtype_d == DG_BF16 ? BF16::pack(v[2 * q], v[2 * q + 1])
-                                : F16::pack(v[2 * q], v[2 * q + 1]);
-  uint16_t* d = static_cast<uint16_t*>(p.D) + drow + col0;
-  if (full && p.vec >= 16) {
-    reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    if (r >= left || col >= p.N) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(box + tc::epi_box_offset(r, lane & 3));
+    const int64_t row = tile.row0 + row_in_tile + r;
+    uint8_t* d = static_cast<uint8_t*>(p.D) + (matrix * p.stride_d + row * p.ldd + col) * z;
+    if (p.vec_d && col + per <= p.N) {
+      *reinterpret_cast<uint4*>(d) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      if (z == 4) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) d[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+        for (int k = 0; k < 4; ++k)
+          if (col + k < p.N) reinterpret_cast<uint32_t*>(d)[k] = w[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (col + k < p.N)
+            reinterpret_cast<uint16_t*>(d)[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+      }
+    }
   }
 }
 
@@ -232,13 +351,15 @@ template <Fp8Mode Mode, int BN, int Stages, bool ColScale>
 __global__ void __launch_bounds__(kTcThreads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ CUtensorMap tmap_d,
+                    const __grid_constant__ CUtensorMap tmap_sa,
                     const __grid_constant__ F8Params p) {
   using L = F8Smem<BN, Stages, ColScale>;
   constexpr int kBufs = L::kBufs;
   constexpr int kHalf = BN / 2;  // columns per sum warp
   constexpr int kTmemCols = kBufs * BN;
   static_assert(kHalf % 32 == 0 && kTmemCols <= 512, "tile width");
-  constexpr uint32_t idesc = idesc_f16_f32(kRowsPerTile, BN);  // operand format 0 is E4M3 here
+  constexpr uint32_t idesc = idesc_f16_f32(kRowsPerCta, BN);  // operand format 0 is E4M3 here
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -249,8 +370,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* tmem_full = empty_bar + Stages;
   uint64_t* tmem_empty = tmem_full + kBufs;
   uint64_t* drain_bar = tmem_empty + kBufs;
-  uint64_t* col_full = drain_bar + 1;  // ColScale: the two groups of column scales
-  uint64_t* col_empty = col_full + 2;
+  uint64_t* scale_full = drain_bar + 1;
+  uint64_t* scale_empty = scale_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
   int* off = reinterpret_cast<int*>(smem + L::kOffGroups);
@@ -267,18 +388,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&tmem_empty[b], kSumWarps);
     }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&col_full[g], 1);
-      mbar_init(&col_empty[g], kSumWarps);
+      mbar_init(&scale_full[g], 1);
+      mbar_init(&scale_empty[g], kSumWarps);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tmap_a);
     tma_prefetch_desc(&tmap_b);
+    tma_prefetch_desc(&tmap_d);
+    tma_prefetch_desc(&tmap_sa);
   }
-  if (warp == 9) tmem_alloc<kTmemCols>(tmem_slot);
+  if (warp == kMmaWarp) tmem_alloc<kTmemCols>(tmem_slot);
   // Launched as a programmatic dependent: everything above is this CTA's own
   // on-chip state; global memory waits for the kernel before.
   grid_dependency_wait();
@@ -299,8 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int e0 = 0; e0 < p.count; e0 += 32) {
         const int e = e0 + lane;
         int v = 0;
-        if (e < p.count)
-          v = (max(off[e + 1] - off[e], 0) + kRowsPerTile - 1) / kRowsPerTile;
+        if (e < p.count) v = (max(off[e + 1] - off[e], 0) + kRowsPerCta - 1) / kRowsPerCta;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int u = __shfl_up_sync(0xffffffffu, v, d);
@@ -321,8 +443,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp >= kSumWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
-      // ------------------------------------------------------------ producer
+    if (warp == kTmaWarp) {
+      // ---------------------------------------------------------- producer
       if (elect_one_lane()) {
         const uint64_t pol = policy_evict_last();  // tiles are read again by other CTAs
         int stage = 0;
@@ -336,11 +458,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ok = false;
               break;
             }
+            uint8_t* dst_a = smem + L::kOffA + stage * kStageA;
+            uint8_t* dst_b = smem + L::kOffB + stage * L::kTileB;
             mbar_arrive_expect_tx(&full_bar[stage], p.stage_tx);
-            tma_load_2d(&tmap_a, &full_bar[stage], smem + L::kOffA + stage * kStageA, kb * kBlock,
-                        tile.row0, pol);
-            tma_load_2d(&tmap_b, &full_bar[stage], smem + L::kOffB + stage * L::kTileB, kb * kBlock,
-                        b_row, pol);
+            tma_load_2d(&tmap_a, &full_bar[stage], dst_a, kb * kBlock, tile.row0, pol);
+            tma_load_2d(&tmap_b, &full_bar[stage], dst_b, kb * kBlock, b_row, pol);
             ++issued;
             if (++stage == Stages) {
               stage = 0;
@@ -350,74 +472,103 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         grid_launch_dependents();
         if (!ok) *abort_flag = 1;
-        // the copies this thread started land before the CTA goes away, whoever gave up
+        // the copies land before the CTA goes away, whoever gave up
         const int64_t first = issued > Stages ? issued - Stages : 0;
         for (int64_t i = first; i < issued; ++i)
           mbar_wait(&full_bar[i % Stages], static_cast<uint32_t>((i / Stages) & 1), p.timeout_ns,
                     p.status);
       }
-    } else if (warp == 9) {
-      // ------------------------------------------------------------ MMA issuer
-      if (elect_one_lane()) {
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, buf_phase = 0;
-        while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
-          for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
-            if (!mbar_wait_abortable(&tmem_empty[buf], buf_phase ^ 1, p.timeout_ns, p.status,
-                                     abort_flag) ||
-                !mbar_wait_abortable(&full_bar[stage], phase, p.timeout_ns, p.status, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint64_t da = smem_desc_sw128(smem_addr(smem + L::kOffA + stage * kStageA));
-            const uint64_t db = smem_desc_sw128(smem_addr(smem + L::kOffB + stage * L::kTileB));
-            // K step k starts 32 bytes further into the swizzled rows: +2 in the
-            // descriptor's 16-byte address field
-  #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma_f8(tmem_base + static_cast<uint32_t>(buf * BN), da + 2 * k, db + 2 * k, idesc,
-                        k != 0);
-            tc_commit(&empty_bar[stage]);
-            tc_commit(&tmem_full[buf]);
-            if (++stage == Stages) {
-              stage = 0;
-              phase ^= 1;
-            }
-            if (++buf == kBufs) {
-              buf = 0;
-              buf_phase ^= 1;
-            }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------- MMA issuer
+      // The whole warp walks the loop, so that its values stay in uniform
+      // registers, where the MMA wants them; one lane issues.
+      const uint32_t issue = elect_one_lane();
+      const uint64_t desc_a = smem_desc_sw128(smem_addr(smem + L::kOffA));
+      const uint64_t desc_b = smem_desc_sw128(smem_addr(smem + L::kOffB));
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
+        for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
+          // The operands are usually there before the buffer is: what the
+          // buffer's release waits for comes after it, in as few steps as
+          // can be.
+          ok = warp_wait(&full_bar[stage], phase, p, abort_flag) &&
+               warp_wait(&tmem_empty[buf], buf_phase ^ 1, p, abort_flag);
+          if (!ok) break;
+          tc_fence_after_sync();
+          mma_block(tmem_base + static_cast<uint32_t>(buf * BN),
+                        desc_a + static_cast<uint64_t>(stage * (kStageA >> 4)),
+                        desc_b + static_cast<uint64_t>(stage * (L::kTileB >> 4)), idesc,
+                        smem_addr(&tmem_full[buf]), smem_addr(&empty_bar[stage]), issue);
+          if (++stage == Stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+          if (++buf == kBufs) {
+            buf = 0;
+            buf_phase ^= 1;
           }
         }
-        if (!ok) *abort_flag = 1;
-        tc_commit(drain_bar);  // the MMAs issued end before the tensor memory is freed
+      }
+      if (!ok) *abort_flag = 1;
+      // the MMAs issued end before the tensor memory is freed
+      if (issue) {
+        tc_commit(drain_bar);
         mbar_wait(drain_bar, 0, p.timeout_ns, p.status);
       }
-    } else if (ColScale && warp == 10) {
-      // -------------------------------------------------------- column scales
+    } else if (warp == kScaleWarp) {
+      // -------------------------------------------------------------- scales
+      const uint64_t pol_scale = policy_evict_last();
+      int64_t groups = 0;
       int g = 0;
       uint32_t g_phase = 0;
       while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
-        for (int kb = tile.kb0; kb < tile.kb1; kb += kColGroup) {
-          ok = mbar_wait_abortable(&col_empty[g], g_phase ^ 1, p.timeout_ns, p.status, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
+        // groups lie at multiples of four K blocks: a tile's first may begin
+        // before the tile
+        for (int kb = tile.kb0 / kScaleGroup * kScaleGroup; kb < tile.kb1; kb += kScaleGroup) {
+          ok = warp_wait(&scale_empty[g], g_phase ^ 1, p, abort_flag);
           if (!ok) break;
-          float v[kColGroup][BN / 32];
+          uint8_t* rows = smem + L::kOffRow + g * kRowScaleBytes;
+          if (ColScale) {
+            // [4][BN], a lane's columns 32 apart
+            float* cs = col_scale + g * kScaleGroup * BN + lane;
 #pragma unroll
-          for (int i = 0; i < BN / 32; ++i) {
-            const float* sb = p.sb + min(tile.n0 + lane + 32 * i, p.N - 1) * p.lds_b;
+            for (int i = 0; i < BN / 32; i += 4) {
+              float4 v[4];
 #pragma unroll
-            for (int k = 0; k < kColGroup; ++k)
-              v[k][i] = kb + k < tile.kb1 ? __ldg(sb + kb + k) : 0.0f;
+              for (int j = 0; j < 4; ++j) {
+                const int64_t col = min(tile.n0 + lane + 32 * (i + j), p.N - 1);
+                load_group(v[j], p.sb + col * p.lds_b, kb, tile.kb1, p.vec_b);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                cs[32 * (i + j)] = v[j].x;
+                cs[BN + 32 * (i + j)] = v[j].y;
+                cs[2 * BN + 32 * (i + j)] = v[j].z;
+                cs[3 * BN + 32 * (i + j)] = v[j].w;
+              }
+            }
           }
+          if (p.vec_a) {
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&scale_full[g], kRowScaleBytes);
+              tma_load_2d(&tmap_sa, &scale_full[g], rows, kb, tile.row0, pol_scale);
+            }
+          } else {
+            float4 v[4];
 #pragma unroll
-          for (int k = 0; k < kColGroup; ++k)
+            for (int i = 0; i < 4; ++i) {
+              const int64_t r = min(tile.row0 + lane + 32 * i, p.M - 1);
+              load_group(v[i], p.sa + r * p.lds_a, kb, tile.kb1, 0);
+            }
 #pragma unroll
-            for (int i = 0; i < BN / 32; ++i)
-              col_scale[(g * kColGroup + k) * BN + lane + 32 * i] = v[k][i];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&col_full[g]);
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(rows + (lane + 32 * i) * 16) = v[i];
+            __syncwarp();
+            lane0_arrive(smem_addr(&scale_full[g]), lane);
+          }
+          ++groups;
           if (++g == 2) {
             g = 0;
             g_phase ^= 1;
@@ -425,69 +576,91 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       if (!ok) *abort_flag = 1;
+      // the copies land before the CTA goes away
+      for (int64_t i = groups > 2 ? groups - 2 : 0; i < groups; ++i)
+        warp_wait(&scale_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), p, abort_flag);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    // ------------------------------------------------------ sums and epilogue
-    const int quarter = warp & 3, half = warp >> 2;
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const int r = quarter * 32 + lane;
+    // ---------------------------------------------------- sums and epilogue
+    const int in_tile = (warp & 3) * 32, half = warp >> 2;
+    const uint32_t src0 =
+        tmem_base + (static_cast<uint32_t>(in_tile) << 16) + static_cast<uint32_t>(half * kHalf);
+    const uint32_t empty0 = smem_addr(&tmem_empty[0]);
+    uint8_t* box = smem + L::kOffBox + warp * kBoxBytes;
     int buf = 0, g = 0;
     uint32_t buf_phase = 0, g_phase = 0;
     while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
       float2 acc[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      const int col0 = tile.n0 + half * kHalf;
-      const float* sa = p.sa + static_cast<int64_t>(tile.row0 + min(r, tile.rows - 1)) * p.lds_a;
-      const float* sb = p.sb + (Mode == Fp8Mode::kRows ? tile.expert * p.stride_sb : 0) +
-                        static_cast<int64_t>(min(col0, p.N - 1) / kBlock) * p.lds_b;
-      float a_next = 0.0f, b_next = 1.0f;
-      if (tile.kb0 < tile.kb1) {
-        a_next = __ldg(sa + tile.kb0);
-        if (!ColScale) b_next = __ldg(sb + tile.kb0);
-      }
+      // The row's scales of a group of K blocks come from shared memory, the
+      // half's weight block's (one address per warp) straight from memory, one
+      // group ahead.
+      const float* sb = nullptr;
+      if (!ColScale)
+        sb = p.sb + (Mode == Fp8Mode::kRows ? tile.expert * p.stride_sb : 0) +
+             static_cast<int64_t>(min(tile.n0 + half * kHalf, p.N - 1) / kBlock) * p.lds_b;
+      float4 ra, ca, cb;
+      if (!ColScale && tile.kb0 < tile.kb1) load_group(cb, sb, 0, tile.kb1, p.vec_b);
+#pragma unroll 1
       for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
-        const float s = a_next * b_next;
-        if (kb + 1 < tile.kb1) {
-          a_next = __ldg(sa + kb + 1);
-          if (!ColScale) b_next = __ldg(sb + kb + 1);
+        const int in_group = kb % kScaleGroup;
+        if (in_group == 0 || kb == tile.kb0) {
+          ok = warp_wait(&scale_full[g], g_phase, p, abort_flag);
+          ra = *reinterpret_cast<const float4*>(smem + L::kOffRow + g * kRowScaleBytes +
+                                                (in_tile + lane) * 16);
+          if (!ColScale) {
+            ca = cb;
+            load_group(cb, sb, kb + kScaleGroup, tile.kb1, p.vec_b);
+          } else {
+            // a segment's first block may lie inside a group
+            for (int i = 0; i < in_group; ++i) ra = make_float4(ra.y, ra.z, ra.w, 0.0f);
+          }
         }
-        const int in_group = (kb - tile.kb0) % kColGroup;
-        if (ColScale && in_group == 0)
-          ok = mbar_wait_abortable(&col_full[g], g_phase, p.timeout_ns, p.status, abort_flag);
-        ok = ok && mbar_wait_abortable(&tmem_full[buf], buf_phase, p.timeout_ns, p.status,
-                                       abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        const float* cs = col_scale + (g * kScaleGroup + in_group) * BN + half * kHalf;
+        ok = ok && warp_wait(&tmem_full[buf], buf_phase, p, abort_flag);
         if (!ok) break;
         tc_fence_after_sync();
+        const uint32_t src = src0 + static_cast<uint32_t>(buf * BN);
+        // 16 columns are loaded while the 16 before are added
+        uint32_t v[2][16];
+        tmem_ld_16cols(src, v[0]);
+        const float s = ColScale ? ra.x : ra.x * ca.x;
         const float2 s2 = make_float2(s, s);
-        const uint32_t src = tmem_base + lane_base + static_cast<uint32_t>(buf * BN + half * kHalf);
-        const float* cs = col_scale + (g * kColGroup + in_group) * BN + half * kHalf;
+        ra = make_float4(ra.y, ra.z, ra.w, 0.0f);
+        if (!ColScale) ca = make_float4(ca.y, ca.z, ca.w, 0.0f);
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 32) {
-          uint32_t v[32];
-          tmem_ld_32cols(src + c, v);
-          tc_wait_ld();
-          if (c + 32 >= kHalf) {
+        for (int c = 0; c < kHalf; c += 16) {
+          uint32_t(&x)[16] = v[(c / 16) & 1];
+          tc_wait_ld16(x);
+          if (c + 16 < kHalf) {
+            tmem_ld_16cols(src + c + 16, v[(c / 16 + 1) & 1]);
+          } else {
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tmem_empty[buf]);
+            lane0_arrive(empty0 + static_cast<uint32_t>(buf * 8), lane);
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            if (ColScale) x = mul2(x, *reinterpret_cast<const float2*>(cs + c + 2 * i));
-            acc[c / 2 + i] = fma2(x, s2, acc[c / 2 + i]);
+          for (int i = 0; i < 8; i += 2) {
+            float2 t0 = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            float2 t1 = make_float2(__uint_as_float(x[2 * i + 2]), __uint_as_float(x[2 * i + 3]));
+            if (ColScale) {
+              const float4 k = *reinterpret_cast<const float4*>(cs + c + 2 * i);
+              t0 = mul2(t0, make_float2(k.x, k.y));
+              t1 = mul2(t1, make_float2(k.z, k.w));
+            }
+            acc[c / 2 + i] = fma2(t0, s2, acc[c / 2 + i]);
+            acc[c / 2 + i + 1] = fma2(t1, s2, acc[c / 2 + i + 1]);
           }
         }
         if (++buf == kBufs) {
           buf = 0;
           buf_phase ^= 1;
         }
-        if (ColScale && (in_group == kColGroup - 1 || kb + 1 == tile.kb1)) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&col_empty[g]);
+        if (in_group == kScaleGroup - 1 || kb + 1 == tile.kb1) {
+          __syncwarp();  // every lane has its scales of the group
+          lane0_arrive(smem_addr(&scale_empty[g]), lane);
           if (++g == 2) {
             g = 0;
             g_phase ^= 1;
@@ -495,39 +668,115 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       if (!ok) break;
-      if (r < tile.rows) {
-        const int64_t drow = (Mode == Fp8Mode::kK ? tile.expert * p.stride_d : 0) +
-                             static_cast<int64_t>(tile.row0 + r) * p.ldd;
-        const int64_t bias0 = Mode == Fp8Mode::kRows ? tile.expert * p.stride_bias : 0;
+      // D, 32 columns at a time; the sums move down so that the loop's body
+      // (whose GELU is long) is there once
+      const int matrix = Mode == Fp8Mode::kK ? tile.expert : 0;
+      const int64_t row = tile.row0 + min(in_tile + lane, tile.rows - 1);
+      const int64_t drow = matrix * p.stride_d + row * p.ldd;
+      const int64_t bias0 = Mode == Fp8Mode::kRows ? tile.expert * p.stride_bias : 0;
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 32) {
+        const int col0 = tile.n0 + half * kHalf + c;
+        if (col0 >= p.N || tile.rows <= in_tile) break;
+        uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 16) {
-          float v[16];
+        for (int h = 0; h < 2; ++h) {
+          float x[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            v[2 * i] = acc[c / 2 + i].x;
-            v[2 * i + 1] = acc[c / 2 + i].y;
+            x[2 * i] = acc[8 * h + i].x;
+            x[2 * i + 1] = acc[8 * h + i].y;
           }
-          finish16(v, p, drow, col0 + c, p.bias, bias0);
+          finish16(x, p, drow, col0 + 16 * h, bias0);
+          if (p.dtype_d == DG_F32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
+          } else if (p.dtype_d == DG_BF16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[8 * h + i] = BF16::pack(x[2 * i], x[2 * i + 1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[8 * h + i] = F16::pack(x[2 * i], x[2 * i + 1]);
+          }
+          // the box is full: 16 FP32 columns, or both halves' 16-bit ones
+          if (p.dtype_d == DG_F32 ? col0 + 16 * h < p.N : h == 1) {
+            if (lane == 0) bulk_wait_group_read<0>();  // its last store has read it
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(box + tc::epi_box_offset(lane, q)) =
+                  make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            send_box(&tmap_d, box, p, tile, in_tile, p.dtype_d == DG_F32 ? col0 + 16 * h : col0,
+                     matrix, lane);
+          }
         }
+#pragma unroll
+        for (int i = 0; i + 16 < kHalf / 2; ++i) acc[i] = acc[i + 16];
       }
     }
     if (!ok) *abort_flag = 1;
+    if (lane == 0) bulk_wait_group<0>();  // this thread's stores end before the CTA does
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc<kTmemCols>(tmem_base);
   }
 }
 
+// D as a stack of `count` matrices: boxes of 32 rows x 64 bytes, 64-byte
+// swizzle.  Kept per thread as tc::make_map_2d keeps its maps.
+cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int64_t rows,
+                         int64_t cols, int64_t ld, int64_t count, int64_t stride) {
+  struct Entry {
+    const void* base;
+    int64_t rows, cols, ld, count, stride;
+    int dtype;
+    CUtensorMap map;
+  };
+  constexpr int kCache = 16;
+  thread_local Entry cache[kCache];
+  thread_local int used = 0, next = 0;
+  for (int i = 0; i < used; ++i) {
+    const Entry& c = cache[i];
+    if (c.base == base && c.rows == rows && c.cols == cols && c.ld == ld && c.count == count &&
+        c.stride == stride && c.dtype == static_cast<int>(dtype)) {
+      *map = c.map;
+      return cudaSuccess;
+    }
+  }
+  tc::EncodeTiledFn fn = tc::encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const int z = dtype == DG_F32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(count)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * z),
+                                 static_cast<cuuint64_t>((count > 1 ? stride : rows * ld) * z)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / z), 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType type = dtype == DG_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == DG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  cache[next] = Entry{base, rows, cols, ld, count, stride, static_cast<int>(dtype), *map};
+  next = (next + 1) % kCache;
+  if (used < kCache) ++used;
+  return cudaSuccess;
+}
+
 template <Fp8Mode Mode, int BN, int Stages, bool ColScale>
 cudaError_t run_fp8(const Fp8Args& a) {
   using L = F8Smem<BN, Stages, ColScale>;
-  const int box_a = Mode == Fp8Mode::kDense && a.M < kRowsPerTile
+  // Fewer rows than a tile: only those (whole swizzle atoms of 8) are loaded;
+  // the stale shared memory below feeds rows of D that are not there.
+  const int box_a = Mode == Fp8Mode::kDense && a.M < kRowsPerCta
                         ? static_cast<int>((a.M + 7) / 8 * 8)
-                        : kRowsPerTile;
+                        : kRowsPerCta;
   CUtensorMap ta, tb;
   cudaError_t e = tc::make_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, a.M, a.K, a.lda, box_a,
                                   128, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -540,7 +789,7 @@ cudaError_t run_fp8(const Fp8Args& a) {
   F8Params p;
   p.M = static_cast<int>(a.M);
   p.N = static_cast<int>(a.N);
-  p.m_blocks = static_cast<int>((a.M + kRowsPerTile - 1) / kRowsPerTile);
+  p.m_blocks = static_cast<int>((a.M + kRowsPerCta - 1) / kRowsPerCta);
   p.n_blocks = static_cast<int>((a.N + BN - 1) / BN);
   p.k_blocks = static_cast<int>((a.K + kBlock - 1) / kBlock);
   p.k_rows = static_cast<int>(a.K);
@@ -566,10 +815,32 @@ cudaError_t run_fp8(const Fp8Args& a) {
   p.flags = a.epi;
   p.dtype_d = static_cast<int>(a.dtype_d);
   const int64_t z = a.dtype_d == DG_F32 ? 4 : 2;
-  p.vec = (a.ldd * z) % 16 == 0 && (a.stride_d * z) % 16 == 0 ? 16 : 0;
+  p.vec_d = (a.ldd * z) % 16 == 0 && (a.stride_d * z) % 16 == 0 ? 1 : 0;
+  // TMA clips a store at N in whole 16-byte pieces: another N would write past it
+  p.tma_d = p.vec_d && (a.N * z) % 16 == 0 ? 1 : 0;
+  auto vec = [](const float* s, int64_t ld, int64_t stride) {
+    return (reinterpret_cast<uintptr_t>(s) & 15) == 0 && ld % 4 == 0 && stride % 4 == 0;
+  };
+  p.vec_a = vec(a.sa, a.lds_a, 0);
+  p.vec_b = vec(a.sb, a.lds_b, a.stride_sb);
   p.stage_tx = static_cast<uint32_t>(box_a * 128 + L::kTileB);
   p.status = a.status;
   p.timeout_ns = a.timeout_ns;
+  CUtensorMap td = ta;  // not used without tma_d
+  if (p.tma_d) {
+    e = make_out_map(&td, a.D, a.dtype_d, a.M, a.N, a.ldd, Mode == Fp8Mode::kK ? a.count : 1,
+                     a.stride_d);
+    if (e != cudaSuccess) return e;
+  }
+
+  CUtensorMap tsa = ta;  // not used without vec_a
+  if (p.vec_a) {
+    // whole groups: they end within the row's pitch, a multiple of four
+    const int64_t width = (p.k_blocks + kScaleGroup - 1) / kScaleGroup * kScaleGroup;
+    e = tc::make_map_2d(&tsa, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.sa, a.M, width, a.lds_a * 4,
+                        kRowsPerCta, kScaleGroup, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+  }
 
   auto kern = gemm_fp8_kernel<Mode, BN, Stages, ColScale>;
   int dev = 0;
@@ -583,35 +854,42 @@ cudaError_t run_fp8(const Fp8Args& a) {
     if (r != cudaSuccess) return r;
     if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                L::bytes(Mode == Fp8Mode::kDense ? 0 : kMaxExperts));
+                                L::bytes(Mode == Fp8Mode::kDense ? 0 : kMaxFp8Experts));
   });
   if (e != cudaSuccess) return e;
   // Experts' tiles are counted on the device: at most one part-filled row
   // block per expert beside the full ones.
   const int64_t most = Mode == Fp8Mode::kRows
-                           ? (a.M / kRowsPerTile + std::min(a.count, a.M)) * p.n_blocks
+                           ? (a.M / kRowsPerCta + std::min(a.count, a.M)) * p.n_blocks
                            : tiles;
   if (most > (1 << 30)) return cudaErrorInvalidConfiguration;  // tile numbers are 32-bit
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(most, a.sm_count));
-  e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kTcThreads),
-                       static_cast<size_t>(L::bytes(p.count)), a.stream, ta, tb, p);
+  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(most, a.sm_count));
+  e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kTcThreads),
+                       static_cast<size_t>(L::bytes(p.count)), a.stream, ta, tb, td, tsa, p);
   count_launches(1);
   return e;
 }
 
-template <Fp8Mode Mode>
-cudaError_t run_mode(const Fp8Args& a) {
-  if (a.block_rows_b == 1) return run_fp8<Mode, 256, 4, true>(a);
-  return run_fp8<Mode, 256, 4, false>(a);
+// 128 x 256 tiles where there are enough for the SMs, else 128 x 128.
+template <Fp8Mode Mode, bool ColScale>
+cudaError_t run_shape(const Fp8Args& a) {
+  const int64_t row_blocks =
+      Mode == Fp8Mode::kRows ? a.M / 128 + std::min(a.count, a.M) : (a.M + 127) / 128;
+  const int64_t wide_tiles =
+      row_blocks * ((a.N + 255) / 256) * (Mode == Fp8Mode::kK ? a.count : 1);
+  if (wide_tiles >= a.sm_count) return run_fp8<Mode, 256, 4, ColScale>(a);
+  return run_fp8<Mode, 128, 5, ColScale>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_tc(const Fp8Args& a) {
   switch (a.mode) {
-    case Fp8Mode::kDense: return run_mode<Fp8Mode::kDense>(a);
-    case Fp8Mode::kRows: return run_fp8<Fp8Mode::kRows, 256, 4, false>(a);
-    case Fp8Mode::kK: return run_fp8<Fp8Mode::kK, 256, 4, true>(a);
+    case Fp8Mode::kDense:
+      return a.block_rows_b == 1 ? run_shape<Fp8Mode::kDense, true>(a)
+                                 : run_shape<Fp8Mode::kDense, false>(a);
+    case Fp8Mode::kRows: return run_shape<Fp8Mode::kRows, false>(a);
+    case Fp8Mode::kK: return run_shape<Fp8Mode::kK, true>(a);
   }
   return cudaErrorInvalidValue;
 }

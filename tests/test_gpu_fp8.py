@@ -126,7 +126,8 @@ def check(got, t, err, dtype):
 
 SIZES = [(1, 1, 1), (1, 8960, 1536), (3, 100, 128), (8, 256, 129), (9, 31, 700), (16, 513, 2064),
          (17, 64, 128), (31, 130, 127), (100, 200, 1000), (128, 256, 512), (129, 257, 640),
-         (300, 1000, 384), (257, 520, 2049), (1024, 1100, 256)]
+         (300, 1000, 384), (257, 520, 2049), (1024, 1100, 256), (2100, 2300, 300), (777, 7000, 130),
+         (2048, 2560, 1152)]
 
 
 @pytest.mark.parametrize("block_rows", [1, 128])
@@ -260,7 +261,7 @@ def test_grouped_offsets_are_clamped(dg):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("M,N", [(64, 100), (256, 300), (129, 513)])
+@pytest.mark.parametrize("M,N", [(64, 100), (256, 300), (129, 513), (1400, 1501)])
 @pytest.mark.parametrize("sizes", [[128], [0, 256, 128, 0], [640, 128], [0]])
 def test_grouped_wgrad(dg, sizes, M, N, dtype):
     offsets = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
