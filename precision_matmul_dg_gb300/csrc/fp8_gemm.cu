@@ -55,16 +55,10 @@ namespace {
 
 using namespace fp8;
 
-constexpr int kTcThreads = 384;
-constexpr int kLaunchRegs = 168, kSumRegs = 216, kOtherRegs = 72;  // per thread
-static_assert(2 * kSumRegs + kOtherRegs == 3 * kLaunchRegs, "shares of the launch's registers");
 constexpr int kScaleGroup = 4;  // K blocks (of one number / 4) whose scales are staged together
-constexpr int kSumWarps = 8;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10;
 constexpr int kRowsPerCta = 128;  // TMEM lanes
 constexpr int kStageA = kRowsPerCta * 128;
 constexpr int kRowScaleBytes = kRowsPerCta * kScaleGroup * 4;
-constexpr int kBoxBytes = 32 * 64;  // 32 rows of 64 bytes, 64-byte swizzle
 
 struct F8Params {
   int M, N;  // kRows: M rows in all
@@ -91,17 +85,42 @@ struct F8Params {
   uint64_t timeout_ns;
 };
 
+// The two shapes of a CTA: 128 x 256 tiles, two warpgroups of sum warps and a
+// third for the rest, alone on its SM; or 128 x 128 tiles, one and one, two
+// CTAs to an SM.  A sum thread takes 128 columns of a row either way.
+template <int BN>
+struct F8Shape {
+  static_assert(BN == 128 || BN == 256, "tile width");
+  static constexpr int kSumWarps = BN / 32;
+  static constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kScaleWarp = kSumWarps + 2;
+  static constexpr int kThreads = (kSumWarps + 4) * 32;
+  static constexpr int kCtasPerSm = BN == 256 ? 1 : 2;
+  // registers per thread: at launch, and as the warpgroups share them
+  static constexpr int kLaunchRegs = BN == 256 ? 168 : 128;
+  static constexpr int kSumRegs = BN == 256 ? 216 : 200;
+  static constexpr int kOtherRegs = BN == 256 ? 72 : 56;
+  static_assert(kSumWarps / 4 * kSumRegs + kOtherRegs == (kSumWarps / 4 + 1) * kLaunchRegs,
+                "shares of the launch's registers");
+};
+
 template <int BN, int Stages, bool ColScale>
 struct F8Smem {
+  static constexpr int kSumWarps = F8Shape<BN>::kSumWarps;
   static constexpr int kTileB = BN * 128;
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + Stages * kStageA;
   static constexpr int kOffBox = kOffB + Stages * kTileB;
-  static constexpr int kOffRow = kOffBox + kSumWarps * kBoxBytes;  // row scales [2][128][4]
+  // D's boxes, kBoxes to a sum warp: 32 rows of 128 bytes where there is room.
+  // (A fourth stage of 128 x 256 tiles would leave room for one box of 64-byte
+  // rows: 8192^3 476 us against 466, the experts' FP32 gradients 762 against 694.)
+  static constexpr int kBoxRow = BN == 256 ? 128 : 64;
+  static constexpr int kBoxes = BN == 256 ? 2 : 1;
+  static constexpr int kBoxBytes = 32 * kBoxRow;
+  static constexpr int kOffRow = kOffBox + kSumWarps * kBoxes * kBoxBytes;  // [2][128][4]
   static constexpr int kOffCol = kOffRow + 2 * kRowScaleBytes;
   // column scales [2][4][BN]
   static constexpr int kOffBar = kOffCol + (ColScale ? 2 * kScaleGroup * BN * 4 : 0);
-  static constexpr int kBufs = 512 / BN;
+  static constexpr int kBufs = 2;
   static constexpr int kBars = 2 * Stages + 2 * kBufs + 1 + 4;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffAbort = kOffSlot + 4;
@@ -112,7 +131,9 @@ struct F8Smem {
   static constexpr int bytes(int64_t count) {
     return kFixed + static_cast<int>(count > 0 ? (ColScale ? 1 : 2) * (count + 1) * 4 : 0);
   }
-  static_assert(bytes(kMaxFp8Experts) <= 227 * 1024, "shared memory of a CTA");
+  // an SM has 228 KB, of which each CTA costs 1 KB
+  static_assert(bytes(kMaxFp8Experts) <= (228 / F8Shape<BN>::kCtasPerSm - 1) * 1024,
+                "shared memory of a CTA");
 };
 
 // A tile: rows row0 .. row0 + rows - 1 of A and D, columns from n0, K blocks
@@ -263,10 +284,68 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+// gelu_erf (epilogue.cuh) of two values, its multiplications and additions in
+// packed instructions: GELU(t) = max(t, 0) - |t| q.  The GELU of a tile costs as
+// much as several of its K blocks, so instructions count.
+__device__ __forceinline__ float2 gelu2(float2 t) {
+  constexpr float p = 0.3275911f, a1 = 0.254829592f, a2 = -0.284496736f, a3 = 1.421413741f,
+                  a4 = -1.453152027f, a5 = 1.061405429f;
+  constexpr float kP = p * 0.70710678118654752f;  // p / sqrt 2
+  constexpr float kE = -0.72134752044448170f;     // -log2(e) / 2
+  auto both = [](float x) { return make_float2(x, x); };
+  const float2 a = make_float2(fabsf(t.x), fabsf(t.y));
+  const float2 den = fma2(a, both(kP), both(1.0f));
+  float2 s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(den.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(den.y));
+  float2 q = fma2(both(0.5f * a5), s, both(0.5f * a4));
+  q = fma2(q, s, both(0.5f * a3));
+  q = fma2(q, s, both(0.5f * a2));
+  q = fma2(q, s, both(0.5f * a1));
+  const float2 e = mul2(mul2(a, a), both(kE));
+  const float2 x = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+  q = mul2(mul2(q, s), x);
+  return fma2(mul2(a, both(-1.0f)), q, make_float2(fmaxf(t.x, 0.0f), fmaxf(t.y, 0.0f)));
+}
+
 __device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int dtype) {
   if (dtype == DG_F32) return static_cast<const float*>(p)[i];
   const uint32_t h = static_cast<const uint16_t*>(p)[i];
   return dtype == DG_BF16 ? BF16::one(h) : F16::one(h);
+}
+
+// v[i] += k * (the 16 values of dtype from p on), the first n of them; 16-byte
+// loads where there are 16 at such an address.
+__device__ __forceinline__ void add16(float (&v)[16], float k, const void* p, int dtype, int n) {
+  if (n >= 16 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const uint4* q = static_cast<const uint4*>(p);
+    if (dtype == DG_F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = q[i];
+        v[4 * i] = fmaf(k, __uint_as_float(w.x), v[4 * i]);
+        v[4 * i + 1] = fmaf(k, __uint_as_float(w.y), v[4 * i + 1]);
+        v[4 * i + 2] = fmaf(k, __uint_as_float(w.z), v[4 * i + 2]);
+        v[4 * i + 3] = fmaf(k, __uint_as_float(w.w), v[4 * i + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 w4 = q[i];
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = dtype == DG_BF16 ? BF16::unpack(w[j]) : F16::unpack(w[j]);
+          v[8 * i + 2 * j] = fmaf(k, f.x, v[8 * i + 2 * j]);
+          v[8 * i + 2 * j + 1] = fmaf(k, f.y, v[8 * i + 2 * j + 1]);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) v[i] = fmaf(k, load_as_f32(p, i, dtype), v[i]);
+  }
 }
 
 // alpha * t + beta * D, bias and GELU of 16 columns from col0 on, row `drow`
@@ -274,21 +353,20 @@ __device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int dtype
 __device__ __forceinline__ void finish16(float (&v)[16], const F8Params& p, int64_t drow, int col0,
                                          int64_t bias0) {
   const int n = p.N - col0;
+  const int64_t z = p.dtype_d == DG_F32 ? 4 : 2;
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] *= p.alpha;
-  if (p.beta != 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) v[i] = fmaf(p.beta, load_as_f32(p.D, drow + col0 + i, p.dtype_d), v[i]);
-  }
-  if (p.flags & kEpiBias) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) v[i] += load_as_f32(p.bias, bias0 + col0 + i, p.dtype_d);
-  }
+  if (p.beta != 0.0f)
+    add16(v, p.beta, static_cast<const uint8_t*>(p.D) + (drow + col0) * z, p.dtype_d, n);
+  if (p.flags & kEpiBias)
+    add16(v, 1.0f, static_cast<const uint8_t*>(p.bias) + (bias0 + col0) * z, p.dtype_d, n);
   if (p.flags & kEpiGelu) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = gelu_erf(v[i]);
+    for (int i = 0; i < 16; i += 2) {
+      const float2 g = gelu2(make_float2(v[i], v[i + 1]));
+      v[i] = g.x;
+      v[i + 1] = g.y;
+    }
   }
 }
 
@@ -301,9 +379,18 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
-// Sends a box (this warp's 32 rows, 64 bytes from column col0 on) to D (of the
-// stack's matrix z): by TMA where all 32 rows are D's, else four lanes per
-// row.  Either way lane 0 closes one bulk group.
+// Where the 16-byte piece q of row r of a box lies: the swizzle of D's map,
+// under which a warp's lanes, a row each, meet no bank conflicts.
+template <int Row>
+__device__ __forceinline__ uint32_t box_offset(int r, int q) {
+  return static_cast<uint32_t>(Row == 128 ? r * 128 + ((q ^ (r & 7)) << 4)
+                                          : r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+}
+
+// Sends a box (this warp's 32 rows, Row bytes from column col0 on) to D (of the
+// stack's matrix z): by TMA where all 32 rows are D's, else a row in Row / 16
+// lanes.  Either way lane 0 closes one bulk group.
+template <int Row>
 __device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_t* box,
                                          const F8Params& p, const F8Tile& tile, int row_in_tile,
                                          int col0, int matrix, int lane) {
@@ -319,14 +406,16 @@ __device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_
   }
   if (lane == 0) bulk_commit_group();
   __syncwarp();
+  constexpr int kLanes = Row / 16, kRows = 32 / kLanes;
   const int z = p.dtype_d == DG_F32 ? 4 : 2;
   const int per = 16 / z;  // columns in 16 bytes
-  const int col = col0 + (lane & 3) * per;
+  const int q = lane % kLanes;
+  const int col = col0 + q * per;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 2);
+  for (int i = 0; i < 32 / kRows; ++i) {
+    const int r = i * kRows + lane / kLanes;
     if (r >= left || col >= p.N) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(box + tc::epi_box_offset(r, lane & 3));
+    const uint4 v = *reinterpret_cast<const uint4*>(box + box_offset<Row>(r, q));
     const int64_t row = tile.row0 + row_in_tile + r;
     uint8_t* d = static_cast<uint8_t*>(p.D) + (matrix * p.stride_d + row * p.ldd + col) * z;
     if (p.vec_d && col + per <= p.N) {
@@ -348,17 +437,19 @@ __device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_
 }
 
 template <Fp8Mode Mode, int BN, int Stages, bool ColScale>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_d,
                     const __grid_constant__ CUtensorMap tmap_sa,
                     const __grid_constant__ F8Params p) {
   using L = F8Smem<BN, Stages, ColScale>;
+  using S = F8Shape<BN>;
+  constexpr int kSumWarps = S::kSumWarps, kTmaWarp = S::kTmaWarp, kMmaWarp = S::kMmaWarp,
+                kScaleWarp = S::kScaleWarp;
   constexpr int kBufs = L::kBufs;
-  constexpr int kHalf = BN / 2;  // columns per sum warp
+  constexpr int kHalf = 128;  // columns per sum warp
   constexpr int kTmemCols = kBufs * BN;
-  static_assert(kHalf % 32 == 0 && kTmemCols <= 512, "tile width");
   constexpr uint32_t idesc = idesc_f16_f32(kRowsPerCta, BN);  // operand format 0 is E4M3 here
 
   extern __shared__ uint8_t smem_raw[];
@@ -409,7 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Offsets clamped to the rows there are (kK: in K blocks, rounded down).
     const int limit = Mode == Fp8Mode::kRows ? p.M : p.k_rows;
     bool odd = false;
-    for (int e = threadIdx.x; e <= p.count; e += kTcThreads) {
+    for (int e = threadIdx.x; e <= p.count; e += S::kThreads) {
       const int v = min(max(__ldg(p.offsets + e), 0), limit);
       odd |= Mode == Fp8Mode::kK && (v & (kBlock - 1)) != 0;
       off[e] = Mode == Fp8Mode::kK ? v / kBlock : v;
@@ -442,7 +533,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   F8Tile tile;
 
   if (warp >= kSumWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
     if (warp == kTmaWarp) {
       // ---------------------------------------------------------- producer
       if (elect_one_lane()) {
@@ -581,14 +672,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         warp_wait(&scale_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), p, abort_flag);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSumRegs));
     // ---------------------------------------------------- sums and epilogue
     const int in_tile = (warp & 3) * 32, half = warp >> 2;
     const uint32_t src0 =
         tmem_base + (static_cast<uint32_t>(in_tile) << 16) + static_cast<uint32_t>(half * kHalf);
     const uint32_t empty0 = smem_addr(&tmem_empty[0]);
-    uint8_t* box = smem + L::kOffBox + warp * kBoxBytes;
-    int buf = 0, g = 0;
+    constexpr int kBoxRow = L::kBoxRow;
+    uint8_t* boxes = smem + L::kOffBox + warp * L::kBoxes * L::kBoxBytes;
+    int buf = 0, g = 0, next_box = 0;
     uint32_t buf_phase = 0, g_phase = 0;
     while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
       float2 acc[kHalf / 2];
@@ -674,40 +766,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int64_t row = tile.row0 + min(in_tile + lane, tile.rows - 1);
       const int64_t drow = matrix * p.stride_d + row * p.ldd;
       const int64_t bias0 = Mode == Fp8Mode::kRows ? tile.expert * p.stride_bias : 0;
+      const int col_end = tile.rows > in_tile ? min(p.N, tile.n0 + (half + 1) * kHalf) : 0;
+      int fill = 0, box_col = 0;  // the open box: 16-byte pieces in it, its first column
 #pragma unroll 1
-      for (int c = 0; c < kHalf; c += 32) {
-        const int col0 = tile.n0 + half * kHalf + c;
-        if (col0 >= p.N || tile.rows <= in_tile) break;
-        uint32_t w[16];
+      for (int col0 = tile.n0 + half * kHalf; col0 < col_end; col0 += 32) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const int col = col0 + 16 * h;
+          if (col >= col_end) break;
           float x[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             x[2 * i] = acc[8 * h + i].x;
             x[2 * i + 1] = acc[8 * h + i].y;
           }
-          finish16(x, p, drow, col0 + 16 * h, bias0);
+          finish16(x, p, drow, col, bias0);
+          uint8_t* box = boxes + next_box * L::kBoxBytes;
+          if (fill == 0) {
+            box_col = col;
+            if (lane == 0) bulk_wait_group_read<L::kBoxes - 1>();  // its last store has read it
+            __syncwarp();
+          }
           if (p.dtype_d == DG_F32) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
-          } else if (p.dtype_d == DG_BF16) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[8 * h + i] = BF16::pack(x[2 * i], x[2 * i + 1]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[8 * h + i] = F16::pack(x[2 * i], x[2 * i + 1]);
-          }
-          // the box is full: 16 FP32 columns, or both halves' 16-bit ones
-          if (p.dtype_d == DG_F32 ? col0 + 16 * h < p.N : h == 1) {
-            if (lane == 0) bulk_wait_group_read<0>();  // its last store has read it
-            __syncwarp();
-#pragma unroll
             for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(box + tc::epi_box_offset(lane, q)) =
+              *reinterpret_cast<float4*>(box + box_offset<kBoxRow>(lane, fill + q)) =
+                  make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            fill += 4;
+          } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = p.dtype_d == DG_BF16 ? BF16::pack(x[2 * i], x[2 * i + 1])
+                                          : F16::pack(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              *reinterpret_cast<uint4*>(box + box_offset<kBoxRow>(lane, fill + q)) =
                   make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-            send_box(&tmap_d, box, p, tile, in_tile, p.dtype_d == DG_F32 ? col0 + 16 * h : col0,
-                     matrix, lane);
+            fill += 2;
+          }
+          if (fill == kBoxRow / 16 || col + 16 >= col_end) {
+            send_box<kBoxRow>(&tmap_d, box, p, tile, in_tile, box_col, matrix, lane);
+            fill = 0;
+            if (++next_box == L::kBoxes) next_box = 0;
           }
         }
 #pragma unroll
@@ -726,14 +827,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// D as a stack of `count` matrices: boxes of 32 rows x 64 bytes, 64-byte
-// swizzle.  Kept per thread as tc::make_map_2d keeps its maps.
+// D as a stack of `count` matrices: boxes of 32 rows x box_row bytes (64 or
+// 128), swizzled over their rows.  Kept per thread as tc::make_map_2d keeps its maps.
 cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int64_t rows,
-                         int64_t cols, int64_t ld, int64_t count, int64_t stride) {
+                         int64_t cols, int64_t ld, int64_t count, int64_t stride, int box_row) {
   struct Entry {
     const void* base;
     int64_t rows, cols, ld, count, stride;
-    int dtype;
+    int dtype, box_row;
     CUtensorMap map;
   };
   constexpr int kCache = 16;
@@ -742,7 +843,7 @@ cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int
   for (int i = 0; i < used; ++i) {
     const Entry& c = cache[i];
     if (c.base == base && c.rows == rows && c.cols == cols && c.ld == ld && c.count == count &&
-        c.stride == stride && c.dtype == static_cast<int>(dtype)) {
+        c.stride == stride && c.dtype == static_cast<int>(dtype) && c.box_row == box_row) {
       *map = c.map;
       return cudaSuccess;
     }
@@ -754,16 +855,17 @@ cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int
                               static_cast<cuuint64_t>(count)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * z),
                                  static_cast<cuuint64_t>((count > 1 ? stride : rows * ld) * z)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / z), 32, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_row / z), 32, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType type = dtype == DG_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dtype == DG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box_row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  cache[next] = Entry{base, rows, cols, ld, count, stride, static_cast<int>(dtype), *map};
+  cache[next] = Entry{base, rows, cols, ld, count, stride, static_cast<int>(dtype), box_row, *map};
   next = (next + 1) % kCache;
   if (used < kCache) ++used;
   return cudaSuccess;
@@ -829,7 +931,7 @@ cudaError_t run_fp8(const Fp8Args& a) {
   CUtensorMap td = ta;  // not used without tma_d
   if (p.tma_d) {
     e = make_out_map(&td, a.D, a.dtype_d, a.M, a.N, a.ldd, Mode == Fp8Mode::kK ? a.count : 1,
-                     a.stride_d);
+                     a.stride_d, L::kBoxRow);
     if (e != cudaSuccess) return e;
   }
 
@@ -852,7 +954,7 @@ cudaError_t run_fp8(const Fp8Args& a) {
     cudaFuncAttributes fa{};
     const cudaError_t r = cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
     if (r != cudaSuccess) return r;
-    if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
+    if (fa.numRegs != F8Shape<BN>::kLaunchRegs) return cudaErrorNotSupported;
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::bytes(Mode == Fp8Mode::kDense ? 0 : kMaxFp8Experts));
   });
@@ -863,8 +965,9 @@ cudaError_t run_fp8(const Fp8Args& a) {
                            ? (a.M / kRowsPerCta + std::min(a.count, a.M)) * p.n_blocks
                            : tiles;
   if (most > (1 << 30)) return cudaErrorInvalidConfiguration;  // tile numbers are 32-bit
-  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(most, a.sm_count));
-  e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kTcThreads),
+  const int64_t room = static_cast<int64_t>(a.sm_count) * F8Shape<BN>::kCtasPerSm;
+  const int64_t ctas = std::max<int64_t>(1, std::min(most, room));
+  e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(F8Shape<BN>::kThreads),
                        static_cast<size_t>(L::bytes(p.count)), a.stream, ta, tb, td, tsa, p);
   count_launches(1);
   return e;
@@ -877,8 +980,8 @@ cudaError_t run_shape(const Fp8Args& a) {
       Mode == Fp8Mode::kRows ? a.M / 128 + std::min(a.count, a.M) : (a.M + 127) / 128;
   const int64_t wide_tiles =
       row_blocks * ((a.N + 255) / 256) * (Mode == Fp8Mode::kK ? a.count : 1);
-  if (wide_tiles >= a.sm_count) return run_fp8<Mode, 256, 4, ColScale>(a);
-  return run_fp8<Mode, 128, 5, ColScale>(a);
+  if (wide_tiles >= a.sm_count) return run_fp8<Mode, 256, 3, ColScale>(a);
+  return run_fp8<Mode, 128, ColScale ? 2 : 3, ColScale>(a);
 }
 
 }  // namespace

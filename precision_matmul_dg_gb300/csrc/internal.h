@@ -301,7 +301,7 @@ cudaError_t launch_fp8_tc(const Fp8Args& a);      // fp8_gemm.cu: tcgen05
 cudaError_t launch_fp8_skinny(const Fp8Args& a);  // fp8_skinny.cu: few rows (dense or kRows)
 constexpr int64_t kFp8SkinnyRows = 16;
 constexpr int64_t kMaxExperts = 1024;    // of a sort
-constexpr int64_t kMaxFp8Experts = 512;  // of a grouped product
+constexpr int64_t kMaxFp8Experts = 384;  // of a grouped product
 
 // Expert routing (moe.cu).
 struct MoeSortJob {
