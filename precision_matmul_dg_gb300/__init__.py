@@ -602,14 +602,24 @@ def gemm_host(A, B, D, C=None, K=None, bias=None, alpha=1.0, beta=0.0, epilogue=
 # ------------------------------------------------- FP8 and expert routing
 
 _FP = None  # (torch, {16-bit and 32-bit float dtype: code}), built on first use
+_raw_stream = None
 
 
 def _fp():
-    global _FP
+    global _FP, _raw_stream
     if _FP is None:
         import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _FP = (torch, {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
     return _FP
+
+
+def _stream_of(t, stream):
+    """The handle of `stream`, by default the current one of t's device (as
+    torch.cuda.current_stream, whose Stream object costs more than a launch)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream_handle(stream)
 
 
 def _float_code(t, what, kinds=(F16, BF16)):
@@ -621,10 +631,14 @@ def _float_code(t, what, kinds=(F16, BF16)):
 
 
 def _rows(t, dtype, what, shape=None, dim=2):
-    """Checks a tensor's type, dimensions, unit last stride and (where given) shape."""
+    """The strides of t, which must be on the GPU, of this type, of `dim`
+    dimensions with unit last stride and (where given) of this shape."""
+    s = t.stride()
+    if t.dtype is dtype and t.is_cuda and len(s) == dim and s[-1] == 1 and (
+            shape is None or t.shape == shape):
+        return s
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    s = t.stride()
     if len(s) != dim or (s[-1] != 1 and t.shape[-1] > 1 and t.numel()):
         raise ValueError("%s must be %d-D with unit last stride" % (what, dim))
     if shape is not None and t.shape != shape:
@@ -680,7 +694,7 @@ def quantize_fp8(X, form="rows", block_rows=1, out=None, stream=None):
     elif form == "transposed":
         args = none + args
     _check(lib().dg_quantize_fp8(rows, K, code, X.data_ptr(), sx[0], block_rows, *args,
-                                 _stream_handle(stream)))
+                                 _stream_of(X, stream)))
     return out
 
 
@@ -712,7 +726,7 @@ def gemm_fp8(A, scale_a, B, scale_b, D, bias=None, alpha=1.0, beta=0.0, epilogue
         M, N, K, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[0],
         scale_b.data_ptr(), zb[0], 1 if nb == N else 128, D.data_ptr(), dt, sd[0],
         None if bias is None else bias.data_ptr(), alpha, beta, _epi_code(epilogue),
-        _stream_handle(stream)))
+        _stream_of(D, stream)))
     return D
 
 
@@ -746,7 +760,7 @@ def gemm_fp8_grouped(A, scale_a, B, scale_b, offsets, D, bias=None, alpha=1.0, b
         count, rows, N, K, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[1],
         sb[0], scale_b.data_ptr(), zb[1], zb[0], offsets.data_ptr(), D.data_ptr(), dt, sd[0],
         None if bias is None else bias.data_ptr(), stride_bias, alpha, beta, _epi_code(epilogue),
-        _stream_handle(stream)))
+        _stream_of(D, stream)))
     return D
 
 
@@ -773,7 +787,7 @@ def gemm_fp8_grouped_wgrad(A, scale_a, B, scale_b, offsets, D, alpha=1.0, beta=0
     _check(lib().dg_gemm_fp8_grouped_wgrad(
         count, M, N, rows, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[0],
         scale_b.data_ptr(), zb[0], offsets.data_ptr(), D.data_ptr(), dt, sd[1], sd[0], alpha, beta,
-        _stream_handle(stream)))
+        _stream_of(D, stream)))
     return D
 
 
@@ -810,7 +824,7 @@ def moe_sort(ids, count, align=1, out=None, stream=None):
         raise ValueError("offsets must be [count + 1], slot_row contiguous like ids")
     _check(lib().dg_moe_sort(tokens, top_k, count, ids.data_ptr(), align, row_slot.shape[0],
                              offsets.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
-                             _stream_handle(stream)))
+                             _stream_of(ids, stream)))
     return out
 
 
@@ -827,7 +841,7 @@ def moe_dispatch(X, row_slot, top_k, D, stream=None):
     sd = _rows(D, X.dtype, "D", (rows, width))
     _check(lib().dg_moe_dispatch(tokens, top_k, width, code, X.data_ptr(), sx[0], rows,
                                  row_slot.data_ptr(), D.data_ptr(), sd[0],
-                                 _stream_handle(stream)))
+                                 _stream_of(X, stream)))
     return D
 
 
@@ -844,7 +858,7 @@ def moe_dispatch_fp8(X, row_slot, top_k, codes, scales, stream=None):
     ss = _rows(scales, torch.float32, "scales", (rows, (width + 127) // 128))
     _check(lib().dg_moe_dispatch_fp8(tokens, top_k, width, code, X.data_ptr(), sx[0], rows,
                                      row_slot.data_ptr(), codes.data_ptr(), sq[0],
-                                     scales.data_ptr(), ss[0], _stream_handle(stream)))
+                                     scales.data_ptr(), ss[0], _stream_of(X, stream)))
     return codes, scales
 
 
@@ -866,7 +880,7 @@ def moe_combine(Y, slot_row, D, weights=None, stream=None):
     _check(lib().dg_moe_combine(tokens, top_k, width, code, Y.data_ptr(), sy[0], Y.shape[0],
                                 slot_row.data_ptr(),
                                 None if weights is None else weights.data_ptr(), D.data_ptr(),
-                                sd[0], _stream_handle(stream)))
+                                sd[0], _stream_of(Y, stream)))
     return D
 
 
@@ -901,7 +915,7 @@ def moe_combine_backward(dD, Y, slot_row, row_slot, weights, dY, dweights=None, 
         tokens, top_k, width, code, dD.data_ptr(), s_dd[0],
         None if dweights is None else Y.data_ptr(), s_y[0], rows, row_slot.data_ptr(),
         slot_row.data_ptr(), None if weights is None else weights.data_ptr(), dY.data_ptr(),
-        s_dy[0], None if dweights is None else dweights.data_ptr(), _stream_handle(stream)))
+        s_dy[0], None if dweights is None else dweights.data_ptr(), _stream_of(dD, stream)))
     return dY, dweights
 
 
