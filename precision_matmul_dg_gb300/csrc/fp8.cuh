@@ -56,6 +56,24 @@ __device__ __forceinline__ uint32_t e4m3x4(float v0, float v1, float v2, float v
   return out;
 }
 
+// Quotients rounded to nearest, for a in [kFloor, 2^100): the quotient by an
+// approximate reciprocal, corrected by its remainder, which one FMA gives
+// exactly (P. Markstein, Computation of elementary functions on the IBM RISC
+// System/6000 processor, 1990).  The general division takes a tenth of the row
+// kernel's time.
+__device__ __forceinline__ float over_top(float a) {  // a / 448
+  constexpr float c = 1.0f / kTop;
+  const float q = a * c;
+  return fmaf(fmaf(-q, kTop, a), c, q);
+}
+__device__ __forceinline__ float top_over(float a) {  // 448 / a
+  float f;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(f) : "f"(a));
+  f = fmaf(fmaf(-a, f, 1.0f), f, f);
+  const float q = kTop * f;
+  return fmaf(fmaf(-q, a, kTop), f, q);
+}
+
 // What quantizes a block: its scale and the factor that its values take.  A
 // block with an infinity or a NaN has the scale NaN and codes 0.
 struct BlockScale {
@@ -67,8 +85,13 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
   BlockScale b;
   b.bad = amax_bits >= T::kInf;
   const float amax = fmaxf(T::one(b.bad ? 0u : amax_bits), kFloor);
-  b.factor = __fdiv_rn(kTop, amax);
-  b.scale = b.bad ? CUDART_NAN_F : __fdiv_rn(amax, kTop);
+  b.factor = top_over(amax);
+  b.scale = over_top(amax);
+  if (amax >= 0x1p100f) {  // the reciprocal nears the subnormal range
+    b.factor = __fdiv_rn(kTop, amax);
+    b.scale = __fdiv_rn(amax, kTop);
+  }
+  if (b.bad) b.scale = CUDART_NAN_F;
   return b;
 }
 

@@ -58,7 +58,7 @@ __device__ __forceinline__ void store_codes16(const uint32_t (&w)[8], const Bloc
   const uint32_t lo[4] = {w[0], w[1], w[2], w[3]}, hi[4] = {w[4], w[5], w[6], w[7]};
   const uint2 c0 = quantize8<T>(lo, b), c1 = quantize8<T>(hi, b);
   if (n >= 16) {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(c0.x, c0.y, c1.x, c1.y);
+    __stcs(reinterpret_cast<uint4*>(dst), make_uint4(c0.x, c0.y, c1.x, c1.y));
   } else {
     const uint32_t c[4] = {c0.x, c0.y, c1.x, c1.y};
 #pragma unroll
@@ -145,8 +145,11 @@ __global__ void __launch_bounds__(kThreads)
 // (of the respective form's rows) or one block for the whole tile.  Thread t
 // reads 16 values of rows t / 8 + 32 i, makes their row-form codes, and puts
 // them in shared memory; then it takes two columns and a quarter of the rows
-// for the transposed form, whose 32 bytes per column go out as whole sectors.
-constexpr int kPitch = kBlock + 8;  // 16-bit elements per shared row
+// for the transposed form, whose codes go back through shared memory and out
+// as whole 128-byte lines.
+constexpr int kPitch = kBlock + 8;       // 16-bit elements per shared row
+constexpr int kCodePitch = kBlock + 16;  // bytes per shared column of codes
+static_assert(kBlock * kCodePitch <= kBlock * kPitch * 2, "the codes take the tile's place");
 
 struct TileParams {
   const uint16_t* X;
@@ -249,30 +252,41 @@ __global__ void __launch_bounds__(kThreads)
     o[0][q] = s[0].bad ? 0u : e4m3x4(v[0].x * f0, v[1].x * f0, v[2].x * f0, v[3].x * f0);
     o[1][q] = s[1].bad ? 0u : e4m3x4(v[0].y * f1, v[1].y * f1, v[2].y * f1, v[3].y * f1);
   }
-  const int64_t rr = r0 + part * 32;  // first of the 32 rows, a position along the output's rows
+  // through shared memory, so that eight lanes write a column's 128 bytes
+  __syncthreads();  // the tile has been read
+  uint8_t* ct_smem = reinterpret_cast<uint8_t*>(tile);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t c = c0 + 2 * pair + h;
-    if (c >= p.K) break;
-    uint8_t* dst = p.codes_t + c * p.ldqt + rr;
-    if (rr + 32 <= p.rows) {
-      reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[h][0], o[h][1], o[h][2], o[h][3]);
-      reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[h][4], o[h][5], o[h][6], o[h][7]);
-    } else {
+    const int c = 2 * pair + h;
+    uint4* d = reinterpret_cast<uint4*>(ct_smem + c * kCodePitch + part * 32);
+    d[0] = make_uint4(o[h][0], o[h][1], o[h][2], o[h][3]);
+    d[1] = make_uint4(o[h][4], o[h][5], o[h][6], o[h][7]);
+    if (!p.whole && part == 0 && c0 + c < p.K) p.scales_t[(c0 + c) * p.ldst + rt] = s[h].scale;
+  }
+  __syncthreads();
+  const int64_t rr = r0 + sub * 16;  // a position along the output's rows
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (rr + i < p.rows) dst[i] = static_cast<uint8_t>(o[h][i >> 2] >> (8 * (i & 3)));
+  for (int i = 0; i < 4; ++i) {
+    const int c = (t >> 3) + 32 * i;
+    if (c0 + c >= p.K || rr >= p.rows) break;
+    const uint4 v = *reinterpret_cast<const uint4*>(ct_smem + c * kCodePitch + sub * 16);
+    uint8_t* dst = p.codes_t + (c0 + c) * p.ldqt + rr;
+    if (rr + 16 <= p.rows) {
+      __stcs(reinterpret_cast<uint4*>(dst), v);
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (rr + k < p.rows) dst[k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
     }
-    if (!p.whole && part == 0) p.scales_t[c * p.ldst + rt] = s[h].scale;
   }
   if (p.whole && t == 0) p.scales_t[ct * p.ldst + rt] = s[0].scale;
 }
 
 template <typename T>
 cudaError_t rows_launch(const RowParams& p, bool gather, dim3 grid, cudaStream_t stream) {
-  return gather ? launch_dependent(quantize_rows_kernel<T, true>, grid, dim3(kThreads), 0, stream, p)
-                : launch_dependent(quantize_rows_kernel<T, false>, grid, dim3(kThreads), 0, stream,
-                                   p);
+  auto kern = gather ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>;
+  return launch_dependent(kern, grid, dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace

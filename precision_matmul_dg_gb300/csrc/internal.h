@@ -252,6 +252,10 @@ struct Fp8RowsJob {
   int64_t top_k = 1, tokens = 0;
 };
 cudaError_t launch_quantize_fp8_rows(const Fp8RowsJob& j, cudaStream_t stream, int sm_count);
+// The gather of rows quantized before (codes, pitch ldx; scales, one row of
+// ceil(K / 128) per token) into j's outputs (moe.cu).
+cudaError_t launch_moe_dispatch_codes(const Fp8RowsJob& j, const void* codes, int64_t ldx,
+                                      const float* scales, cudaStream_t stream, int sm_count);
 struct Fp8TilesJob {
   bool bf16;
   const void* X;
@@ -346,6 +350,9 @@ struct CallContext {
   int sm_count;
 };
 dg_status call_context(CallContext* out);
+// Scratch of at least `bytes` bytes on (device, stream), shared with the
+// widened operands: for data that the same call writes and reads.
+dg_status get_scratch(int dev, cudaStream_t stream, int64_t bytes, void** out);
 
 // Kernel-launch counter and error state (api.cu).  None of these allocate.
 void count_launches(int n);

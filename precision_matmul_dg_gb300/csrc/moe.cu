@@ -17,14 +17,15 @@ using namespace fp8;
 // ---------------------------------------------------------------------------
 // The slots are cut into one contiguous run per CTA of the cluster and those
 // into one run per warp, so that (CTA, warp, position) is slot order and the
-// result is stable without any atomic:
-//   1. each warp counts its run by expert, 32 slots at a time: lanes with the
-//      same expert find each other (match) and the lowest adds their number
-//      to the warp's own row of counters;
+// result is stable whatever the timing:
+//   1. each warp counts its run by expert in its own row of counters;
 //   2. per expert, the warps' counts become running sums; the CTAs exchange
 //      their totals through distributed shared memory, and every CTA computes
 //      the segments' starts;
-//   3. each warp walks its run again and gives each slot its row.
+//   3. each warp walks its run again, 32 slots at a time: lanes with the same
+//      expert find each other with one ballot per bit of its number (a match
+//      instruction takes longer: 131 thousand slots 31 us, with ballots 15) and
+//      take the rows from the expert's running count on, in lane order.
 // Bound by latency: the slots are read twice (8 bytes) and written once, a
 // few hundred kilobytes at most.
 constexpr int kSortThreads = 1024;
@@ -35,6 +36,8 @@ struct SortParams {
   const int32_t* ids;
   int slots, count, align_mask;  // align - 1
   int per_warp;                  // slots per warp, a multiple of 32
+  int warps;                     // per CTA that get slots
+  int bits;                      // of an expert's number
   int64_t rows;
   int32_t *offsets, *row_slot, *slot_row;
 };
@@ -45,7 +48,34 @@ __device__ __forceinline__ int ld_cluster_int(uint32_t addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const __grid_constant__ SortParams p) {
+// The experts of slots s, s + 32, ...: -1 past `last` and where the choice is
+// dropped.  All loads are under way before the first is used.
+constexpr int kSortAhead = 8;
+__device__ __forceinline__ void load_experts(const SortParams& p, int s, int last,
+                                             int (&e)[kSortAhead]) {
+#pragma unroll
+  for (int i = 0; i < kSortAhead; ++i) e[i] = s + 32 * i < last ? __ldg(p.ids + s + 32 * i) : -1;
+#pragma unroll
+  for (int i = 0; i < kSortAhead; ++i)
+    if (e[i] >= p.count) e[i] = -1;
+#pragma unroll
+  for (int i = 0; i < kSortAhead; ++i) e[i] = max(e[i], -1);
+}
+
+// The lanes whose expert is this lane's (-1 is no expert's number: its bits are
+// those of the last, its sign sets it apart).
+__device__ __forceinline__ unsigned same_lanes(int e, int bits) {
+  unsigned m = __ballot_sync(0xffffffffu, e < 0);
+  m = e < 0 ? m : ~m;
+  for (int b = 0; b < bits; ++b) {
+    const unsigned set = __ballot_sync(0xffffffffu, (e >> b) & 1);
+    m &= (e >> b) & 1 ? set : ~set;
+  }
+  return m;
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    moe_sort_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ int sort_smem[];
   const int count = p.count;
   int* totals = sort_smem;                // [count]: this CTA's slots per expert
@@ -56,29 +86,36 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const __grid_con
   __shared__ int warp_sum[kSortWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
-  for (int i = threadIdx.x; i < kSortWarps * count; i += kSortThreads) hist[i] = 0;
+  for (int i = threadIdx.x; i < p.warps * count; i += kSortThreads) hist[i] = 0;
   __syncthreads();
   grid_dependency_wait();
 
-  const int64_t first64 = (static_cast<int64_t>(rank) * kSortWarps + warp) * p.per_warp;
-  const int first = static_cast<int>(first64 < p.slots ? first64 : p.slots);
-  const int last = static_cast<int>(first64 + p.per_warp < p.slots ? first64 + p.per_warp : p.slots);
+  const int64_t first64 = (static_cast<int64_t>(rank) * p.warps + warp) * p.per_warp;
+  const int first = static_cast<int>(warp < p.warps && first64 < p.slots ? first64 : p.slots);
+  const int64_t last64 = first64 + p.per_warp;
+  const int last = static_cast<int>(last64 < p.slots ? last64 : p.slots);
   int* mine = hist + warp * count;
-  for (int s0 = first; s0 < last; s0 += 32) {
-    const int s = s0 + lane;
-    int e = s < last ? __ldg(p.ids + s) : -1;
-    if (e < 0 || e >= count) e = -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
+  for (int s0 = first; s0 < last; s0 += 32 * kSortAhead) {
+    int e[kSortAhead];
+    load_experts(p, s0 + lane, last, e);
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) {
+      if (s0 + 32 * i >= last) break;
+      if (e[i] >= 0) atomicAdd(&mine[e[i]], 1);  // a count: the order does not matter
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < count; e += kSortThreads) {
     int sum = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = hist[w * count + e];
-      hist[w * count + e] = sum;
-      sum += c;
+    for (int w0 = 0; w0 < p.warps; w0 += 8) {
+      int c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = w0 + i < p.warps ? hist[(w0 + i) * count + e] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (w0 + i < p.warps) hist[(w0 + i) * count + e] = sum;
+        sum += c[i];
+      }
     }
     totals[e] = sum;
   }
@@ -128,20 +165,24 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const __grid_con
   cluster_arrive_release();
   __syncthreads();
 
-  for (int s0 = first; s0 < last; s0 += 32) {
-    const int s = s0 + lane;
-    int e = s < last ? __ldg(p.ids + s) : -1;
-    if (e < 0 || e >= count) e = -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const unsigned below = same & ((1u << lane) - 1u);
-    int row = -1;
-    if (e >= 0) row = start[e] + mine[e] + __popc(below);
-    __syncwarp();
-    if (e >= 0 && below == 0) mine[e] += __popc(same);
-    __syncwarp();
-    if (s < last) {
-      p.slot_row[s] = row;
-      if (row >= 0) p.row_slot[row] = s;
+  for (int s0 = first; s0 < last; s0 += 32 * kSortAhead) {
+    int e[kSortAhead];
+    load_experts(p, s0 + lane, last, e);
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) {
+      const int s = s0 + 32 * i + lane;
+      if (s0 + 32 * i >= last) break;
+      const unsigned same = same_lanes(e[i], p.bits);
+      const unsigned below = same & ((1u << lane) - 1u);
+      int row = -1;
+      if (e[i] >= 0) row = start[e[i]] + mine[e[i]] + __popc(below);
+      __syncwarp();
+      if (e[i] >= 0 && below == 0) mine[e[i]] += __popc(same);
+      __syncwarp();
+      if (s < last) {
+        p.slot_row[s] = row;
+        if (row >= 0) p.row_slot[row] = s;
+      }
     }
   }
   // -1 in the padding of each segment and past the last one
@@ -149,8 +190,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const __grid_con
     for (int e = rank * kSortWarps + warp; e < count; e += ctas * kSortWarps)
       for (int r = offs[e] + seg[e] + lane; r < offs[e + 1]; r += 32) p.row_slot[r] = -1;
   }
-  for (int64_t r = offs[count] + static_cast<int64_t>(rank) * kSortThreads + threadIdx.x; r < p.rows;
-       r += static_cast<int64_t>(ctas) * kSortThreads)
+  const int64_t all_threads = static_cast<int64_t>(ctas) * kSortThreads;
+  for (int64_t r = offs[count] + rank * kSortThreads + threadIdx.x; r < p.rows; r += all_threads)
     p.row_slot[r] = -1;
   cluster_wait_acquire();
 }
@@ -172,9 +213,12 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, int n) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Rows are written once and read by a later kernel: a streaming store leaves
+// L2 to the rows that are read again (4096 tokens to 16384 rows of 2048: 21.8
+// us, 27.4 with plain stores).
 __device__ __forceinline__ void store8(uint16_t* p, const uint4& v, int n) {
   if (n >= 8) {
-    *reinterpret_cast<uint4*>(p) = v;
+    __stcs(reinterpret_cast<uint4*>(p), v);
     return;
   }
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -215,7 +259,8 @@ struct RowsParams {
 };
 
 // D[r] = X[row_slot[r] / top_k], zeros without a slot: a warp per row.
-__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kRowThreads)
+    dispatch_kernel(const __grid_constant__ RowsParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -234,13 +279,61 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_cons
   }
 }
 
+// codes[r], scales[r] = those of X's row row_slot[r] / top_k (codes 0 and the
+// scale of an empty block without a slot): a warp per row.
+struct CodesParams {
+  const uint8_t* X;  // codes of the tokens, pitch ldx bytes, a multiple of 16
+  int64_t ldx;
+  const float* sx;  // [tokens][blocks]
+  uint8_t* D;
+  int64_t ldd;
+  float* sd;
+  int64_t lds;
+  const int32_t* row_slot;
+  int64_t tokens, rows;
+  int top_k, width, blocks;
+};
+
+__global__ void __launch_bounds__(kRowThreads)
+    dispatch_codes_kernel(const __grid_constant__ CodesParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kRowThreads / 32);
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+       r < p.rows; r += step) {
+    const int slot = __ldg(p.row_slot + r);
+    const int t = slot < 0 ? -1 : static_cast<int>(static_cast<unsigned>(slot) / p.top_k);
+    const bool there = t >= 0 && t < p.tokens;
+    const uint8_t* src = p.X + (there ? t * p.ldx : 0);
+    uint8_t* dst = p.D + r * p.ldd;
+#pragma unroll 4
+    for (int k = lane * 16; k < p.width; k += 512) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (there) v = *reinterpret_cast<const uint4*>(src + k);  // written by the kernel before
+      if (k + 16 <= p.width) {
+        __stcs(reinterpret_cast<uint4*>(dst + k), v);
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (k + i < p.width) dst[k + i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+      }
+    }
+    for (int b = lane; b < p.blocks; b += 32)
+      p.sd[r * p.lds + b] =
+          there ? p.sx[static_cast<int64_t>(t) * p.blocks + b] : __fdiv_rn(kFloor, kTop);
+  }
+}
+
 // D[t] = sum over j of weights[t, j] * Y[slot_row[t, j]]: a thread takes eight
 // columns of one token and loads kInFlight of its rows at a time; FP32 sums
 // in the order of j.
 constexpr int kInFlight = 8;
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kRowThreads)
+    combine_kernel(const __grid_constant__ RowsParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
@@ -382,13 +475,18 @@ cudaError_t launch_moe_sort(const MoeSortJob& j, cudaStream_t stream) {
   p.offsets = j.offsets;
   p.row_slot = j.row_slot;
   p.slot_row = j.slot_row;
-  // one CTA for each 4096 slots (128 per warp), up to the cluster's eight
-  const int64_t want = (static_cast<int64_t>(p.slots) + 4095) / 4096;
+  // one CTA for each 2048 slots (64 per warp), up to the cluster's eight; a
+  // warp takes at least 32
+  const int64_t want = (static_cast<int64_t>(p.slots) + 2047) / 2048;
   int ctas = 1;
   while (ctas < kSortMaxCtas && ctas < want) ctas *= 2;
-  const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
-  const int64_t per_warp = ((p.slots + warps - 1) / warps + 31) / 32 * 32;
-  p.per_warp = static_cast<int>(per_warp > 0 ? per_warp : 32);
+  const int64_t per_cta = (static_cast<int64_t>(p.slots) + ctas - 1) / ctas;
+  const int64_t steps = ((per_cta + kSortWarps - 1) / kSortWarps + 31) / 32;
+  const int64_t per_warp = std::max<int64_t>(1, steps) * 32;
+  p.per_warp = static_cast<int>(per_warp);
+  p.bits = 0;
+  while ((1 << p.bits) < j.count) ++p.bits;
+  p.warps = static_cast<int>(std::max<int64_t>(1, (per_cta + per_warp - 1) / per_warp));
 
   int dev = 0;
   cudaGetDevice(&dev);
@@ -423,6 +521,31 @@ cudaError_t launch_moe_dispatch(const MoeRowsJob& j, cudaStream_t stream, int sm
   const int64_t cap = static_cast<int64_t>(sm_count) * 8 * 4;
   const cudaError_t e =
       launch_dependent(dispatch_kernel, dim3(static_cast<unsigned>(std::min(ctas, cap))),
+                       dim3(kRowThreads), 0, stream, p);
+  count_launches(1);
+  return e;
+}
+
+cudaError_t launch_moe_dispatch_codes(const Fp8RowsJob& j, const void* codes, int64_t ldx,
+                                      const float* scales, cudaStream_t stream, int sm_count) {
+  CodesParams p;
+  p.X = static_cast<const uint8_t*>(codes);
+  p.ldx = ldx;
+  p.sx = scales;
+  p.D = static_cast<uint8_t*>(j.codes);
+  p.ldd = j.ldq;
+  p.sd = j.scales;
+  p.lds = j.lds;
+  p.row_slot = j.row_slot;
+  p.tokens = j.tokens;
+  p.rows = j.rows;
+  p.top_k = static_cast<int>(j.top_k);
+  p.width = static_cast<int>(j.K);
+  p.blocks = static_cast<int>((j.K + kBlock - 1) / kBlock);
+  const int64_t ctas = (j.rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
+  const int64_t cap = static_cast<int64_t>(sm_count) * 8 * 4;
+  const cudaError_t e =
+      launch_dependent(dispatch_codes_kernel, dim3(static_cast<unsigned>(std::min(ctas, cap))),
                        dim3(kRowThreads), 0, stream, p);
   count_launches(1);
   return e;

@@ -90,6 +90,20 @@ def test_quantize_special_values(dg, dtype):
         assert np.array_equal(codes_of(row[0]), codes_of(got[0]))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_quantize_every_largest_value(dg, dtype):
+    # a block for every finite magnitude: scales and factors are the rounded quotients
+    bits = np.arange(0, 0x7C00 if dtype == "f16" else 0x7F80).astype(np.uint16)
+    x = torch.from_numpy(bits.view(np.int16)).view(TYPES[dtype])
+    rows = torch.zeros(len(bits), 128, dtype=x.dtype)
+    rows[:, 5] = x
+    rows[:, 77] = -x * 0.7
+    got = dg.quantize_fp8(rows.cuda())
+    want = ref.quantize(rows.double().numpy())
+    assert np.array_equal(got[1].cpu().numpy(), want[1])
+    assert np.array_equal(ref.VALUES[codes_of(got[0])], ref.VALUES[want[0]])
+
+
 def test_quantize_smallest_bf16(dg):
     x = torch.full((2, 128), 1e-39, dtype=torch.bfloat16)
     x[1] = 3e38
