@@ -251,7 +251,7 @@ dg_status dg_gemm_fp8_grouped(int64_t count, int64_t rows, int64_t N, int64_t K,
   a.beta = beta;
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   fill_context(&a, c);
-  return launched(rows <= kFp8SkinnyRows * count || K == 0 ? launch_fp8_skinny(a)
+  return launched(rows <= kFp8SkinnyRowsEach * count || K == 0 ? launch_fp8_skinny(a)
                                                            : launch_fp8_tc(a),
                   "kernel launch");
 }

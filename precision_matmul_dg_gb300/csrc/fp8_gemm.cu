@@ -55,7 +55,12 @@ namespace {
 
 using namespace fp8;
 
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168, kSumRegs = 216, kOtherRegs = 72;  // per thread
+static_assert(2 * kSumRegs + kOtherRegs == 3 * kLaunchRegs, "shares of the launch's registers");
 constexpr int kScaleGroup = 4;  // K blocks (of one number / 4) whose scales are staged together
+constexpr int kSumWarps = 8;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10;
 constexpr int kRowsPerCta = 128;  // TMEM lanes
 constexpr int kStageA = kRowsPerCta * 128;
 constexpr int kRowScaleBytes = kRowsPerCta * kScaleGroup * 4;
@@ -63,6 +68,7 @@ constexpr int kRowScaleBytes = kRowsPerCta * kScaleGroup * 4;
 struct F8Params {
   int M, N;  // kRows: M rows in all
   int m_blocks, n_blocks, k_blocks;
+  int split, split_blocks;  // Split: CTAs per tile, and K blocks of each (whole scale groups)
   int tiles;  // kDense, kK
   int group_m, count;
   int b_rows;  // rows of B's map from one expert to the next
@@ -85,27 +91,8 @@ struct F8Params {
   uint64_t timeout_ns;
 };
 
-// The two shapes of a CTA: 128 x 256 tiles, two warpgroups of sum warps and a
-// third for the rest, alone on its SM; or 128 x 128 tiles, one and one, two
-// CTAs to an SM.  A sum thread takes 128 columns of a row either way.
-template <int BN>
-struct F8Shape {
-  static_assert(BN == 128 || BN == 256, "tile width");
-  static constexpr int kSumWarps = BN / 32;
-  static constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kScaleWarp = kSumWarps + 2;
-  static constexpr int kThreads = (kSumWarps + 4) * 32;
-  static constexpr int kCtasPerSm = BN == 256 ? 1 : 2;
-  // registers per thread: at launch, and as the warpgroups share them
-  static constexpr int kLaunchRegs = BN == 256 ? 168 : 128;
-  static constexpr int kSumRegs = BN == 256 ? 216 : 200;
-  static constexpr int kOtherRegs = BN == 256 ? 72 : 56;
-  static_assert(kSumWarps / 4 * kSumRegs + kOtherRegs == (kSumWarps / 4 + 1) * kLaunchRegs,
-                "shares of the launch's registers");
-};
-
 template <int BN, int Stages, bool ColScale>
 struct F8Smem {
-  static constexpr int kSumWarps = F8Shape<BN>::kSumWarps;
   static constexpr int kTileB = BN * 128;
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + Stages * kStageA;
@@ -113,14 +100,14 @@ struct F8Smem {
   // D's boxes, kBoxes to a sum warp: 32 rows of 128 bytes where there is room.
   // (A fourth stage of 128 x 256 tiles would leave room for one box of 64-byte
   // rows: 8192^3 476 us against 466, the experts' FP32 gradients 762 against 694.)
-  static constexpr int kBoxRow = BN == 256 ? 128 : 64;
+  static constexpr int kBoxRow = 128;
   static constexpr int kBoxes = BN == 256 ? 2 : 1;
   static constexpr int kBoxBytes = 32 * kBoxRow;
   static constexpr int kOffRow = kOffBox + kSumWarps * kBoxes * kBoxBytes;  // [2][128][4]
   static constexpr int kOffCol = kOffRow + 2 * kRowScaleBytes;
   // column scales [2][4][BN]
   static constexpr int kOffBar = kOffCol + (ColScale ? 2 * kScaleGroup * BN * 4 : 0);
-  static constexpr int kBufs = 2;
+  static constexpr int kBufs = 512 / BN;
   static constexpr int kBars = 2 * Stages + 2 * kBufs + 1 + 4;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
   static constexpr int kOffAbort = kOffSlot + 4;
@@ -131,9 +118,7 @@ struct F8Smem {
   static constexpr int bytes(int64_t count) {
     return kFixed + static_cast<int>(count > 0 ? (ColScale ? 1 : 2) * (count + 1) * 4 : 0);
   }
-  // an SM has 228 KB, of which each CTA costs 1 KB
-  static_assert(bytes(kMaxFp8Experts) <= (228 / F8Shape<BN>::kCtasPerSm - 1) * 1024,
-                "shared memory of a CTA");
+  static_assert(bytes(kMaxFp8Experts) <= 227 * 1024, "shared memory of a CTA");
 };
 
 // A tile: rows row0 .. row0 + rows - 1 of A and D, columns from n0, K blocks
@@ -143,12 +128,12 @@ struct F8Tile {
 };
 
 struct F8Walk {
-  int t, expert;
+  int t, expert, rank;  // rank: the CTA's share of K (Split)
 };
 
 // The CTA's next tile; false past its last.  `off` and `pre` are the experts'
 // row offsets and running row block counts (kRows), off the K blocks (kK).
-template <Fp8Mode Mode, int BN>
+template <Fp8Mode Mode, int BN, bool Split>
 __device__ __forceinline__ bool next_tile(F8Walk& w, const F8Params& p, const int* off,
                                           const int* pre, F8Tile& o) {
   if (Mode == Fp8Mode::kRows) {
@@ -176,12 +161,16 @@ __device__ __forceinline__ bool next_tile(F8Walk& w, const F8Params& p, const in
       o.kb0 = off[o.expert];
       o.kb1 = max(off[o.expert + 1], o.kb0);
     }
+    if (Split) {
+      o.kb0 = min(w.rank * p.split_blocks, p.k_blocks);
+      o.kb1 = min(o.kb0 + p.split_blocks, p.k_blocks);
+    }
     tc::tile_coords(local, p.m_blocks, p.n_blocks, p.group_m, m, nb);
     o.row0 = m * kRowsPerCta;
     o.rows = min(kRowsPerCta, p.M - o.row0);
     o.n0 = nb * BN;
   }
-  w.t += static_cast<int>(gridDim.x);
+  w.t += Split ? p.tiles : static_cast<int>(gridDim.x);  // a split tile is the CTA's only one
   return true;
 }
 
@@ -370,6 +359,15 @@ __device__ __forceinline__ void finish16(float (&v)[16], const F8Params& p, int6
   }
 }
 
+__device__ __forceinline__ float4 ld_cluster_float4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t x,
                                              int32_t y, int32_t z) {
   asm volatile(
@@ -387,15 +385,18 @@ __device__ __forceinline__ uint32_t box_offset(int r, int q) {
                                           : r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
 }
 
-// Sends a box (this warp's 32 rows, Row bytes from column col0 on) to D (of the
-// stack's matrix z): by TMA where all 32 rows are D's, else a row in Row / 16
-// lanes.  Either way lane 0 closes one bulk group.
+// Sends a box (this warp's 32 rows, `pieces` of 16 bytes from column col0 on)
+// to D (of the stack's matrix z): by TMA where all 32 rows are D's and the box
+// is full or ends with D, else a row in Row / 16 lanes.  Either way lane 0
+// closes one bulk group.
 template <int Row>
 __device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_t* box,
                                          const F8Params& p, const F8Tile& tile, int row_in_tile,
-                                         int col0, int matrix, int lane) {
+                                         int col0, int pieces, int matrix, int lane) {
   const int left = tile.rows - row_in_tile;  // rows of the box that are D's
-  if (p.tma_d && left >= 32) {
+  const int z = p.dtype_d == DG_F32 ? 4 : 2;
+  const int per = 16 / z;  // columns in 16 bytes
+  if (p.tma_d && left >= 32 && (pieces == Row / 16 || col0 + pieces * per >= p.N)) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -407,14 +408,12 @@ __device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_
   if (lane == 0) bulk_commit_group();
   __syncwarp();
   constexpr int kLanes = Row / 16, kRows = 32 / kLanes;
-  const int z = p.dtype_d == DG_F32 ? 4 : 2;
-  const int per = 16 / z;  // columns in 16 bytes
   const int q = lane % kLanes;
   const int col = col0 + q * per;
 #pragma unroll
   for (int i = 0; i < 32 / kRows; ++i) {
     const int r = i * kRows + lane / kLanes;
-    if (r >= left || col >= p.N) continue;
+    if (r >= left || q >= pieces || col >= p.N) continue;
     const uint4 v = *reinterpret_cast<const uint4*>(box + box_offset<Row>(r, q));
     const int64_t row = tile.row0 + row_in_tile + r;
     uint8_t* d = static_cast<uint8_t*>(p.D) + (matrix * p.stride_d + row * p.ldd + col) * z;
@@ -436,19 +435,16 @@ __device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_
   }
 }
 
-template <Fp8Mode Mode, int BN, int Stages, bool ColScale>
-__global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm)
+template <Fp8Mode Mode, int BN, int Stages, bool ColScale, bool Split>
+__global__ void __launch_bounds__(kThreads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_d,
                     const __grid_constant__ CUtensorMap tmap_sa,
                     const __grid_constant__ F8Params p) {
   using L = F8Smem<BN, Stages, ColScale>;
-  using S = F8Shape<BN>;
-  constexpr int kSumWarps = S::kSumWarps, kTmaWarp = S::kTmaWarp, kMmaWarp = S::kMmaWarp,
-                kScaleWarp = S::kScaleWarp;
   constexpr int kBufs = L::kBufs;
-  constexpr int kHalf = 128;  // columns per sum warp
+  constexpr int kHalf = BN / 2;  // columns per sum warp
   constexpr int kTmemCols = kBufs * BN;
   constexpr uint32_t idesc = idesc_f16_f32(kRowsPerCta, BN);  // operand format 0 is E4M3 here
 
@@ -500,7 +496,7 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
     // Offsets clamped to the rows there are (kK: in K blocks, rounded down).
     const int limit = Mode == Fp8Mode::kRows ? p.M : p.k_rows;
     bool odd = false;
-    for (int e = threadIdx.x; e <= p.count; e += S::kThreads) {
+    for (int e = threadIdx.x; e <= p.count; e += kThreads) {
       const int v = min(max(__ldg(p.offsets + e), 0), limit);
       odd |= Mode == Fp8Mode::kK && (v & (kBlock - 1)) != 0;
       off[e] = Mode == Fp8Mode::kK ? v / kBlock : v;
@@ -528,12 +524,16 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  bool ok = true;
-  F8Walk walk{static_cast<int>(blockIdx.x), 0};
+  bool ok = true, met = false;  // met: the cluster's first barrier (Split)
+  F8Walk walk{static_cast<int>(blockIdx.x), 0, 0};
+  if (Split) {
+    walk.rank = static_cast<int>(cluster_ctarank());
+    walk.t = static_cast<int>(blockIdx.x) / p.split;
+  }
   F8Tile tile;
 
   if (warp >= kSumWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) {
       // ---------------------------------------------------------- producer
       if (elect_one_lane()) {
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
         int stage = 0;
         uint32_t phase = 0;
         int64_t issued = 0;
-        while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
+        while (ok && next_tile<Mode, BN, Split>(walk, p, off, pre, tile)) {
           const int b_row = (Mode == Fp8Mode::kRows ? tile.expert * p.b_rows : 0) + tile.n0;
           for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
             if (!mbar_wait_abortable(&empty_bar[stage], phase ^ 1, p.timeout_ns, p.status,
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
       const uint64_t desc_b = smem_desc_sw128(smem_addr(smem + L::kOffB));
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
-      while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
+      while (ok && next_tile<Mode, BN, Split>(walk, p, off, pre, tile)) {
         for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
           // The operands are usually there before the buffer is: what the
           // buffer's release waits for comes after it, in as few steps as
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
       int64_t groups = 0;
       int g = 0;
       uint32_t g_phase = 0;
-      while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
+      while (ok && next_tile<Mode, BN, Split>(walk, p, off, pre, tile)) {
         // groups lie at multiples of four K blocks: a tile's first may begin
         // before the tile
         for (int kb = tile.kb0 / kScaleGroup * kScaleGroup; kb < tile.kb1; kb += kScaleGroup) {
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
         warp_wait(&scale_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), p, abort_flag);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSumRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     // ---------------------------------------------------- sums and epilogue
     const int in_tile = (warp & 3) * 32, half = warp >> 2;
     const uint32_t src0 =
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
     uint8_t* boxes = smem + L::kOffBox + warp * L::kBoxes * L::kBoxBytes;
     int buf = 0, g = 0, next_box = 0;
     uint32_t buf_phase = 0, g_phase = 0;
-    while (ok && next_tile<Mode, BN>(walk, p, off, pre, tile)) {
+    while (ok && next_tile<Mode, BN, Split>(walk, p, off, pre, tile)) {
       float2 acc[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
         sb = p.sb + (Mode == Fp8Mode::kRows ? tile.expert * p.stride_sb : 0) +
              static_cast<int64_t>(min(tile.n0 + half * kHalf, p.N - 1) / kBlock) * p.lds_b;
       float4 ra, ca, cb;
-      if (!ColScale && tile.kb0 < tile.kb1) load_group(cb, sb, 0, tile.kb1, p.vec_b);
+      if (!ColScale && tile.kb0 < tile.kb1) load_group(cb, sb, tile.kb0, tile.kb1, p.vec_b);
 #pragma unroll 1
       for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
         const int in_group = kb % kScaleGroup;
@@ -760,16 +760,45 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
         }
       }
       if (!ok) break;
+      int first = tile.n0 + half * kHalf, columns = kHalf;  // of D, for this warp to finish
+      if (Split) {
+        // Each CTA's sums go to its own shared memory (its stages are spent:
+        // every MMA has been waited for), and each finishes its share of the
+        // columns, adding the CTAs' sums in the order of K.
+        columns = kHalf / p.split;
+        const int skip = walk.rank * columns;
+        first += skip;
+        float4* mine = reinterpret_cast<float4*>(smem) + warp * (kHalf / 4) * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < kHalf / 4; ++i)
+          mine[i * 32] =
+              make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+        cluster_sync();
+        met = true;
+        const uint32_t share = smem_addr(mine + skip / 4 * 32);
+#pragma unroll
+        for (int i = 0; i < kHalf / 8; ++i) {
+          if (4 * i >= columns) break;
+          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int r = 0; r < p.split; ++r) {
+            const float4 v = ld_cluster_float4(
+                mapa_shared(share + static_cast<uint32_t>(i * 32 * 16), static_cast<uint32_t>(r)));
+            sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+          }
+          acc[2 * i] = make_float2(sum.x, sum.y);
+          acc[2 * i + 1] = make_float2(sum.z, sum.w);
+        }
+      }
       // D, 32 columns at a time; the sums move down so that the loop's body
       // (whose GELU is long) is there once
       const int matrix = Mode == Fp8Mode::kK ? tile.expert : 0;
       const int64_t row = tile.row0 + min(in_tile + lane, tile.rows - 1);
       const int64_t drow = matrix * p.stride_d + row * p.ldd;
       const int64_t bias0 = Mode == Fp8Mode::kRows ? tile.expert * p.stride_bias : 0;
-      const int col_end = tile.rows > in_tile ? min(p.N, tile.n0 + (half + 1) * kHalf) : 0;
+      const int col_end = tile.rows > in_tile ? min(p.N, first + columns) : 0;
       int fill = 0, box_col = 0;  // the open box: 16-byte pieces in it, its first column
 #pragma unroll 1
-      for (int col0 = tile.n0 + half * kHalf; col0 < col_end; col0 += 32) {
+      for (int col0 = first; col0 < col_end; col0 += 32) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int col = col0 + 16 * h;
@@ -806,7 +835,7 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
             fill += 2;
           }
           if (fill == kBoxRow / 16 || col + 16 >= col_end) {
-            send_box<kBoxRow>(&tmap_d, box, p, tile, in_tile, box_col, matrix, lane);
+            send_box<kBoxRow>(&tmap_d, box, p, tile, in_tile, box_col, fill, matrix, lane);
             fill = 0;
             if (++next_box == L::kBoxes) next_box = 0;
           }
@@ -819,6 +848,10 @@ __global__ void __launch_bounds__(F8Shape<BN>::kThreads, F8Shape<BN>::kCtasPerSm
     if (lane == 0) bulk_wait_group<0>();  // this thread's stores end before the CTA does
   }
   __syncwarp();
+  if (Split) {
+    if (!met) cluster_sync();  // the sums are there
+    cluster_sync();            // and have been read
+  }
   tc_fence_before_sync();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -871,8 +904,8 @@ cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int
   return cudaSuccess;
 }
 
-template <Fp8Mode Mode, int BN, int Stages, bool ColScale>
-cudaError_t run_fp8(const Fp8Args& a) {
+template <Fp8Mode Mode, int BN, int Stages, bool ColScale, bool Split = false>
+cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
   using L = F8Smem<BN, Stages, ColScale>;
   // Fewer rows than a tile: only those (whole swizzle atoms of 8) are loaded;
   // the stale shared memory below feeds rows of D that are not there.
@@ -898,6 +931,9 @@ cudaError_t run_fp8(const Fp8Args& a) {
   const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_blocks *
                         (Mode == Fp8Mode::kK ? a.count : 1);
   p.tiles = static_cast<int>(std::min<int64_t>(tiles, INT32_MAX));
+  const int groups = (p.k_blocks + kScaleGroup - 1) / kScaleGroup;
+  p.split = split;
+  p.split_blocks = (groups + split - 1) / split * kScaleGroup;
   p.group_m = 16;
   p.count = Mode == Fp8Mode::kDense ? 0 : static_cast<int>(a.count);
   p.b_rows = static_cast<int>(b_pitch);
@@ -944,7 +980,7 @@ cudaError_t run_fp8(const Fp8Args& a) {
     if (e != cudaSuccess) return e;
   }
 
-  auto kern = gemm_fp8_kernel<Mode, BN, Stages, ColScale>;
+  auto kern = gemm_fp8_kernel<Mode, BN, Stages, ColScale, Split>;
   int dev = 0;
   cudaGetDevice(&dev);
   static std::atomic<uint64_t> attr_set{0};
@@ -954,7 +990,7 @@ cudaError_t run_fp8(const Fp8Args& a) {
     cudaFuncAttributes fa{};
     const cudaError_t r = cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern));
     if (r != cudaSuccess) return r;
-    if (fa.numRegs != F8Shape<BN>::kLaunchRegs) return cudaErrorNotSupported;
+    if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::bytes(Mode == Fp8Mode::kDense ? 0 : kMaxFp8Experts));
   });
@@ -965,15 +1001,29 @@ cudaError_t run_fp8(const Fp8Args& a) {
                            ? (a.M / kRowsPerCta + std::min(a.count, a.M)) * p.n_blocks
                            : tiles;
   if (most > (1 << 30)) return cudaErrorInvalidConfiguration;  // tile numbers are 32-bit
-  const int64_t room = static_cast<int64_t>(a.sm_count) * F8Shape<BN>::kCtasPerSm;
-  const int64_t ctas = std::max<int64_t>(1, std::min(most, room));
-  e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(F8Shape<BN>::kThreads),
-                       static_cast<size_t>(L::bytes(p.count)), a.stream, ta, tb, td, tsa, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      Split ? most * split : std::max<int64_t>(1, std::min<int64_t>(most, a.sm_count))));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(L::bytes(p.count));
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = Split ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, ta, tb, td, tsa, p);
   count_launches(1);
   return e;
 }
 
-// 128 x 256 tiles where there are enough for the SMs, else 128 x 128.
+// 128 x 256 tiles where there are enough for the SMs, else 128 x 128, of which
+// a dense product's are split along K over clusters of two or four CTAs while
+// SMs are left and each keeps eight K blocks.
 template <Fp8Mode Mode, bool ColScale>
 cudaError_t run_shape(const Fp8Args& a) {
   const int64_t row_blocks =
@@ -981,7 +1031,14 @@ cudaError_t run_shape(const Fp8Args& a) {
   const int64_t wide_tiles =
       row_blocks * ((a.N + 255) / 256) * (Mode == Fp8Mode::kK ? a.count : 1);
   if (wide_tiles >= a.sm_count) return run_fp8<Mode, 256, 3, ColScale>(a);
-  return run_fp8<Mode, 128, ColScale ? 2 : 3, ColScale>(a);
+  if constexpr (Mode == Fp8Mode::kDense) {
+    const int64_t tiles = row_blocks * ((a.N + 127) / 128);
+    const int64_t k_blocks = (a.K + kBlock - 1) / kBlock;
+    int split = 1;
+    while (split < 4 && tiles * split * 2 <= a.sm_count && k_blocks >= split * 2 * 8) split *= 2;
+    if (split > 1) return run_fp8<Mode, 128, 5, ColScale, true>(a, split);
+  }
+  return run_fp8<Mode, 128, 5, ColScale>(a);
 }
 
 }  // namespace

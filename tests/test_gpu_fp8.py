@@ -141,7 +141,8 @@ def check(got, t, err, dtype):
 SIZES = [(1, 1, 1), (1, 8960, 1536), (3, 100, 128), (8, 256, 129), (9, 31, 700), (16, 513, 2064),
          (17, 64, 128), (31, 130, 127), (100, 200, 1000), (128, 256, 512), (129, 257, 640),
          (300, 1000, 384), (257, 520, 2049), (1024, 1100, 256), (2100, 2300, 300), (777, 7000, 130),
-         (2048, 2560, 1152)]
+         (2048, 2560, 1152),
+         (65, 300, 2049), (200, 130, 4100), (70, 1000, 6000), (130, 515, 8200)]
 
 
 @pytest.mark.parametrize("block_rows", [1, 128])
