@@ -63,6 +63,7 @@ constexpr int kSumWarps = 8;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10;
 constexpr int kRowsPerCta = 128;  // TMEM lanes
 constexpr int kStageA = kRowsPerCta * 128;
+constexpr int kBoxRow = 128, kBoxBytes = 32 * kBoxRow;  // a box of D: 32 rows of 128 bytes
 constexpr int kRowScaleBytes = kRowsPerCta * kScaleGroup * 4;
 
 struct F8Params {
@@ -97,16 +98,14 @@ struct F8Smem {
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + Stages * kStageA;
   static constexpr int kOffBox = kOffB + Stages * kTileB;
-  // D's boxes, kBoxes to a sum warp: 32 rows of 128 bytes where there is room.
-  // (A fourth stage of 128 x 256 tiles would leave room for one box of 64-byte
-  // rows: 8192^3 476 us against 466, the experts' FP32 gradients 762 against 694.)
-  static constexpr int kBoxRow = 128;
+  // D's boxes per sum warp.  (A fourth stage of 128 x 256 tiles would leave room
+  // for one box of 64-byte rows: 8192^3 476 us against 466, the experts' FP32
+  // gradients 762 against 694.)
   static constexpr int kBoxes = BN == 256 ? 2 : 1;
-  static constexpr int kBoxBytes = 32 * kBoxRow;
   static constexpr int kOffRow = kOffBox + kSumWarps * kBoxes * kBoxBytes;  // [2][128][4]
   static constexpr int kOffCol = kOffRow + 2 * kRowScaleBytes;
-  // column scales [2][4][BN]
-  static constexpr int kOffBar = kOffCol + (ColScale ? 2 * kScaleGroup * BN * 4 : 0);
+  // column scales [2][4][BN], or the halves' block scales [2][2][4]
+  static constexpr int kOffBar = kOffCol + 2 * kScaleGroup * (ColScale ? BN : 2) * 4;
   static constexpr int kBufs = 512 / BN;
   static constexpr int kBars = 2 * Stages + 2 * kBufs + 1 + 4;
   static constexpr int kOffSlot = kOffBar + kBars * 8;
@@ -379,24 +378,22 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 
 // Where the 16-byte piece q of row r of a box lies: the swizzle of D's map,
 // under which a warp's lanes, a row each, meet no bank conflicts.
-template <int Row>
 __device__ __forceinline__ uint32_t box_offset(int r, int q) {
-  return static_cast<uint32_t>(Row == 128 ? r * 128 + ((q ^ (r & 7)) << 4)
-                                          : r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+  return static_cast<uint32_t>(r * kBoxRow + ((q ^ (r & 7)) << 4));
 }
 
 // Sends a box (this warp's 32 rows, `pieces` of 16 bytes from column col0 on)
 // to D (of the stack's matrix z): by TMA where all 32 rows are D's and the box
-// is full or ends with D, else a row in Row / 16 lanes.  Either way lane 0
-// closes one bulk group.
-template <int Row>
+// is full or ends with D; else by the warp, eight lanes to a row of 16-byte
+// pieces, or, where D's rows are not aligned so, all lanes to a row, 4 bytes
+// each.  Either way lane 0 closes one bulk group.
 __device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_t* box,
                                          const F8Params& p, const F8Tile& tile, int row_in_tile,
                                          int col0, int pieces, int matrix, int lane) {
-  const int left = tile.rows - row_in_tile;  // rows of the box that are D's
+  const int left = min(32, tile.rows - row_in_tile);  // rows of the box that are D's
   const int z = p.dtype_d == DG_F32 ? 4 : 2;
   const int per = 16 / z;  // columns in 16 bytes
-  if (p.tma_d && left >= 32 && (pieces == Row / 16 || col0 + pieces * per >= p.N)) {
+  if (p.tma_d && left == 32 && (pieces == kBoxRow / 16 || col0 + pieces * per >= p.N)) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -407,30 +404,44 @@ __device__ __forceinline__ void send_box(const CUtensorMap* tmap_d, const uint8_
   }
   if (lane == 0) bulk_commit_group();
   __syncwarp();
-  constexpr int kLanes = Row / 16, kRows = 32 / kLanes;
-  const int q = lane % kLanes;
-  const int col = col0 + q * per;
+  const int64_t row = tile.row0 + row_in_tile;
+  uint8_t* d = static_cast<uint8_t*>(p.D) + (matrix * p.stride_d + row * p.ldd + col0) * z;
+  const int64_t pitch = p.ldd * z;
+  const int bytes = min(pieces * 16, (p.N - col0) * z);  // of a row
+  if (p.vec_d) {
+    const int at = (lane & 7) * 16;
 #pragma unroll
-  for (int i = 0; i < 32 / kRows; ++i) {
-    const int r = i * kRows + lane / kLanes;
-    if (r >= left || q >= pieces || col >= p.N) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(box + box_offset<Row>(r, q));
-    const int64_t row = tile.row0 + row_in_tile + r;
-    uint8_t* d = static_cast<uint8_t*>(p.D) + (matrix * p.stride_d + row * p.ldd + col) * z;
-    if (p.vec_d && col + per <= p.N) {
-      *reinterpret_cast<uint4*>(d) = v;
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      if (z == 4) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (col + k < p.N) reinterpret_cast<uint32_t*>(d)[k] = w[k];
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      if (r >= left || at >= bytes) continue;
+      const uint4 v = *reinterpret_cast<const uint4*>(box + box_offset(r, lane & 7));
+      uint8_t* dst = d + r * pitch + at;
+      if (at + 16 <= bytes) {
+        *reinterpret_cast<uint4*>(dst) = v;
       } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (col + k < p.N)
-            reinterpret_cast<uint16_t*>(d)[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t h = w[k >> 1] >> (16 * (k & 1));
+          if (at + 2 * k < bytes) reinterpret_cast<uint16_t*>(dst)[k] = static_cast<uint16_t>(h);
+        }
       }
+    }
+    return;
+  }
+  const int at = lane * 4;
+  if (at >= bytes) return;
+  const bool whole = at + 4 <= bytes && (pitch & 3) == 0 && (p.stride_d * z & 3) == 0;
+#pragma unroll 8
+  for (int r = 0; r < left; ++r) {
+    const uint32_t v =
+        *reinterpret_cast<const uint32_t*>(box + box_offset(r, lane >> 2) + (lane & 3) * 4);
+    uint8_t* dst = d + r * pitch + at;
+    if (whole) {
+      *reinterpret_cast<uint32_t*>(dst) = v;
+    } else {
+      reinterpret_cast<uint16_t*>(dst)[0] = static_cast<uint16_t>(v);
+      if (at + 4 <= bytes) reinterpret_cast<uint16_t*>(dst)[1] = static_cast<uint16_t>(v >> 16);
     }
   }
 }
@@ -615,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g_phase = 0;
       while (ok && next_tile<Mode, BN, Split>(walk, p, off, pre, tile)) {
         // groups lie at multiples of four K blocks: a tile's first may begin
-        // before the tile
+        // before the tile; an empty segment has none
+        if (tile.kb0 >= tile.kb1) continue;
         for (int kb = tile.kb0 / kScaleGroup * kScaleGroup; kb < tile.kb1; kb += kScaleGroup) {
           ok = warp_wait(&scale_empty[g], g_phase ^ 1, p, abort_flag);
           if (!ok) break;
@@ -639,6 +651,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 cs[3 * BN + 32 * (i + j)] = v[j].w;
               }
             }
+          }
+          if (!ColScale && lane < 2 * kScaleGroup) {
+            // lane = 4 half + K block of the group (past the last: the last)
+            const int col = min(tile.n0 + lane / kScaleGroup * kHalf, p.N - 1);
+            const int b = min(kb + lane % kScaleGroup, tile.kb1 - 1);
+            col_scale[g * 2 * kScaleGroup + lane] =
+                __ldg(p.sb + (Mode == Fp8Mode::kRows ? tile.expert * p.stride_sb : 0) +
+                      static_cast<int64_t>(col / kBlock) * p.lds_b + b);
           }
           if (p.vec_a) {
             __syncwarp();
@@ -678,23 +698,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t src0 =
         tmem_base + (static_cast<uint32_t>(in_tile) << 16) + static_cast<uint32_t>(half * kHalf);
     const uint32_t empty0 = smem_addr(&tmem_empty[0]);
-    constexpr int kBoxRow = L::kBoxRow;
-    uint8_t* boxes = smem + L::kOffBox + warp * L::kBoxes * L::kBoxBytes;
+    uint8_t* boxes = smem + L::kOffBox + warp * L::kBoxes * kBoxBytes;
     int buf = 0, g = 0, next_box = 0;
     uint32_t buf_phase = 0, g_phase = 0;
     while (ok && next_tile<Mode, BN, Split>(walk, p, off, pre, tile)) {
       float2 acc[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      // The row's scales of a group of K blocks come from shared memory, the
-      // half's weight block's (one address per warp) straight from memory, one
-      // group ahead.
-      const float* sb = nullptr;
-      if (!ColScale)
-        sb = p.sb + (Mode == Fp8Mode::kRows ? tile.expert * p.stride_sb : 0) +
-             static_cast<int64_t>(min(tile.n0 + half * kHalf, p.N - 1) / kBlock) * p.lds_b;
-      float4 ra, ca, cb;
-      if (!ColScale && tile.kb0 < tile.kb1) load_group(cb, sb, tile.kb0, tile.kb1, p.vec_b);
+      // the scales of a group of K blocks: the row's, and its half's weight block's
+      float4 ra, ca;
 #pragma unroll 1
       for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
         const int in_group = kb % kScaleGroup;
@@ -702,13 +714,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&scale_full[g], g_phase, p, abort_flag);
           ra = *reinterpret_cast<const float4*>(smem + L::kOffRow + g * kRowScaleBytes +
                                                 (in_tile + lane) * 16);
-          if (!ColScale) {
-            ca = cb;
-            load_group(cb, sb, kb + kScaleGroup, tile.kb1, p.vec_b);
-          } else {
-            // a segment's first block may lie inside a group
+          if (!ColScale)
+            ca = *reinterpret_cast<const float4*>(col_scale + (g * 2 + half) * kScaleGroup);
+          else  // a segment's first block may lie inside a group
             for (int i = 0; i < in_group; ++i) ra = make_float4(ra.y, ra.z, ra.w, 0.0f);
-          }
         }
         const float* cs = col_scale + (g * kScaleGroup + in_group) * BN + half * kHalf;
         ok = ok && warp_wait(&tmem_full[buf], buf_phase, p, abort_flag);
@@ -810,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[2 * i + 1] = acc[8 * h + i].y;
           }
           finish16(x, p, drow, col, bias0);
-          uint8_t* box = boxes + next_box * L::kBoxBytes;
+          uint8_t* box = boxes + next_box * kBoxBytes;
           if (fill == 0) {
             box_col = col;
             if (lane == 0) bulk_wait_group_read<L::kBoxes - 1>();  // its last store has read it
@@ -819,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.dtype_d == DG_F32) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<float4*>(box + box_offset<kBoxRow>(lane, fill + q)) =
+              *reinterpret_cast<float4*>(box + box_offset(lane, fill + q)) =
                   make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
             fill += 4;
           } else {
@@ -830,12 +839,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           : F16::pack(x[2 * i], x[2 * i + 1]);
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-              *reinterpret_cast<uint4*>(box + box_offset<kBoxRow>(lane, fill + q)) =
+              *reinterpret_cast<uint4*>(box + box_offset(lane, fill + q)) =
                   make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
             fill += 2;
           }
           if (fill == kBoxRow / 16 || col + 16 >= col_end) {
-            send_box<kBoxRow>(&tmap_d, box, p, tile, in_tile, box_col, fill, matrix, lane);
+            send_box(&tmap_d, box, p, tile, in_tile, box_col, fill, matrix, lane);
             fill = 0;
             if (++next_box == L::kBoxes) next_box = 0;
           }
@@ -860,14 +869,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// D as a stack of `count` matrices: boxes of 32 rows x box_row bytes (64 or
-// 128), swizzled over their rows.  Kept per thread as tc::make_map_2d keeps its maps.
+// D as a stack of `count` matrices: boxes of 32 rows x 128 bytes, 128-byte
+// swizzle.  Kept per thread as tc::make_map_2d keeps its maps.
 cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int64_t rows,
-                         int64_t cols, int64_t ld, int64_t count, int64_t stride, int box_row) {
+                         int64_t cols, int64_t ld, int64_t count, int64_t stride) {
   struct Entry {
     const void* base;
     int64_t rows, cols, ld, count, stride;
-    int dtype, box_row;
+    int dtype;
     CUtensorMap map;
   };
   constexpr int kCache = 16;
@@ -876,7 +885,7 @@ cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int
   for (int i = 0; i < used; ++i) {
     const Entry& c = cache[i];
     if (c.base == base && c.rows == rows && c.cols == cols && c.ld == ld && c.count == count &&
-        c.stride == stride && c.dtype == static_cast<int>(dtype) && c.box_row == box_row) {
+        c.stride == stride && c.dtype == static_cast<int>(dtype)) {
       *map = c.map;
       return cudaSuccess;
     }
@@ -888,17 +897,17 @@ cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int
                               static_cast<cuuint64_t>(count)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * z),
                                  static_cast<cuuint64_t>((count > 1 ? stride : rows * ld) * z)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_row / z), 32, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kBoxRow / z), 32, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType type = dtype == DG_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dtype == DG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        box_row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  cache[next] = Entry{base, rows, cols, ld, count, stride, static_cast<int>(dtype), box_row, *map};
+  cache[next] = Entry{base, rows, cols, ld, count, stride, static_cast<int>(dtype), *map};
   next = (next + 1) % kCache;
   if (used < kCache) ++used;
   return cudaSuccess;
@@ -967,7 +976,7 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
   CUtensorMap td = ta;  // not used without tma_d
   if (p.tma_d) {
     e = make_out_map(&td, a.D, a.dtype_d, a.M, a.N, a.ldd, Mode == Fp8Mode::kK ? a.count : 1,
-                     a.stride_d, L::kBoxRow);
+                     a.stride_d);
     if (e != cudaSuccess) return e;
   }
 
@@ -1021,21 +1030,29 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
   return e;
 }
 
-// 128 x 256 tiles where there are enough for the SMs, else 128 x 128, of which
-// a dense product's are split along K over clusters of two or four CTAs while
-// SMs are left and each keeps eight K blocks.
+// 128 x 256 tiles, except where 128 x 128 tiles take no more rounds over the
+// SMs: a K block of the narrow tile costs 0.8 of the wide one's time (2000 x
+// 2000 x 2000, 128 wide tiles or 256 narrow: 16.6 us or 18.3; 1000 x 2000 x
+// 2000, 64 or 128: 20.7 or 12.7).  A dense product's narrow tiles are split
+// along K over clusters of two or four CTAs while SMs are left and each keeps
+// five K blocks (256 x 4096 x 8192: 18.5 us, whole 23.5; 64 x 8000 x 1000, of
+// eight blocks: 10.3 us in halves, whole 7.0).
 template <Fp8Mode Mode, bool ColScale>
 cudaError_t run_shape(const Fp8Args& a) {
-  const int64_t row_blocks =
-      Mode == Fp8Mode::kRows ? a.M / 128 + std::min(a.count, a.M) : (a.M + 127) / 128;
-  const int64_t wide_tiles =
-      row_blocks * ((a.N + 255) / 256) * (Mode == Fp8Mode::kK ? a.count : 1);
-  if (wide_tiles >= a.sm_count) return run_fp8<Mode, 256, 3, ColScale>(a);
+  const int64_t row_blocks = (Mode == Fp8Mode::kRows
+                                  ? a.M / 128 + std::min(a.count, a.M)
+                                  : (a.M + 127) / 128) *
+                             (Mode == Fp8Mode::kK ? a.count : 1);
+  auto rounds = [&](int64_t bn) {
+    const int64_t tiles = row_blocks * ((a.N + bn - 1) / bn);
+    return (tiles + a.sm_count - 1) / a.sm_count;
+  };
+  if (rounds(256) < rounds(128)) return run_fp8<Mode, 256, 3, ColScale>(a);
   if constexpr (Mode == Fp8Mode::kDense) {
     const int64_t tiles = row_blocks * ((a.N + 127) / 128);
     const int64_t k_blocks = (a.K + kBlock - 1) / kBlock;
     int split = 1;
-    while (split < 4 && tiles * split * 2 <= a.sm_count && k_blocks >= split * 2 * 8) split *= 2;
+    while (split < 4 && tiles * split * 2 <= a.sm_count && k_blocks >= split * 2 * 5) split *= 2;
     if (split > 1) return run_fp8<Mode, 128, 5, ColScale, true>(a, split);
   }
   return run_fp8<Mode, 128, 5, ColScale>(a);

@@ -142,7 +142,7 @@ SIZES = [(1, 1, 1), (1, 8960, 1536), (3, 100, 128), (8, 256, 129), (9, 31, 700),
          (17, 64, 128), (31, 130, 127), (100, 200, 1000), (128, 256, 512), (129, 257, 640),
          (300, 1000, 384), (257, 520, 2049), (1024, 1100, 256), (2100, 2300, 300), (777, 7000, 130),
          (2048, 2560, 1152),
-         (65, 300, 2049), (200, 130, 4100), (70, 1000, 6000), (130, 515, 8200)]
+         (65, 300, 2049), (200, 130, 4100), (70, 1000, 6000), (130, 515, 8200), (300, 1000, 2900)]
 
 
 @pytest.mark.parametrize("block_rows", [1, 128])
@@ -293,6 +293,23 @@ def test_grouped_wgrad(dg, sizes, M, N, dtype):
             check(d[e, :, :N], *ref.product(av[:, at], bv[:, at], alpha=0.25, beta=beta,
                                             d=np.full((M, N), 2.0)), dtype)
         assert (d[:, :, N:] == 2.0).all()
+
+
+@pytest.mark.parametrize("M,N", [(600, 700), (140, 150)])
+def test_grouped_wgrad_between_empty_segments(dg, M, N):
+    # many empty experts at segment starts that are no multiple of four blocks,
+    # several tiles to a CTA
+    sizes = [0, 128, 0, 0, 384, 0] + [0, 0, 128, 0, 0] * 8 + [0] * 10
+    offsets = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    rows = int(offsets[-1])
+    a, sa, av = operand(M, rows, 53)
+    b, sb, bv = operand(N, rows, 54)
+    d = torch.full((len(sizes), M, N), 2.0, device="cuda")
+    dg.gemm_fp8_grouped_wgrad(a, sa, b, sb, gpu(offsets), d)
+    dg.check_status()
+    for e in range(len(sizes)):
+        at = slice(offsets[e], offsets[e + 1])
+        check(d[e], *ref.product(av[:, at], bv[:, at]), "f32")
 
 
 def test_grouped_wgrad_reports_misaligned_segments(dg):
