@@ -475,9 +475,9 @@ dg_status dg_quantize_fp8(int64_t rows, int64_t K, dg_dtype dtype_x, const void 
  *     N .. ldd - 1 are never touched).  bias: [N] of dtype_d, read only by the
  *     bias epilogues.  Epilogues as dg_gemm.
  *   M == 0 or N == 0 is a no-op; K == 0 gives epilogue(beta * D).
- * Few rows (M <= 16) run a streaming kernel that reads each weight once; more
- * run on tcgen05 with the block sums scaled and added in registers.  Nothing
- * is allocated.
+ * Few rows (M <= 32) run a kernel that streams the weights through shared
+ * memory into warp-level MMAs; more run on tcgen05 with the block sums scaled
+ * and added in registers.  Results are bit-stable; nothing is allocated.
  * Errors: as dg_gemm, with these rules. */
 dg_status dg_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
                       const float *scale_a, int64_t lds_a, const void *B, int64_t ldb,
@@ -495,7 +495,7 @@ dg_status dg_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
  *   stride_b is a multiple of ldb and at least N * ldb.  Rows outside every
  *   segment are neither read nor written.  Offsets are taken as clamped to
  *   [0, rows]; an end before its start is an empty segment.
- *   count is at most 512.  Other rules as dg_gemm_fp8. */
+ *   count is at most 1024.  Other rules as dg_gemm_fp8. */
 dg_status dg_gemm_fp8_grouped(int64_t count, int64_t rows, int64_t N, int64_t K, const void *A,
                               int64_t lda, const float *scale_a, int64_t lds_a, const void *B,
                               int64_t ldb, int64_t stride_b, const float *scale_b, int64_t lds_b,
@@ -550,7 +550,11 @@ dg_status dg_moe_dispatch(int64_t tokens, int64_t top_k, int64_t width, dg_dtype
                           void *D, int64_t ldd, dg_stream_t stream);
 
 /* The same, quantized on the way (dg_quantize_fp8 with 1 x 128 blocks): the
- * operand of dg_gemm_fp8_grouped without a 16-bit copy in between. */
+ * operand of dg_gemm_fp8_grouped without a 16-bit copy in between.  Where
+ * tokens have two or more rows and rows * width is 2^23 or more, the tokens are
+ * quantized first, into a per-(device, stream) workspace that grows with
+ * cudaMalloc (under CUDA-graph capture, make one call of the same sizes on the
+ * capturing stream before capture begins). */
 dg_status dg_moe_dispatch_fp8(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
                               const void *X, int64_t ldx, int64_t rows, const int32_t *row_slot,
                               void *codes, int64_t ldq, float *scales, int64_t lds,

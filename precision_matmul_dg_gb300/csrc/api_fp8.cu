@@ -205,8 +205,8 @@ dg_status dg_gemm_fp8_grouped(int64_t count, int64_t rows, int64_t N, int64_t K,
   dg_status s = check_sizes(rows, N, K);
   if (s != DG_OK) return s;
   if (count < 0) return bad("negative count");
-  if (count > kMaxFp8Experts)
-    return set_errorf(DG_ERR_UNSUPPORTED, "more than %lld experts", (long long)kMaxFp8Experts);
+  if (count > kMaxExperts)
+    return set_errorf(DG_ERR_UNSUPPORTED, "more than %lld experts", (long long)kMaxExperts);
   if (count == 0 || rows == 0 || N == 0) return DG_OK;
   Fp8Args a{};
   if ((s = check_output(D, dtype_d, ldd, N, bias, alpha, beta, epilogue, &a.epi)) != DG_OK)
@@ -266,8 +266,8 @@ dg_status dg_gemm_fp8_grouped_wgrad(int64_t count, int64_t M, int64_t N, int64_t
   dg_status s = check_sizes(M, N, rows);
   if (s != DG_OK) return s;
   if (count < 0) return bad("negative count");
-  if (count > kMaxFp8Experts)
-    return set_errorf(DG_ERR_UNSUPPORTED, "more than %lld experts", (long long)kMaxFp8Experts);
+  if (count > kMaxExperts)
+    return set_errorf(DG_ERR_UNSUPPORTED, "more than %lld experts", (long long)kMaxExperts);
   if (count == 0 || M == 0 || N == 0) return DG_OK;
   Fp8Args a{};
   if ((s = check_output(D, dtype_d, ldd, N, nullptr, alpha, beta, DG_EPI_NONE, &a.epi)) != DG_OK)

@@ -117,7 +117,7 @@ struct F8Smem {
   static constexpr int bytes(int64_t count) {
     return kFixed + static_cast<int>(count > 0 ? (ColScale ? 1 : 2) * (count + 1) * 4 : 0);
   }
-  static_assert(bytes(kMaxFp8Experts) <= 227 * 1024, "shared memory of a CTA");
+  static_assert(bytes(kMaxExperts) <= 227 * 1024, "shared memory of a CTA");
 };
 
 // A tile: rows row0 .. row0 + rows - 1 of A and D, columns from n0, K blocks
@@ -1001,7 +1001,7 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
     if (r != cudaSuccess) return r;
     if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                L::bytes(Mode == Fp8Mode::kDense ? 0 : kMaxFp8Experts));
+                                L::bytes(Mode == Fp8Mode::kDense ? 0 : kMaxExperts));
   });
   if (e != cudaSuccess) return e;
   // Experts' tiles are counted on the device: at most one part-filled row

@@ -67,7 +67,7 @@ struct SkinnySmem {
   static constexpr int kBlockBytes = (kRowsW + kRowsX) * kBlock;
   static constexpr int kStage = kStageBlocks * kBlockBytes;
   static constexpr int kRed = 2 * kMmaWarps * NT * 4 * 32 * 4;
-  static constexpr int kGroups = static_cast<int>(2 * (kMaxFp8Experts + 1) * 4);
+  static constexpr int kGroups = static_cast<int>(2 * (kMaxExperts + 1) * 4);
   static constexpr int kFree = 226 * 1024 - kRed - 256 - kGroups;  // 1 KB to align the base
   static constexpr int kStages = kFree / kStage < 8 ? kFree / kStage : 8;
   static_assert(kStages >= 2, "ring");
@@ -380,7 +380,7 @@ cudaError_t run_skinny(const Fp8Args& a, SkinnyParams p) {
   static std::atomic<uint64_t> attr_set{0};
   e = once_per_device(attr_set, dev, [&]() {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                L::bytes(kMaxFp8Experts));
+                                L::bytes(kMaxExperts));
   });
   if (e != cudaSuccess) return e;
   const int64_t chunks = p.offsets ? a.M / (8 * NT) + std::min(a.count, a.M)

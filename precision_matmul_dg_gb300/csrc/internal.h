@@ -306,8 +306,7 @@ cudaError_t launch_fp8_skinny(const Fp8Args& a);  // fp8_skinny.cu: few rows (de
 // rows of a dense product, and per expert of a grouped one, up to which
 // launch_fp8_skinny is faster
 constexpr int64_t kFp8SkinnyRows = 32, kFp8SkinnyRowsEach = 16;
-constexpr int64_t kMaxExperts = 1024;    // of a sort
-constexpr int64_t kMaxFp8Experts = 384;  // of a grouped product
+constexpr int64_t kMaxExperts = 1024;
 
 // Expert routing (moe.cu).
 struct MoeSortJob {

@@ -61,7 +61,7 @@ def test_grouped(dg):
                  stride_bias=0, alpha=1.0, beta=0.0, epi=0)
         a.update(kw)
         return dg.lib().dg_gemm_fp8_grouped(*a.values(), None)
-    for kw, word in ((dict(count=-1), "negative"), (dict(count=513), "experts"),
+    for kw, word in ((dict(count=-1), "negative"), (dict(count=1025), "experts"),
                      (dict(off=None), "offsets"), (dict(stride_b=300 * 256 + 16), "stride_b"),
                      (dict(stride_b=299 * 256), "stride_b"), (dict(stride_sb=5), "stride_sb"),
                      (dict(N=1 << 30, stride_b=256 << 30, ldd=1 << 30, count=4, stride_sb=1 << 40),
@@ -75,7 +75,7 @@ def test_grouped(dg):
                  lds_b=2, off=P, D=P, t=5, ldd=16, stride_d=128, alpha=1.0, beta=0.0)
         a.update(kw)
         return dg.lib().dg_gemm_fp8_grouped_wgrad(*a.values(), None)
-    for kw, word in ((dict(count=513), "experts"), (dict(stride_d=100), "stride_d"),
+    for kw, word in ((dict(count=1025), "experts"), (dict(stride_d=100), "stride_d"),
                      (dict(off=None), "offsets"), (dict(lda=200), "A: row pitch"),
                      (dict(t=2), "F16, BF16 or F32")):
         refused(dg, grad(**kw), word)
