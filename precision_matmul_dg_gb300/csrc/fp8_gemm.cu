@@ -20,9 +20,11 @@
 //               128 bytes each, 128-byte swizzle);
 //   warp 9      tensor memory allocation; MMA issuer, 4 x tcgen05.mma
 //               (kind::f8f6f4, K = 32) per stage;
-//   warp 10     with 1 x 128 blocks in B: brings the columns' scales of four K
-//               blocks at a time to shared memory, two such groups ahead;
-//   warp 11     nothing: it completes the third warpgroup.
+//   warps 10-11 bring the scales of four K blocks at a time to shared memory,
+//               two such groups ahead (a sum thread that loads its row's scale
+//               itself reads 32 lines with 31 others; that cost 137 clocks a K
+//               block): the rows' by TMA, the columns' (1 x 128 blocks in B)
+//               transposed, half of them each, or the halves' weight blocks'.
 //
 // CG = 2: a cluster of two CTAs computes a tile of 256 rows with cta_group::2
 // MMAs, each CTA holding 128 rows of A and half of B's rows: 32 KB instead of
@@ -337,7 +339,9 @@ __device__ __forceinline__ void add16(float (&v)[16], float k, const void* p, in
 }
 
 // alpha * t + beta * D, bias and GELU of 16 columns from col0 on, row `drow`
-// (element offset of D).  Columns >= N read nothing.
+// (element offset of D).  Columns >= N read nothing.  Gradients have neither
+// bias nor GELU.
+template <Fp8Mode Mode>
 __device__ __forceinline__ void finish16(float (&v)[16], const F8Params& p, int64_t drow, int col0,
                                          int64_t bias0) {
   const int n = p.N - col0;
@@ -346,9 +350,9 @@ __device__ __forceinline__ void finish16(float (&v)[16], const F8Params& p, int6
   for (int i = 0; i < 16; ++i) v[i] *= p.alpha;
   if (p.beta != 0.0f)
     add16(v, p.beta, static_cast<const uint8_t*>(p.D) + (drow + col0) * z, p.dtype_d, n);
-  if (p.flags & kEpiBias)
+  if (Mode != Fp8Mode::kK && (p.flags & kEpiBias))
     add16(v, 1.0f, static_cast<const uint8_t*>(p.bias) + (bias0 + col0) * z, p.dtype_d, n);
-  if (p.flags & kEpiGelu) {
+  if (Mode != Fp8Mode::kK && (p.flags & kEpiGelu)) {
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       const float2 g = gelu2(make_float2(v[i], v[i + 1]));
@@ -370,9 +374,9 @@ __device__ __forceinline__ float4 ld_cluster_float4(uint32_t cluster_addr) {
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t x,
                                              int32_t y, int32_t z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z)
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], "
+      "[%1], %5;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z), "l"(policy_evict_first())
       : "memory");
 }
 
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tmem_empty[b], kSumWarps);
     }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&scale_full[g], 1);
+      mbar_init(&scale_full[g], ColScale ? 2 : 1);
       mbar_init(&scale_empty[g], kSumWarps);
     }
     mbar_init(drain_bar, 1);
@@ -618,72 +622,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(drain_bar);
         mbar_wait(drain_bar, 0, p.timeout_ns, p.status);
       }
-    } else if (warp == kScaleWarp) {
+    } else if (warp == kScaleWarp || ColScale) {
       // -------------------------------------------------------------- scales
+      // Groups lie at multiples of four K blocks: a tile's first may begin
+      // before the tile; an empty segment has none.  The next group's column
+      // scales are loaded before its place is free.
+      const int part = warp - kScaleWarp;  // ColScale: this warp's half of the columns
       const uint64_t pol_scale = policy_evict_last();
+      constexpr int kCols = ColScale ? BN / 64 : 1;  // per lane
+      float4 v[kCols];
       int64_t groups = 0;
-      int g = 0;
+      int g = 0, kb = 0;
       uint32_t g_phase = 0;
-      while (ok && next_tile<Mode, BN, Split>(walk, p, off, pre, tile)) {
-        // groups lie at multiples of four K blocks: a tile's first may begin
-        // before the tile; an empty segment has none
-        if (tile.kb0 >= tile.kb1) continue;
-        for (int kb = tile.kb0 / kScaleGroup * kScaleGroup; kb < tile.kb1; kb += kScaleGroup) {
-          ok = warp_wait(&scale_empty[g], g_phase ^ 1, p, abort_flag);
-          if (!ok) break;
-          uint8_t* rows = smem + L::kOffRow + g * kRowScaleBytes;
-          if (ColScale) {
-            // [4][BN], a lane's columns 32 apart
-            float* cs = col_scale + g * kScaleGroup * BN + lane;
+      tile.kb1 = 0;
+      auto next_group = [&]() {
+        kb += kScaleGroup;
+        while (kb >= tile.kb1) {
+          if (!next_tile<Mode, BN, Split>(walk, p, off, pre, tile)) return false;
+          kb = tile.kb0 < tile.kb1 ? tile.kb0 / kScaleGroup * kScaleGroup : tile.kb1;
+        }
+        if (ColScale) {
 #pragma unroll
-            for (int i = 0; i < BN / 32; i += 4) {
-              float4 v[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int64_t col = min(tile.n0 + lane + 32 * (i + j), p.N - 1);
-                load_group(v[j], p.sb + col * p.lds_b, kb, tile.kb1, p.vec_b);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                cs[32 * (i + j)] = v[j].x;
-                cs[BN + 32 * (i + j)] = v[j].y;
-                cs[2 * BN + 32 * (i + j)] = v[j].z;
-                cs[3 * BN + 32 * (i + j)] = v[j].w;
-              }
-            }
+          for (int j = 0; j < kCols; ++j) {
+            const int64_t col = min(tile.n0 + part * (BN / 2) + lane + 32 * j, p.N - 1);
+            load_group(v[j], p.sb + col * p.lds_b, kb, tile.kb1, p.vec_b);
           }
-          if (!ColScale && lane < 2 * kScaleGroup) {
-            // lane = 4 half + K block of the group (past the last: the last)
-            const int col = min(tile.n0 + lane / kScaleGroup * kHalf, p.N - 1);
-            const int b = min(kb + lane % kScaleGroup, tile.kb1 - 1);
-            col_scale[g * 2 * kScaleGroup + lane] =
-                __ldg(p.sb + (Mode == Fp8Mode::kRows ? tile.expert * p.stride_sb : 0) +
-                      static_cast<int64_t>(col / kBlock) * p.lds_b + b);
-          }
-          if (p.vec_a) {
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&scale_full[g], kRowScaleBytes);
-              tma_load_2d(&tmap_sa, &scale_full[g], rows, kb, tile.row0, pol_scale);
-            }
-          } else {
-            float4 v[4];
+        } else if (lane < 2 * kScaleGroup) {
+          // lane = 4 half + K block of the group (past the last: the last)
+          const int col = min(tile.n0 + lane / kScaleGroup * kHalf, p.N - 1);
+          const int64_t block = col / kBlock;
+          v[0].x = __ldg(p.sb + (Mode == Fp8Mode::kRows ? tile.expert * p.stride_sb : 0) +
+                         block * p.lds_b + min(kb + lane % kScaleGroup, tile.kb1 - 1));
+        }
+        return true;
+      };
+      while (next_group()) {
+        ok = warp_wait(&scale_empty[g], g_phase ^ 1, p, abort_flag);
+        if (!ok) break;
+        if (ColScale) {
+          // [4][BN], a lane's columns 32 apart
+          float* cs = col_scale + g * kScaleGroup * BN + part * (BN / 2) + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int64_t r = min(tile.row0 + lane + 32 * i, p.M - 1);
-              load_group(v[i], p.sa + r * p.lds_a, kb, tile.kb1, 0);
-            }
+          for (int j = 0; j < kCols; ++j) {
+            cs[32 * j] = v[j].x;
+            cs[BN + 32 * j] = v[j].y;
+            cs[2 * BN + 32 * j] = v[j].z;
+            cs[3 * BN + 32 * j] = v[j].w;
+          }
+        } else if (lane < 2 * kScaleGroup) {
+          col_scale[g * 2 * kScaleGroup + lane] = v[0].x;
+        }
+        uint8_t* rows = smem + L::kOffRow + g * kRowScaleBytes;
+        if (part == 0 && !p.vec_a) {
+          float4 r[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(rows + (lane + 32 * i) * 16) = v[i];
-            __syncwarp();
-            lane0_arrive(smem_addr(&scale_full[g]), lane);
+          for (int i = 0; i < 4; ++i) {
+            const int64_t row = min(tile.row0 + lane + 32 * i, p.M - 1);
+            load_group(r[i], p.sa + row * p.lds_a, kb, tile.kb1, 0);
           }
-          ++groups;
-          if (++g == 2) {
-            g = 0;
-            g_phase ^= 1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(rows + (lane + 32 * i) * 16) = r[i];
+        }
+        __syncwarp();
+        if (part == 0 && p.vec_a) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&scale_full[g], kRowScaleBytes);
+            tma_load_2d(&tmap_sa, &scale_full[g], rows, kb, tile.row0, pol_scale);
           }
+        } else {
+          lane0_arrive(smem_addr(&scale_full[g]), lane);
+        }
+        ++groups;
+        if (++g == 2) {
+          g = 0;
+          g_phase ^= 1;
         }
       }
       if (!ok) *abort_flag = 1;
@@ -818,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[2 * i] = acc[8 * h + i].x;
             x[2 * i + 1] = acc[8 * h + i].y;
           }
-          finish16(x, p, drow, col, bias0);
+          finish16<Mode>(x, p, drow, col, bias0);
           uint8_t* box = boxes + next_box * kBoxBytes;
           if (fill == 0) {
             box_col = col;
