@@ -47,6 +47,7 @@
 // in runs of whole rows.  Straight from registers a store touches 32 rows, one
 // line each: 5500 clocks per 128 x 256 tile.
 #include <algorithm>
+#include <type_traits>
 
 #include "epilogue.cuh"
 #include "fp8.cuh"
@@ -103,7 +104,7 @@ struct F8Smem {
   // D's boxes per sum warp.  (A fourth stage of 128 x 256 tiles would leave room
   // for one box of 64-byte rows: 8192^3 476 us against 466, the experts' FP32
   // gradients 762 against 694.)
-  static constexpr int kBoxes = BN == 256 ? 2 : 1;
+  static constexpr int kBoxes = BN == 256 || Stages < 5 ? 2 : 1;
   static constexpr int kOffRow = kOffBox + kSumWarps * kBoxes * kBoxBytes;  // [2][128][4]
   static constexpr int kOffCol = kOffRow + 2 * kRowScaleBytes;
   // column scales [2][4][BN], or the halves' block scales [2][2][4]
@@ -296,6 +297,11 @@ __device__ __forceinline__ float2 gelu2(float2 t) {
   const float2 x = make_float2(ex2_approx(e.x), ex2_approx(e.y));
   q = mul2(mul2(q, s), x);
   return fma2(mul2(a, both(-1.0f)), q, make_float2(fmaxf(t.x, 0.0f), fmaxf(t.y, 0.0f)));
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(float2 a, float2 b, float2 c, float2 d) {
+  return make_uint4(T::pack(a.x, a.y), T::pack(b.x, b.y), T::pack(c.x, c.y), T::pack(d.x, d.y));
 }
 
 __device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int dtype) {
@@ -818,6 +824,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t drow = matrix * p.stride_d + row * p.ldd;
       const int64_t bias0 = Mode == Fp8Mode::kRows ? tile.expert * p.stride_bias : 0;
       const int col_end = tile.rows > in_tile ? min(p.N, first + columns) : 0;
+      const bool scaled_only = p.beta == 0.0f && p.flags == 0;
+      if (!Split && scaled_only && tile.rows > in_tile && first + kHalf <= p.N) {
+        // All of the warp's columns, alpha only: no more than the stores need
+        // (with the loop below, for which 40 clocks a column are spent, a tile
+        // took 5900 clocks).
+        const float2 alpha = make_float2(p.alpha, p.alpha);
+        auto pass = [&](auto columns_of_box, auto put) {
+          constexpr int kCols = decltype(columns_of_box)::value;
+#pragma unroll
+          for (int c = 0; c < kHalf; c += kCols) {
+            uint8_t* box = boxes + next_box * kBoxBytes;
+            if (++next_box == L::kBoxes) next_box = 0;
+            if (lane == 0) bulk_wait_group_read<L::kBoxes - 1>();  // its last store has read it
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < kBoxRow / 16; ++q)
+              *reinterpret_cast<uint4*>(box + box_offset(lane, q)) =
+                  put(c / 2 + q * (kCols * 16 / kBoxRow / 2));
+            send_box(&tmap_d, box, p, tile, in_tile, first + c, kBoxRow / 16, matrix, lane);
+          }
+        };
+        if (p.dtype_d == DG_F32)
+          pass(std::integral_constant<int, 32>(), [&](int i) {
+            const float2 x = mul2(acc[i], alpha), y = mul2(acc[i + 1], alpha);
+            return make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
+                              __float_as_uint(y.y));
+          });
+        else if (p.dtype_d == DG_BF16)
+          pass(std::integral_constant<int, 64>(), [&](int i) {
+            return pack8<BF16>(mul2(acc[i], alpha), mul2(acc[i + 1], alpha),
+                               mul2(acc[i + 2], alpha), mul2(acc[i + 3], alpha));
+          });
+        else
+          pass(std::integral_constant<int, 64>(), [&](int i) {
+            return pack8<F16>(mul2(acc[i], alpha), mul2(acc[i + 1], alpha),
+                              mul2(acc[i + 2], alpha), mul2(acc[i + 3], alpha));
+          });
+        continue;
+      }
       int fill = 0, box_col = 0;  // the open box: 16-byte pieces in it, its first column
 #pragma unroll 1
       for (int col0 = first; col0 < col_end; col0 += 32) {
@@ -846,10 +891,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             fill += 4;
           } else {
             uint32_t w[8];
+            if (p.dtype_d == DG_BF16) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              w[i] = p.dtype_d == DG_BF16 ? BF16::pack(x[2 * i], x[2 * i + 1])
-                                          : F16::pack(x[2 * i], x[2 * i + 1]);
+              for (int i = 0; i < 8; ++i) w[i] = BF16::pack(x[2 * i], x[2 * i + 1]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = F16::pack(x[2 * i], x[2 * i + 1]);
+            }
 #pragma unroll
             for (int q = 0; q < 2; ++q)
               *reinterpret_cast<uint4*>(box + box_offset(lane, fill + q)) =
