@@ -26,25 +26,29 @@
 //               block): the rows' by TMA, the columns' (1 x 128 blocks in B)
 //               transposed, half of them each, or the halves' weight blocks'.
 //
-// CG = 2: a cluster of two CTAs computes a tile of 256 rows with cta_group::2
-// MMAs, each CTA holding 128 rows of A and half of B's rows: 32 KB instead of
-// 48 KB come in per 128 x 256 x 128 block.  (A CTA alone is held by those
-// copies: at 1/4 of the MMAs and 1/4 of the TMEM loads it still took 660 clocks
-// per block, 72 bytes per clock and SM, where the MMAs take 512.)
+// What a K block of a 128 x 256 tile takes is about 830 clocks, where its MMAs
+// take 512 and its TMEM loads 560: with two buffers of 256 columns, an MMA waits
+// for the release of the buffer before last, a release for the loads of the
+// last column, and both for an mbarrier's way there (8192^3: 423 us, 67% of the
+// tensor rate).  Measured with no gain: pairs of CTAs (cta_group::2, half of B
+// each), two CTAs per SM with 128 x 128 tiles, a fourth stage, loads of 32
+// columns.
 //
-// A sum thread holds up to 128 sums beside two 32-column loads, more than the
+// A sum thread holds up to 128 sums beside two 16-column loads, more than the
 // 168 registers that 384 threads can have each: the third warpgroup keeps 72
 // and the two of the sum warps take 216 (2 x 216 + 72 = 3 x 168).
 //
-// The kernel is persistent: unit u (CTA or pair) takes tiles u, u + units, ...
-// Experts' segments are read from the device's offsets: every CTA counts the
-// segments' row blocks into shared memory, and every role walks the same tile
-// list.  A row tile may run into the next expert's rows (they are loaded,
-// never stored).  Weight gradients walk (expert, tile) with K = the segment.
+// The kernel is persistent: CTA u takes tiles u, u + CTAs, ...  Experts'
+// segments are read from the device's offsets: every CTA counts the segments'
+// row blocks into shared memory, and every role walks the same tile list.  A
+// row tile may run into the next expert's rows (they are loaded, never stored).
+// Weight gradients walk (expert, tile) with K = the segment.  Split: a dense
+// product of few tiles has a cluster of CTAs per tile, a share of K each, whose
+// sums meet through distributed shared memory in the order of K.
 //
-// D leaves through shared memory: a warp's 32 rows x 64 bytes at a time, by
-// TMA, or (a segment's last rows, layouts that TMA does not take) by the warp
-// in runs of whole rows.  Straight from registers a store touches 32 rows, one
+// D leaves through shared memory: a warp's 32 rows x 128 bytes at a time,
+// by TMA, or (a segment's last rows, layouts that TMA does not take) by the
+// warp in runs of whole rows.  Straight from registers a store touches 32 rows, one
 // line each: 5500 clocks per 128 x 256 tile.
 #include <algorithm>
 #include <type_traits>
@@ -101,10 +105,7 @@ struct F8Smem {
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kOffA + Stages * kStageA;
   static constexpr int kOffBox = kOffB + Stages * kTileB;
-  // D's boxes per sum warp.  (A fourth stage of 128 x 256 tiles would leave room
-  // for one box of 64-byte rows: 8192^3 476 us against 466, the experts' FP32
-  // gradients 762 against 694.)
-  static constexpr int kBoxes = BN == 256 || Stages < 5 ? 2 : 1;
+  static constexpr int kBoxes = BN == 256 ? 2 : 1;  // D's, per sum warp
   static constexpr int kOffRow = kOffBox + kSumWarps * kBoxes * kBoxBytes;  // [2][128][4]
   static constexpr int kOffCol = kOffRow + 2 * kRowScaleBytes;
   // column scales [2][4][BN], or the halves' block scales [2][2][4]
@@ -183,25 +184,26 @@ __device__ __forceinline__ bool next_tile(F8Walk& w, const F8Params& p, const in
 __device__ __forceinline__ void mma_block(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t done_bar, uint32_t free_bar,
                                           uint32_t issue) {
-    asm volatile(
-        "{\n\t.reg .pred i, f, t;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.u32 i, %6, 0;\n\t"
-        "setp.ne.u32 f, 0, 0;\n\t"
-        "setp.eq.u32 t, 0, 0;\n\t"
-        "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
-        "add.s64 a, %1, 2;\n\t"
-        "add.s64 b, %2, 2;\n\t"
-        "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
-        "add.s64 a, %1, 4;\n\t"
-        "add.s64 b, %2, 4;\n\t"
-        "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
-        "add.s64 a, %1, 6;\n\t"
-        "add.s64 b, %2, 6;\n\t"
-        "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
-        "@i tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
-        "@i tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(done_bar), "r"(free_bar), "r"(issue)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred i, f, t;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.u32 i, %6, 0;\n\t"
+      "setp.ne.u32 f, 0, 0;\n\t"
+      "setp.eq.u32 t, 0, 0;\n\t"
+      "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+      "add.s64 a, %1, 2;\n\t"
+      "add.s64 b, %2, 2;\n\t"
+      "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\t"
+      "add.s64 b, %2, 4;\n\t"
+      "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\t"
+      "add.s64 b, %2, 6;\n\t"
+      "@i tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "@i tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+      "@i tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+      :
+      : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(done_bar), "r"(free_bar), "r"(issue)
+      : "memory");
 }
 
 // A wait of a whole warp, all lanes polling together so that the warp stays
@@ -609,9 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after_sync();
           mma_block(tmem_base + static_cast<uint32_t>(buf * BN),
-                        desc_a + static_cast<uint64_t>(stage * (kStageA >> 4)),
-                        desc_b + static_cast<uint64_t>(stage * (L::kTileB >> 4)), idesc,
-                        smem_addr(&tmem_full[buf]), smem_addr(&empty_bar[stage]), issue);
+                    desc_a + static_cast<uint64_t>(stage * (kStageA >> 4)),
+                    desc_b + static_cast<uint64_t>(stage * (L::kTileB >> 4)), idesc,
+                    smem_addr(&tmem_full[buf]), smem_addr(&empty_bar[stage]), issue);
           if (++stage == Stages) {
             stage = 0;
             phase ^= 1;
@@ -824,12 +826,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t drow = matrix * p.stride_d + row * p.ldd;
       const int64_t bias0 = Mode == Fp8Mode::kRows ? tile.expert * p.stride_bias : 0;
       const int col_end = tile.rows > in_tile ? min(p.N, first + columns) : 0;
-      const bool scaled_only = p.beta == 0.0f && p.flags == 0;
-      if (!Split && scaled_only && tile.rows > in_tile && first + kHalf <= p.N) {
-        // All of the warp's columns, alpha only: no more than the stores need
-        // (with the loop below, for which 40 clocks a column are spent, a tile
-        // took 5900 clocks).
-        const float2 alpha = make_float2(p.alpha, p.alpha);
+      if (!Split && p.beta == 0.0f && tile.rows > in_tile && first + kHalf <= p.N) {
+        // All of the warp's columns, straight through (in the loop below a tile
+        // took 5900 clocks; experts' gradients 522 us, were 687).
+        float2 alpha = make_float2(p.alpha, p.alpha);
+        if (Mode != Fp8Mode::kK && (p.flags & kEpiBias)) {
+          // the warp's biases through a box (32768 x 4096 x 2048 with GELU: 312
+          // us; loaded by every lane, 16 columns at a time: 355)
+          float* bias = reinterpret_cast<float*>(boxes);
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32)
+            bias[c + lane] = load_as_f32(p.bias, bias0 + first + c + lane, p.dtype_d);
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 4) {
+            const float4 k = *reinterpret_cast<const float4*>(bias + c);
+            acc[c / 2] = fma2(acc[c / 2], alpha, make_float2(k.x, k.y));
+            acc[c / 2 + 1] = fma2(acc[c / 2 + 1], alpha, make_float2(k.z, k.w));
+          }
+          alpha = make_float2(1.0f, 1.0f);
+          __syncwarp();
+        }
+        if (Mode != Fp8Mode::kK && (p.flags & kEpiGelu)) {
+#pragma unroll
+          for (int i = 0; i < kHalf / 2; ++i) acc[i] = gelu2(mul2(acc[i], alpha));
+          alpha = make_float2(1.0f, 1.0f);
+        }
         auto pass = [&](auto columns_of_box, auto put) {
           constexpr int kCols = decltype(columns_of_box)::value;
 #pragma unroll
@@ -964,8 +988,7 @@ cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int
                                    : dtype == DG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   cache[next] = Entry{base, rows, cols, ld, count, stride, static_cast<int>(dtype), *map};
