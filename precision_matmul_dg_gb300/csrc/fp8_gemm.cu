@@ -826,9 +826,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t drow = matrix * p.stride_d + row * p.ldd;
       const int64_t bias0 = Mode == Fp8Mode::kRows ? tile.expert * p.stride_bias : 0;
       const int col_end = tile.rows > in_tile ? min(p.N, first + columns) : 0;
-      if (!Split && p.beta == 0.0f && tile.rows > in_tile && first + kHalf <= p.N) {
-        // All of the warp's columns, straight through (in the loop below a tile
-        // took 5900 clocks; experts' gradients 522 us, were 687).
+      if (!Split && p.beta == 0.0f) {
+        if (col_end == 0 || first >= p.N) continue;
+        // Straight through all of the warp's columns, N's or not (experts' gradients
+        // 527 us, were 687 in the loop below, 5900 clocks a tile; 2000^3, whose last
+        // tiles are cut, 17.2 us, 19.2 with those in the loop).
         float2 alpha = make_float2(p.alpha, p.alpha);
         if (Mode != Fp8Mode::kK && (p.flags & kEpiBias)) {
           // the warp's biases through a box (32768 x 4096 x 2048 with GELU: 312
@@ -838,7 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < kHalf; c += 32)
-            bias[c + lane] = load_as_f32(p.bias, bias0 + first + c + lane, p.dtype_d);
+            bias[c + lane] =
+                load_as_f32(p.bias, bias0 + min(first + c + lane, p.N - 1), p.dtype_d);
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < kHalf; c += 4) {
@@ -858,6 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kCols = decltype(columns_of_box)::value;
 #pragma unroll
           for (int c = 0; c < kHalf; c += kCols) {
+            if (first + c >= p.N) break;
             uint8_t* box = boxes + next_box * kBoxBytes;
             if (++next_box == L::kBoxes) next_box = 0;
             if (lane == 0) bulk_wait_group_read<L::kBoxes - 1>();  // its last store has read it
@@ -1115,12 +1119,13 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
 }
 
 // 128 x 256 tiles, except where 128 x 128 tiles take no more rounds over the
-// SMs: a K block of the narrow tile costs 0.8 of the wide one's time (2000 x
-// 2000 x 2000, 128 wide tiles or 256 narrow: 16.6 us or 18.3; 1000 x 2000 x
-// 2000, 64 or 128: 20.7 or 12.7).  A dense product's narrow tiles are split
-// along K over clusters of two or four CTAs while SMs are left and each keeps
-// five K blocks (256 x 4096 x 8192: 18.5 us, whole 23.5; 64 x 8000 x 1000, of
-// eight blocks: 10.3 us in halves, whole 7.0).
+// SMs: a K block of the narrow tile costs 0.6 of the wide one's time (4096^3, 512
+// wide tiles or 1024 narrow: 65 us or 77; 2000^3, 128 or 256: 14.6 us or 17.5;
+// 1000 x 2000 x 2000, 64 or 128: 18.0 us or 11.9).  A dense product's narrow
+// tiles are split along K over clusters of two or four CTAs while SMs are left
+// and each keeps five K blocks (256 x 4096 x 8192: 18.2 us, whole 22.2; 64 x
+// 4096 x 4096: 9.7, whole 12.4; 64 x 8000 x 1000, of eight blocks: 9.8 us in
+// halves, whole 6.1).
 template <Fp8Mode Mode, bool ColScale>
 cudaError_t run_shape(const Fp8Args& a) {
   const int64_t row_blocks = (Mode == Fp8Mode::kRows
