@@ -7,6 +7,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include "epilogue.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -104,6 +105,47 @@ __device__ __forceinline__ uint2 quantize8(const uint32_t (&w)[4], const BlockSc
   const float f = b.factor;
   return make_uint2(e4m3x4(x0.x * f, x0.y * f, x1.x * f, x1.y * f),
                     e4m3x4(x2.x * f, x2.y * f, x3.x * f, x3.y * f));
+}
+
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<uint64_t*>(&d))
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<uint64_t*>(&d))
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return d;
+}
+
+// GELU of two values: t Phi(t) = max(t, 0) + b Phi(b), b = -|t|, with Phi the
+// normal distribution function and Phi(b) = 2^P(b).  P(b) = -1 + b R(b) is a
+// weighted least-squares fit of log2 Phi on [-6, 0], reweighted until the errors
+// of Phi were level: at most 1.0e-7, and 2.2e-4 of Phi there; P falls steadily
+// below -6 (an error of 3e-12 of GELU) and is cut off at -16, for infinities.
+// The GELU of a tile costs as much as several of its K blocks: one exponential
+// per value and eight packed FMAs per two, without the reciprocal that the
+// form with exp(-t^2 / 2) times a polynomial takes (both share the unit of 16
+// results per clock and SM).
+__device__ __forceinline__ float2 gelu2(float2 t) {
+  constexpr float c[9] = {-1.0f,           1.15111136f,     -4.59140331e-1f,
+                          5.27343079e-2f,  7.43800076e-3f,  4.35754948e-4f,
+                          -6.15835597e-5f, -1.36701265e-5f, -7.71337284e-7f};
+  float2 b, m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(b.x) : "f"(-fabsf(t.x)), "f"(-16.0f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(b.y) : "f"(-fabsf(t.y)), "f"(-16.0f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m.x) : "f"(t.x), "f"(0.0f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m.y) : "f"(t.y), "f"(0.0f));
+  float2 q = make_float2(c[8], c[8]);
+#pragma unroll
+  for (int i = 7; i >= 0; --i) q = fma2(q, b, make_float2(c[i], c[i]));
+  return fma2(b, make_float2(ex2_approx(q.x), ex2_approx(q.y)), m);
 }
 
 }  // namespace fp8

@@ -260,47 +260,6 @@ __device__ __forceinline__ void load_group(float4& v, const float* s, int kb, in
   }
 }
 
-// Two FP32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(*reinterpret_cast<uint64_t*>(&d))
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
-        "l"(*reinterpret_cast<const uint64_t*>(&c)));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(*reinterpret_cast<uint64_t*>(&d))
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return d;
-}
-
-// gelu_erf (epilogue.cuh) of two values, its multiplications and additions in
-// packed instructions: GELU(t) = max(t, 0) - |t| q.  The GELU of a tile costs as
-// much as several of its K blocks, so instructions count.
-__device__ __forceinline__ float2 gelu2(float2 t) {
-  constexpr float p = 0.3275911f, a1 = 0.254829592f, a2 = -0.284496736f, a3 = 1.421413741f,
-                  a4 = -1.453152027f, a5 = 1.061405429f;
-  constexpr float kP = p * 0.70710678118654752f;  // p / sqrt 2
-  constexpr float kE = -0.72134752044448170f;     // -log2(e) / 2
-  auto both = [](float x) { return make_float2(x, x); };
-  const float2 a = make_float2(fabsf(t.x), fabsf(t.y));
-  const float2 den = fma2(a, both(kP), both(1.0f));
-  float2 s;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(den.x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(den.y));
-  float2 q = fma2(both(0.5f * a5), s, both(0.5f * a4));
-  q = fma2(q, s, both(0.5f * a3));
-  q = fma2(q, s, both(0.5f * a2));
-  q = fma2(q, s, both(0.5f * a1));
-  const float2 e = mul2(mul2(a, a), both(kE));
-  const float2 x = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-  q = mul2(mul2(q, s), x);
-  return fma2(mul2(a, both(-1.0f)), q, make_float2(fmaxf(t.x, 0.0f), fmaxf(t.y, 0.0f)));
-}
-
 template <typename T>
 __device__ __forceinline__ uint4 pack8(float2 a, float2 b, float2 c, float2 d) {
   return make_uint4(T::pack(a.x, a.y), T::pack(b.x, b.y), T::pack(c.x, c.y), T::pack(d.x, d.y));

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.beta != 0.0f) v = fmaf(p.beta, load_as_f32(p.D, at, p.dtype_d), v);
         if (p.flags & kEpiBias)
           v += load_as_f32(p.bias, tile.expert * p.stride_bias + n, p.dtype_d);
-        if (p.flags & kEpiGelu) v = gelu_erf(v);
+        if (p.flags & kEpiGelu) v = gelu2(make_float2(v, v)).x;
         if (p.dtype_d == DG_F32)
           static_cast<float*>(p.D)[at] = v;
         else

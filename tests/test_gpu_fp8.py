@@ -177,6 +177,30 @@ def test_gemm_epilogue(dg, M, N, K, dtype, epilogue):
     assert torch.equal(room[:, N:], before[:, N:])
 
 
+@pytest.mark.parametrize("M,N", [(4, 1201), (130, 1201), (5000, 1204)])
+def test_gelu_over_its_range(dg, M, N):
+    """Zero operands: the bias alone is GELU's argument.  Its Phi is good to
+    1e-7 and the exponential's 2^-22 of at most 1/2, the result is rounded."""
+    a = torch.zeros(M, 128, device="cuda").to(torch.float8_e4m3fn)
+    b = torch.zeros(N, 128, device="cuda").to(torch.float8_e4m3fn)
+    one = torch.ones(max(M, N), 1, device="cuda")
+    t = torch.linspace(-12.0, 12.0, N)
+    t[:9] = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3e4, -3e4, float("inf"), -float("inf"),
+                          float("nan")])
+    d = torch.empty(M, N, device="cuda")
+    dg.gemm_fp8(a, one[:M], b, one[:(N + 127) // 128], d, bias=t.cuda(), epilogue="bias_gelu")
+    dg.check_status()
+    got = d.cpu().double()
+    assert torch.equal(got.nan_to_num(-1.0), got[:1].nan_to_num(-1.0).expand_as(got))
+    got = got[-1]
+    assert got[6] == float("inf") and got[7] == 0.0 and torch.isnan(got[8])
+    x = t.double()
+    keep = torch.isfinite(x)
+    want = 0.5 * x * torch.special.erfc(-x / 2.0 ** 0.5)
+    bound = (1e-7 + 2.0 ** -23) * x.abs() + 2.0 ** -23 * want.abs() + 4e-12
+    assert ((got - want).abs() <= bound)[keep].all()
+
+
 @pytest.mark.parametrize("M", [4, 200])
 def test_gemm_without_k(dg, M):
     a, sa = torch.empty(M, 0, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(M, 0).cuda()
