@@ -405,8 +405,9 @@ dg_status dg_moe_dispatch_fp8(int64_t tokens, int64_t top_k, int64_t width, dg_d
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // Each row quantized by itself does a token's work up to top_k times.  Where
   // that is the larger part, the tokens are quantized once into scratch and
-  // the rows copied from there (16384 tokens of 2048 to 139 thousand rows: 70
-  // us against 149; 512 tokens to 4096 rows: 7.0 us either way).
+  // the rows copied from there (16384 tokens of 2048 to 139 thousand rows: 77
+  // us against 150; with the sort, 512 tokens to 4096 rows 9.9 us against
+  // 11.9, 256 to 2048 9.2 either way).
   if (rows >= 2 * tokens && tokens > 0 && rows * width >= (int64_t(1) << 23)) {
     const int64_t pitch = ceil_div(width, 16) * 16, blocks = ceil_div(width, kFp8Block);
     void* scratch = nullptr;

@@ -29,8 +29,11 @@
 // What a K block of a 128 x 256 tile takes is about 830 clocks, where its MMAs
 // take 512 and its TMEM loads 560: with two buffers of 256 columns, an MMA waits
 // for the release of the buffer before last, a release for the loads of the
-// last column, and both for an mbarrier's way there (8192^3: 423 us, 67% of the
-// tensor rate).  Measured with no gain: pairs of CTAs (cta_group::2, half of B
+// last column, and both for an mbarrier's way there (8192^3: 424 us, 67% of the
+// tensor rate; 32768 x 4096 x 2048: 231 us, 64 experts' 32768 rows of the same
+// sizes, whose last tiles are part-filled: 286 us, with GELU 338; FP32 gradients
+// of 64 experts, 4096 x 2048 each: 526 us, 4.07 TB/s of stores, what clearing
+// such a buffer reaches).  Measured with no gain: pairs of CTAs (cta_group::2, half of B
 // each), two CTAs per SM with 128 x 128 tiles, a fourth stage, loads of 32
 // columns.
 //
@@ -685,6 +688,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 acc[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+      // the warp's biases, on their way during the K blocks (32768 x 4096 x 2048
+      // with bias and GELU: 299 us, loaded after them 307)
+      float bias_ahead[kHalf / 32];
+      if (Mode != Fp8Mode::kK && !Split && (p.flags & kEpiBias)) {
+        const int64_t at = Mode == Fp8Mode::kRows ? tile.expert * p.stride_bias : 0;
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 32)
+          bias_ahead[c / 32] =
+              load_as_f32(p.bias, at + min(tile.n0 + half * kHalf + c + lane, p.N - 1), p.dtype_d);
+      }
       // the scales of a group of K blocks: the row's, and its half's weight block's
       float4 ra, ca;
 #pragma unroll 1
@@ -792,15 +805,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tiles are cut, 17.2 us, 19.2 with those in the loop).
         float2 alpha = make_float2(p.alpha, p.alpha);
         if (Mode != Fp8Mode::kK && (p.flags & kEpiBias)) {
-          // the warp's biases through a box (32768 x 4096 x 2048 with GELU: 312
-          // us; loaded by every lane, 16 columns at a time: 355)
+          // the biases to all lanes, by way of a box (each lane loading all of
+          // them, 16 columns at a time: 43 us more)
           float* bias = reinterpret_cast<float*>(boxes);
           if (lane == 0) bulk_wait_group_read<0>();
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 32)
-            bias[c + lane] =
-                load_as_f32(p.bias, bias0 + min(first + c + lane, p.N - 1), p.dtype_d);
+          for (int c = 0; c < kHalf; c += 32) bias[c + lane] = bias_ahead[c / 32];
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < kHalf; c += 4) {

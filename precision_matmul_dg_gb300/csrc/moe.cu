@@ -27,7 +27,7 @@ using namespace fp8;
 //      instruction takes longer: 131 thousand slots 31 us, with ballots 15) and
 //      take the rows from the expert's running count on, in lane order.
 // Bound by latency: the slots are read twice (8 bytes) and written once, a
-// few hundred kilobytes at most.
+// few hundred kilobytes at most (64 slots 3.3 us, 131 thousand 14.6).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxCtas = 8;  // the portable cluster size
@@ -258,7 +258,9 @@ struct RowsParams {
   int64_t row_blocks;        // combine_backward: CTAs past the tokens' that clear padding rows
 };
 
-// D[r] = X[row_slot[r] / top_k], zeros without a slot: a warp per row.
+// D[r] = X[row_slot[r] / top_k], zeros without a slot: a warp per row.  Bound by
+// the stores (16384 tokens of 2048 to 139 thousand rows: 130 us, 4390 GB/s
+// written; 4096 tokens to 16384 rows, about L2's size: 21.8 us).
 __global__ void __launch_bounds__(kRowThreads)
     dispatch_kernel(const __grid_constant__ RowsParams p) {
   grid_dependency_wait();
@@ -280,7 +282,9 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // codes[r], scales[r] = those of X's row row_slot[r] / top_k (codes 0 and the
-// scale of an empty block without a slot): a warp per row.
+// scale of an empty block without a slot): a warp per row.  Bound by the stores
+// (16384 tokens of 2048 to 139 thousand rows: 77 us with the tokens'
+// quantization, 3820 GB/s written; clearing a buffer reaches 4060).
 struct CodesParams {
   const uint8_t* X;  // codes of the tokens, pitch ldx bytes, a multiple of 16
   int64_t ldx;
@@ -328,7 +332,9 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // D[t] = sum over j of weights[t, j] * Y[slot_row[t, j]]: a thread takes eight
 // columns of one token and loads kInFlight of its rows at a time; FP32 sums
-// in the order of j.
+// in the order of j.  Bound by memory: the rows are read once (8192 tokens of
+// 4096 in 8 rows each, this and the gradient below: 371 us, 6510 GB/s; 8
+// tokens 2.6 us).
 constexpr int kInFlight = 8;
 
 template <typename T>
