@@ -929,26 +929,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // D as a stack of `count` matrices: boxes of 32 rows x 128 bytes, 128-byte
-// swizzle.  Kept per thread as tc::make_map_2d keeps its maps.
+// swizzle.
 cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int64_t rows,
                          int64_t cols, int64_t ld, int64_t count, int64_t stride) {
-  struct Entry {
-    const void* base;
-    int64_t rows, cols, ld, count, stride;
-    int dtype;
-    CUtensorMap map;
-  };
-  constexpr int kCache = 16;
-  thread_local Entry cache[kCache];
-  thread_local int used = 0, next = 0;
-  for (int i = 0; i < used; ++i) {
-    const Entry& c = cache[i];
-    if (c.base == base && c.rows == rows && c.cols == cols && c.ld == ld && c.count == count &&
-        c.stride == stride && c.dtype == static_cast<int>(dtype)) {
-      *map = c.map;
-      return cudaSuccess;
-    }
-  }
   tc::EncodeTiledFn fn = tc::encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const int z = dtype == DG_F32 ? 4 : 2;
@@ -964,11 +947,7 @@ cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int
   const CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  cache[next] = Entry{base, rows, cols, ld, count, stride, static_cast<int>(dtype), *map};
-  next = (next + 1) % kCache;
-  if (used < kCache) ++used;
-  return cudaSuccess;
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <Fp8Mode Mode, int BN, int Stages, bool ColScale, bool Split = false>
@@ -980,13 +959,13 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
                         ? static_cast<int>((a.M + 7) / 8 * 8)
                         : kRowsPerCta;
   CUtensorMap ta, tb;
-  cudaError_t e = tc::make_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, a.M, a.K, a.lda, box_a,
-                                  128, CU_TENSOR_MAP_SWIZZLE_128B);
+  cudaError_t e = tc::encode_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, a.M, a.K, a.lda,
+                                    box_a, 128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   const int64_t b_pitch = Mode == Fp8Mode::kRows ? a.stride_b / a.ldb : 0;
   const int64_t b_rows = Mode == Fp8Mode::kRows ? (a.count - 1) * b_pitch + a.N : a.N;
-  e = tc::make_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, b_rows, a.K, a.ldb, BN, 128,
-                      CU_TENSOR_MAP_SWIZZLE_128B);
+  e = tc::encode_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, b_rows, a.K, a.ldb, BN, 128,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   F8Params p;
   p.M = static_cast<int>(a.M);
@@ -1042,8 +1021,8 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
   if (p.vec_a) {
     // whole groups: they end within the row's pitch, a multiple of four
     const int64_t width = (p.k_blocks + kScaleGroup - 1) / kScaleGroup * kScaleGroup;
-    e = tc::make_map_2d(&tsa, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.sa, a.M, width, a.lds_a * 4,
-                        kRowsPerCta, kScaleGroup, CU_TENSOR_MAP_SWIZZLE_NONE);
+    e = tc::encode_map_2d(&tsa, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.sa, a.M, width, a.lds_a * 4,
+                          kRowsPerCta, kScaleGroup, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
   }
 

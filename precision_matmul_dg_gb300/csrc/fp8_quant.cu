@@ -69,8 +69,9 @@ __device__ __forceinline__ void store_codes16(const uint32_t (&w)[8], const Bloc
 
 // Row form, 1 x 128 blocks.  Eight lanes take a block, 16 values (32 bytes)
 // each; 2^log2_tpr threads share a row, and each thread has kRows rows in
-// flight (8192 x 4096: 15.2 us, 6640 GB/s; 16 x 4096 1.8 us).  With a gather (row_slot), row r is X's row row_slot[r] / top_k,
-// or zeros when the slot is -1 or past the tokens.
+// flight (8192 x 4096: 15.2 us, 6640 GB/s; 16 x 4096 1.8 us).  With a gather
+// (row_slot), row r is X's row row_slot[r] / top_k, or zeros when the slot is -1
+// or past the tokens.
 constexpr int kRows = 2;
 
 struct RowParams {

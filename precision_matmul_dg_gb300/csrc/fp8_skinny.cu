@@ -367,11 +367,11 @@ cudaError_t run_skinny(const Fp8Args& a, SkinnyParams p) {
     const int64_t pitch = p.offsets ? a.stride_b / a.ldb : 0;
     p.b_rows = static_cast<int>(pitch);
     const int64_t b_rows = p.offsets ? (a.count - 1) * pitch + a.N : a.N;
-    e = tc::make_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, a.M, a.K, a.lda, L::kRowsX, kBlock,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
+    e = tc::encode_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, a.M, a.K, a.lda, L::kRowsX,
+                          kBlock, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    e = tc::make_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, b_rows, a.K, a.ldb, L::kRowsW,
-                        kBlock, CU_TENSOR_MAP_SWIZZLE_128B);
+    e = tc::encode_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, b_rows, a.K, a.ldb, L::kRowsW,
+                          kBlock, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
   auto kern = skinny_fp8_kernel<NT, RG>;

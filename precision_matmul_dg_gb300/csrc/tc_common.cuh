@@ -378,7 +378,23 @@ inline EncodeTiledFn encode_fn() {
 
 // 2-D tensor map over `rows` rows of `inner` elements (row pitch `pitch_bytes`),
 // box of box_rows x box_inner elements, zero fill outside the tensor.
-// Encoded maps are kept in a small per-thread cache keyed by every argument
+inline cudaError_t encode_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                                 int64_t rows, int64_t inner, int64_t pitch_bytes, int box_rows,
+                                 int box_inner, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner),
+                             static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// encode_map_2d's map.  Encoded maps are kept in a small per-thread cache keyed by every argument
 // (a map holds only an address and a layout, so a hit is always valid).
 inline cudaError_t make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                                int64_t rows, int64_t inner, int64_t pitch_bytes, int box_rows,
@@ -401,17 +417,9 @@ inline cudaError_t make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, cons
       return cudaSuccess;
     }
   }
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner),
-                             static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  const cudaError_t r = encode_map_2d(map, dtype, base, rows, inner, pitch_bytes, box_rows,
+                                      box_inner, swizzle);
+  if (r != cudaSuccess) return r;
   Entry& e = cache[next];
   e.base = base;
   e.rows = rows;
