@@ -550,15 +550,27 @@ dg_status dg_moe_dispatch(int64_t tokens, int64_t top_k, int64_t width, dg_dtype
                           void *D, int64_t ldd, dg_stream_t stream);
 
 /* The same, quantized on the way (dg_quantize_fp8 with 1 x 128 blocks): the
- * operand of dg_gemm_fp8_grouped without a 16-bit copy in between.  Where
- * tokens have two or more rows and rows * width is 2^23 or more, the tokens are
- * quantized first, into a per-(device, stream) workspace that grows with
- * cudaMalloc (under CUDA-graph capture, make one call of the same sizes on the
- * capturing stream before capture begins). */
+ * operand of dg_gemm_fp8_grouped without a 16-bit copy in between.  One launch;
+ * nothing is allocated. */
 dg_status dg_moe_dispatch_fp8(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
                               const void *X, int64_t ldx, int64_t rows, const int32_t *row_slot,
                               void *codes, int64_t ldq, float *scales, int64_t lds,
                               dg_stream_t stream);
+
+/* The same with the caller's scratch, in which the tokens are quantized once
+ * before their rows are copied from there: half the time for large calls (two
+ * launches).  dg_moe_dispatch_fp8_scratch gives the bytes that sizes want: 0
+ * where row by row is as fast, -1 for invalid sizes.
+ *   scratch: device memory, 16-byte aligned, of at least that many bytes, whose
+ *     contents the call overwrites; it must stay until the stream has passed the
+ *     call, and as long as a graph that captured it is replayed.  NULL: row by
+ *     row, as dg_moe_dispatch_fp8.  The results are the same bits. */
+int64_t dg_moe_dispatch_fp8_scratch(int64_t tokens, int64_t top_k, int64_t width, int64_t rows);
+dg_status dg_moe_dispatch_fp8_ex(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
+                                 const void *X, int64_t ldx, int64_t rows,
+                                 const int32_t *row_slot, void *codes, int64_t ldq, float *scales,
+                                 int64_t lds, void *scratch, int64_t scratch_bytes,
+                                 dg_stream_t stream);
 
 /* The way back: D[t,:] = sum over j of weights[t,j] * Y[slot_row[t,j],:] in
  * FP32, in the order of j, rounded once; dropped slots (and rows outside [0,

@@ -39,6 +39,7 @@ EXPORTS = ["dg_query_hw", "dg_plan_tiles", "dg_gemm", "dg_gemm_planned", "dg_gem
            "dg_quantize_mxf4", "dg_gemm_mxf4", "dg_gemm_mxf4_planned",
            "dg_quantize_fp8", "dg_gemm_fp8", "dg_gemm_fp8_grouped", "dg_gemm_fp8_grouped_wgrad",
            "dg_moe_rows", "dg_moe_sort", "dg_moe_dispatch", "dg_moe_dispatch_fp8",
+           "dg_moe_dispatch_fp8_scratch", "dg_moe_dispatch_fp8_ex",
            "dg_moe_combine", "dg_moe_combine_backward",
            "dg_gemm_thin_noalloc", "dg_last_error",
            "dg_check_status", "dg_set_wait_timeout_ns", "dg_selftest_wait_timeout",
@@ -159,6 +160,10 @@ def lib():
     L.dg_moe_sort.argtypes = [i64, i64, i64, vp, i64, i64, vp, vp, vp, vp]
     L.dg_moe_dispatch.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp]
     L.dg_moe_dispatch_fp8.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, i64, vp]
+    L.dg_moe_dispatch_fp8_scratch.argtypes = [i64, i64, i64, i64]
+    L.dg_moe_dispatch_fp8_scratch.restype = ctypes.c_int64
+    L.dg_moe_dispatch_fp8_ex.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, i64, vp,
+                                         i64, vp]
     L.dg_moe_combine.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, vp]
     L.dg_moe_combine_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, vp, vp,
                                           vp, i64, vp, vp]
@@ -175,8 +180,8 @@ def lib():
                  "dg_gemm_grouped", "dg_quantize_mxf4", "dg_gemm_mxf4", "dg_gemm_mxf4_planned",
                  "dg_quantize_fp8", "dg_gemm_fp8", "dg_gemm_fp8_grouped",
                  "dg_gemm_fp8_grouped_wgrad", "dg_moe_sort", "dg_moe_dispatch",
-                 "dg_moe_dispatch_fp8", "dg_moe_combine", "dg_moe_combine_backward",
-                 "dg_check_status",
+                 "dg_moe_dispatch_fp8", "dg_moe_dispatch_fp8_ex", "dg_moe_combine",
+                 "dg_moe_combine_backward", "dg_check_status",
                  "dg_set_wait_timeout_ns", "dg_selftest_wait_timeout", "dg_shutdown"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -845,9 +850,27 @@ def moe_dispatch(X, row_slot, top_k, D, stream=None):
     return D
 
 
+_SCRATCH_FROM = 1 << 23  # rows * width below which dg_moe_dispatch_fp8_scratch asks for nothing
+
+
+def _scratch(torch, nbytes, device, stream):
+    """nbytes of device memory for one call on `stream`: from torch's allocator
+    for that stream (while torch.cuda.graph captures it, from the graph's pool),
+    so its next user comes after the call and a graph keeps what it captured."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def moe_dispatch_fp8(X, row_slot, top_k, codes, scales, stream=None):
     """moe_dispatch and quantize_fp8 in one: codes float8_e4m3fn [rows, width],
-    scales float32 [rows, ceil(width / 128)]."""
+    scales float32 [rows, ceil(width / 128)].  Large calls quantize the tokens
+    once, in scratch from torch's allocator (dg_moe_dispatch_fp8_ex)."""
     torch = (_FP or _fp())[0]
     code = _float_code(X, "X")
     sx = _rows(X, X.dtype, "X")
@@ -856,9 +879,15 @@ def moe_dispatch_fp8(X, row_slot, top_k, codes, scales, stream=None):
     _rows(row_slot, torch.int32, "row_slot", None, 1)
     sq = _rows(codes, torch.float8_e4m3fn, "codes", (rows, width))
     ss = _rows(scales, torch.float32, "scales", (rows, (width + 127) // 128))
-    _check(lib().dg_moe_dispatch_fp8(tokens, top_k, width, code, X.data_ptr(), sx[0], rows,
-                                     row_slot.data_ptr(), codes.data_ptr(), sq[0],
-                                     scales.data_ptr(), ss[0], _stream_of(X, stream)))
+    scratch, nbytes = None, 0
+    if rows * width >= _SCRATCH_FROM:
+        nbytes = lib().dg_moe_dispatch_fp8_scratch(tokens, top_k, width, rows)
+        if nbytes > 0:
+            scratch = _scratch(torch, nbytes, X.device, stream)
+    _check(lib().dg_moe_dispatch_fp8_ex(
+        tokens, top_k, width, code, X.data_ptr(), sx[0], rows, row_slot.data_ptr(),
+        codes.data_ptr(), sq[0], scales.data_ptr(), ss[0],
+        None if scratch is None else scratch.data_ptr(), max(nbytes, 0), _stream_of(X, stream)))
     return codes, scales
 
 

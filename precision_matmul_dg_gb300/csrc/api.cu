@@ -765,18 +765,10 @@ dg_status set_errorf(dg_status s, const char* fmt, ...) {
 
 dg_status set_cuda_error(cudaError_t e, const char* what) { return fail_cuda(e, what); }
 
-dg_status get_scratch(int dev, cudaStream_t stream, int64_t bytes, void** out) {
-  __half* p = nullptr;
-  const dg_status s = get_wide_workspace(dev, stream, (bytes + 1) / 2, &p);
-  *out = p;
-  return s;
-}
-
 dg_status call_context(CallContext* out) {
   DeviceState* st = nullptr;
   const dg_status s = device_state(&st);
   if (s != DG_OK) return s;
-  cudaGetDevice(&out->dev);
   out->status = st->status;
   out->timeout_ns = timeout_ns();
   out->sm_count = st->hw.sm_count;

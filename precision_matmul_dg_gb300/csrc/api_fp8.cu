@@ -95,6 +95,17 @@ dg_status launched(cudaError_t e, const char* what) {
   return set_cuda_error(e, what);
 }
 
+// Bytes of scratch for a dispatch that quantizes the tokens before it copies
+// their rows; 0 where it quantizes row by row.  Each row quantized by itself
+// does a token's work up to top_k times, which for large calls is the larger
+// part (16384 tokens of 2048 to 139 thousand rows: 150 us, the tokens once 77;
+// with the sort, 512 tokens to 4096 rows 11.9 us against 9.9, 256 to 2048 9.2
+// either way).
+int64_t dispatch_scratch(int64_t tokens, int64_t width, int64_t rows) {
+  if (tokens <= 0 || rows < 2 * tokens || rows * width < (int64_t(1) << 23)) return 0;
+  return tokens * (ceil_div(width, 16) * 16 + 4 * ceil_div(width, kFp8Block));
+}
+
 void fill_context(Fp8Args* a, const CallContext& c) {
   a->status = c.status;
   a->timeout_ns = c.timeout_ns;
@@ -374,10 +385,25 @@ dg_status dg_moe_dispatch(int64_t tokens, int64_t top_k, int64_t width, dg_dtype
                   "dispatch launch");
 }
 
+int64_t dg_moe_dispatch_fp8_scratch(int64_t tokens, int64_t top_k, int64_t width, int64_t rows) {
+  clear_error();
+  if (check_routing(tokens, top_k, rows) != DG_OK || check_sizes(width, 0, 0) != DG_OK) return -1;
+  return dispatch_scratch(tokens, width, rows);
+}
+
 dg_status dg_moe_dispatch_fp8(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
                               const void* X, int64_t ldx, int64_t rows, const int32_t* row_slot,
                               void* codes, int64_t ldq, float* scales, int64_t lds,
                               dg_stream_t stream) {
+  return dg_moe_dispatch_fp8_ex(tokens, top_k, width, dtype, X, ldx, rows, row_slot, codes, ldq,
+                                scales, lds, nullptr, 0, stream);
+}
+
+dg_status dg_moe_dispatch_fp8_ex(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
+                                 const void* X, int64_t ldx, int64_t rows,
+                                 const int32_t* row_slot, void* codes, int64_t ldq, float* scales,
+                                 int64_t lds, void* scratch, int64_t scratch_bytes,
+                                 dg_stream_t stream) {
   clear_error();
   dg_status s = check_routing(tokens, top_k, rows);
   if (s == DG_OK) s = check_sizes(width, 0, 0);
@@ -387,6 +413,11 @@ dg_status dg_moe_dispatch_fp8(int64_t tokens, int64_t top_k, int64_t width, dg_d
   if (!row_slot || !aligned4(row_slot)) return bad("row_slot is null or not 4-byte aligned");
   if (tokens > 0 && (s = check_rows16("X", X, ldx, width)) != DG_OK) return s;
   if ((s = check_fp8("the codes", codes, ldq, width, scales, lds)) != DG_OK) return s;
+  const int64_t need = scratch ? dispatch_scratch(tokens, width, rows) : 0;
+  if (scratch && !aligned16(scratch)) return bad("the scratch is not 16-byte aligned");
+  if (scratch_bytes < need)
+    return set_errorf(DG_ERR_INVALID_ARG, "%lld bytes of scratch, need %lld",
+                      (long long)scratch_bytes, (long long)need);
   CallContext c;
   if ((s = call_context(&c)) != DG_OK) return s;
   Fp8RowsJob j;
@@ -403,16 +434,8 @@ dg_status dg_moe_dispatch_fp8(int64_t tokens, int64_t top_k, int64_t width, dg_d
   j.top_k = top_k;
   j.tokens = tokens;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Each row quantized by itself does a token's work up to top_k times.  Where
-  // that is the larger part, the tokens are quantized once into scratch and
-  // the rows copied from there (16384 tokens of 2048 to 139 thousand rows: 77
-  // us against 150; with the sort, 512 tokens to 4096 rows 9.9 us against
-  // 11.9, 256 to 2048 9.2 either way).
-  if (rows >= 2 * tokens && tokens > 0 && rows * width >= (int64_t(1) << 23)) {
+  if (need > 0) {
     const int64_t pitch = ceil_div(width, 16) * 16, blocks = ceil_div(width, kFp8Block);
-    void* scratch = nullptr;
-    s = get_scratch(c.dev, st, tokens * (pitch + 4 * blocks), &scratch);
-    if (s != DG_OK) return s;
     Fp8RowsJob q = j;
     q.rows = tokens;
     q.codes = scratch;

@@ -345,15 +345,11 @@ int64_t gemv_counter_elems(const dg_tile_plan& plan, int64_t N, int64_t batch);
 // What a launcher outside api.cu needs of the current device: its status word,
 // the wait limit in force and its SM count.
 struct CallContext {
-  int dev;
   int* status;
   uint64_t timeout_ns;
   int sm_count;
 };
 dg_status call_context(CallContext* out);
-// Scratch of at least `bytes` bytes on (device, stream), shared with the
-// widened operands: for data that the same call writes and reads.
-dg_status get_scratch(int dev, cudaStream_t stream, int64_t bytes, void** out);
 
 // Kernel-launch counter and error state (api.cu).  None of these allocate.
 void count_launches(int n);
