@@ -608,22 +608,36 @@ def gemm_host(A, B, D, C=None, K=None, bias=None, alpha=1.0, beta=0.0, epilogue=
 
 _FP = None  # (torch, {16-bit and 32-bit float dtype: code}), built on first use
 _raw_stream = None
+_gpus = 0  # that torch sees
 
 
 def _fp():
-    global _FP, _raw_stream
+    global _FP, _raw_stream, _gpus
     if _FP is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _gpus = torch.cuda.device_count()
         _FP = (torch, {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
     return _FP
 
 
-def _stream_of(t, stream):
-    """The handle of `stream`, by default the current one of t's device (as
-    torch.cuda.current_stream, whose Stream object costs more than a launch)."""
+def _same_gpu(torch, tensors):
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("tensors must be on the current GPU (cuda:%d), got one on %s" % (
+                device, t.device))
+
+
+def _stream_of(stream, *tensors):
+    """The handle of `stream`, by default the current one (as
+    torch.cuda.current_stream, whose Stream object costs more than a launch),
+    for a call on these CUDA tensors (None: not given), which must be on the
+    current GPU, where the library launches.  (Where there is one GPU, they are.)"""
+    if _gpus != 1:
+        _same_gpu(_FP[0], tensors)
     if stream is None and _raw_stream is not None:
-        return _raw_stream(t.get_device())
+        return _raw_stream(tensors[0].get_device())
     return _stream_handle(stream)
 
 
@@ -699,7 +713,7 @@ def quantize_fp8(X, form="rows", block_rows=1, out=None, stream=None):
     elif form == "transposed":
         args = none + args
     _check(lib().dg_quantize_fp8(rows, K, code, X.data_ptr(), sx[0], block_rows, *args,
-                                 _stream_of(X, stream)))
+                                 _stream_of(stream, X, *out)))
     return out
 
 
@@ -724,14 +738,13 @@ def gemm_fp8(A, scale_a, B, scale_b, D, bias=None, alpha=1.0, beta=0.0, epilogue
             scale_a.shape[1] < kb or scale_b.shape[1] < kb or nb not in (N, (N + 127) // 128):
         raise ValueError("shape mismatch: A %s with %s, B %s with %s, D %s" % tuple(
             tuple(t.shape) for t in (A, scale_a, B, scale_b, D)))
-    if bias is not None and (bias.dtype is not D.dtype or bias.shape != (N,) or
-                             (N > 1 and bias.stride(0) != 1)):
-        raise ValueError("bias must be [N] of D's type")
+    if bias is not None:
+        _rows(bias, D.dtype, "bias", (N,), 1)
     _check(lib().dg_gemm_fp8(
         M, N, K, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[0],
         scale_b.data_ptr(), zb[0], 1 if nb == N else 128, D.data_ptr(), dt, sd[0],
         None if bias is None else bias.data_ptr(), alpha, beta, _epi_code(epilogue),
-        _stream_of(D, stream)))
+        _stream_of(stream, A, scale_a, B, scale_b, D, bias)))
     return D
 
 
@@ -765,7 +778,7 @@ def gemm_fp8_grouped(A, scale_a, B, scale_b, offsets, D, bias=None, alpha=1.0, b
         count, rows, N, K, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[1],
         sb[0], scale_b.data_ptr(), zb[1], zb[0], offsets.data_ptr(), D.data_ptr(), dt, sd[0],
         None if bias is None else bias.data_ptr(), stride_bias, alpha, beta, _epi_code(epilogue),
-        _stream_of(D, stream)))
+        _stream_of(stream, A, scale_a, B, scale_b, offsets, D, bias)))
     return D
 
 
@@ -792,7 +805,7 @@ def gemm_fp8_grouped_wgrad(A, scale_a, B, scale_b, offsets, D, alpha=1.0, beta=0
     _check(lib().dg_gemm_fp8_grouped_wgrad(
         count, M, N, rows, A.data_ptr(), sa[0], scale_a.data_ptr(), za[0], B.data_ptr(), sb[0],
         scale_b.data_ptr(), zb[0], offsets.data_ptr(), D.data_ptr(), dt, sd[1], sd[0], alpha, beta,
-        _stream_of(D, stream)))
+        _stream_of(stream, A, scale_a, B, scale_b, offsets, D)))
     return D
 
 
@@ -829,7 +842,7 @@ def moe_sort(ids, count, align=1, out=None, stream=None):
         raise ValueError("offsets must be [count + 1], slot_row contiguous like ids")
     _check(lib().dg_moe_sort(tokens, top_k, count, ids.data_ptr(), align, row_slot.shape[0],
                              offsets.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
-                             _stream_of(ids, stream)))
+                             _stream_of(stream, ids, offsets, row_slot, slot_row)))
     return out
 
 
@@ -846,7 +859,7 @@ def moe_dispatch(X, row_slot, top_k, D, stream=None):
     sd = _rows(D, X.dtype, "D", (rows, width))
     _check(lib().dg_moe_dispatch(tokens, top_k, width, code, X.data_ptr(), sx[0], rows,
                                  row_slot.data_ptr(), D.data_ptr(), sd[0],
-                                 _stream_of(X, stream)))
+                                 _stream_of(stream, X, row_slot, D)))
     return D
 
 
@@ -879,6 +892,7 @@ def moe_dispatch_fp8(X, row_slot, top_k, codes, scales, stream=None):
     _rows(row_slot, torch.int32, "row_slot", None, 1)
     sq = _rows(codes, torch.float8_e4m3fn, "codes", (rows, width))
     ss = _rows(scales, torch.float32, "scales", (rows, (width + 127) // 128))
+    handle = _stream_of(stream, X, row_slot, codes, scales)
     scratch, nbytes = None, 0
     if rows * width >= _SCRATCH_FROM:
         nbytes = lib().dg_moe_dispatch_fp8_scratch(tokens, top_k, width, rows)
@@ -887,7 +901,7 @@ def moe_dispatch_fp8(X, row_slot, top_k, codes, scales, stream=None):
     _check(lib().dg_moe_dispatch_fp8_ex(
         tokens, top_k, width, code, X.data_ptr(), sx[0], rows, row_slot.data_ptr(),
         codes.data_ptr(), sq[0], scales.data_ptr(), ss[0],
-        None if scratch is None else scratch.data_ptr(), max(nbytes, 0), _stream_of(X, stream)))
+        None if scratch is None else scratch.data_ptr(), max(nbytes, 0), handle))
     return codes, scales
 
 
@@ -909,7 +923,7 @@ def moe_combine(Y, slot_row, D, weights=None, stream=None):
     _check(lib().dg_moe_combine(tokens, top_k, width, code, Y.data_ptr(), sy[0], Y.shape[0],
                                 slot_row.data_ptr(),
                                 None if weights is None else weights.data_ptr(), D.data_ptr(),
-                                sd[0], _stream_of(Y, stream)))
+                                sd[0], _stream_of(stream, Y, slot_row, D, weights)))
     return D
 
 
@@ -944,7 +958,9 @@ def moe_combine_backward(dD, Y, slot_row, row_slot, weights, dY, dweights=None, 
         tokens, top_k, width, code, dD.data_ptr(), s_dd[0],
         None if dweights is None else Y.data_ptr(), s_y[0], rows, row_slot.data_ptr(),
         slot_row.data_ptr(), None if weights is None else weights.data_ptr(), dY.data_ptr(),
-        s_dy[0], None if dweights is None else dweights.data_ptr(), _stream_of(dD, stream)))
+        s_dy[0], None if dweights is None else dweights.data_ptr(),
+        _stream_of(stream, dD, None if dweights is None else Y, slot_row, row_slot, weights, dY,
+                   dweights)))
     return dY, dweights
 
 
