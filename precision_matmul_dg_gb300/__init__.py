@@ -892,16 +892,16 @@ def moe_dispatch_fp8(X, row_slot, top_k, codes, scales, stream=None):
     _rows(row_slot, torch.int32, "row_slot", None, 1)
     sq = _rows(codes, torch.float8_e4m3fn, "codes", (rows, width))
     ss = _rows(scales, torch.float32, "scales", (rows, (width + 127) // 128))
+    args = (tokens, top_k, width, code, X.data_ptr(), sx[0], rows, row_slot.data_ptr(),
+            codes.data_ptr(), sq[0], scales.data_ptr(), ss[0])
     handle = _stream_of(stream, X, row_slot, codes, scales)
-    scratch, nbytes = None, 0
     if rows * width >= _SCRATCH_FROM:
         nbytes = lib().dg_moe_dispatch_fp8_scratch(tokens, top_k, width, rows)
         if nbytes > 0:
             scratch = _scratch(torch, nbytes, X.device, stream)
-    _check(lib().dg_moe_dispatch_fp8_ex(
-        tokens, top_k, width, code, X.data_ptr(), sx[0], rows, row_slot.data_ptr(),
-        codes.data_ptr(), sq[0], scales.data_ptr(), ss[0],
-        None if scratch is None else scratch.data_ptr(), max(nbytes, 0), handle))
+            _check(lib().dg_moe_dispatch_fp8_ex(*args, scratch.data_ptr(), nbytes, handle))
+            return codes, scales
+    _check(lib().dg_moe_dispatch_fp8(*args, handle))
     return codes, scales
 
 
