@@ -950,6 +950,13 @@ cudaError_t make_out_map(CUtensorMap* map, const void* base, dg_dtype dtype, int
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The K blocks of each CTA of a split tile (the last may have fewer, or none):
+// whole groups.
+int share_of_k(int64_t k_blocks, int split) {
+  const int64_t groups = (k_blocks + kScaleGroup - 1) / kScaleGroup;
+  return static_cast<int>((groups + split - 1) / split * kScaleGroup);
+}
+
 template <Fp8Mode Mode, int BN, int Stages, bool ColScale, bool Split = false>
 cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
   using L = F8Smem<BN, Stages, ColScale>;
@@ -977,9 +984,8 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
   const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_blocks *
                         (Mode == Fp8Mode::kK ? a.count : 1);
   p.tiles = static_cast<int>(std::min<int64_t>(tiles, INT32_MAX));
-  const int groups = (p.k_blocks + kScaleGroup - 1) / kScaleGroup;
   p.split = split;
-  p.split_blocks = (groups + split - 1) / split * kScaleGroup;
+  p.split_blocks = share_of_k(p.k_blocks, split);
   p.group_m = 16;
   p.count = Mode == Fp8Mode::kDense ? 0 : static_cast<int>(a.count);
   p.b_rows = static_cast<int>(b_pitch);
@@ -1071,10 +1077,18 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
 // SMs: a K block of the narrow tile costs 0.6 of the wide one's time (4096^3, 512
 // wide tiles or 1024 narrow: 65 us or 77; 2000^3, 128 or 256: 14.6 us or 17.5;
 // 1000 x 2000 x 2000, 64 or 128: 18.0 us or 11.9).  A dense product's narrow
-// tiles are split along K over clusters of two or four CTAs while SMs are left
-// and each keeps five K blocks (256 x 4096 x 8192: 18.2 us, whole 22.2; 64 x
-// 4096 x 4096: 9.7, whole 12.4; 64 x 8000 x 1000, of eight blocks: 9.8 us in
-// halves, whole 6.1).
+// tiles are split along K over clusters of four CTAs, or of two where there are
+// not SMs for four, if that saves the longest share enough K blocks.  Shares are
+// whole scale groups of four blocks, so the last may be shorter or empty.  A
+// cluster costs about 5 us (its launch, two barriers, the sums' way through
+// shared memory) in halves and 4 in quarters; a K block 0.28 us, with column
+// scales 0.44.  Measured in us, whole / split:
+//   halves, 64 x 8000 and 256 x 4096: K = 4096 (16 blocks saved) 12.7 / 13.0, 5120
+//   (20) 15.1 / 14.2, 8192 (32) 22.2 / 17.9; column scales: K = 2816 (10) 13.4 /
+//   13.8, 3584 (12) 15.8 / 15.6, 4096 (16) 17.8 / 15.7;
+//   quarters, 64 x 4096: K = 2560 (12 saved) 8.9 / 9.3, 2816 (14) 9.6 / 9.3, 4096
+//   (24) 12.5 / 9.6; column scales: K = 1536 (8) 8.4 / 9.0, 1792 (10) 9.4 / 9.0,
+//   4096 (24) 17.5 / 11.2.
 template <Fp8Mode Mode, bool ColScale>
 cudaError_t run_shape(const Fp8Args& a) {
   const int64_t row_blocks = (Mode == Fp8Mode::kRows
@@ -1089,9 +1103,11 @@ cudaError_t run_shape(const Fp8Args& a) {
   if constexpr (Mode == Fp8Mode::kDense) {
     const int64_t tiles = row_blocks * ((a.N + 127) / 128);
     const int64_t k_blocks = (a.K + kBlock - 1) / kBlock;
-    int split = 1;
-    while (split < 4 && tiles * split * 2 <= a.sm_count && k_blocks >= split * 2 * 5) split *= 2;
-    if (split > 1) return run_fp8<Mode, 128, 5, ColScale, true>(a, split);
+    const int split = tiles * 4 <= a.sm_count ? 4 : 2;
+    const int64_t saved = k_blocks - share_of_k(k_blocks, split);
+    const int64_t enough = split == 4 ? (ColScale ? 10 : 14) : (ColScale ? 12 : 18);
+    if (tiles * split <= a.sm_count && saved >= enough)
+      return run_fp8<Mode, 128, 5, ColScale, true>(a, split);
   }
   return run_fp8<Mode, 128, 5, ColScale>(a);
 }
