@@ -8,6 +8,7 @@ runtime linked statically.  Objects go to precision_matmul_dg_gb300/_build/.
 """
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -28,6 +29,12 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
           "-I", INCLUDE, "-I", CSRC]
 
 
+# Sources whose kernels divide their launch's registers among warpgroups: the
+# shares hold for the constant kLaunchRegs only, which ptxas has to give every
+# kernel (with another count the library refuses to launch them).
+FIXED_REGS = ["fp8_gemm.cu"]
+
+
 def nvcc():
     exe = shutil.which("nvcc")
     if exe:
@@ -41,13 +48,23 @@ def nvcc():
 def _compile(src, verbose_ptxas=False):
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     cmd = [nvcc()] + ARCH + COMMON
-    if verbose_ptxas and src.endswith(".cu"):
+    if (verbose_ptxas and src.endswith(".cu")) or src in FIXED_REGS:
         cmd += ["-Xptxas", "-v"]
     if src.endswith(".cpp"):
         cmd += ["-x", "cu"]  # host-only C++, compiled through nvcc for one toolchain
     cmd += ["-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     return src, obj, r.returncode, r.stdout + r.stderr
+
+
+def check_registers(src, text, output):
+    """Raises unless every kernel in ptxas's output has the kLaunchRegs registers
+    that the source text names."""
+    want = int(re.search(r"kLaunchRegs = (\d+)", text).group(1))
+    got = [int(n) for n in re.findall(r"Used (\d+) registers", output)]
+    if not got or any(n != want for n in got):
+        raise RuntimeError("%s: ptxas gave its kernels %s registers, the warpgroups' shares need %d "
+                           "in each" % (src, sorted(set(got)), want))
 
 
 def _stale(objs):
@@ -71,6 +88,9 @@ def build(force=False, verbose_ptxas=False, quiet=True):
             sys.stderr.write("---- %s ----\n%s\n" % (src, out))
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(r[0] for r in failed))
+    for src, _, _, out in results:
+        if src in FIXED_REGS:
+            check_registers(src, open(os.path.join(CSRC, src)).read(), out)
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + [r[1] for r in results]
     r = subprocess.run(cmd, capture_output=True, text=True)
