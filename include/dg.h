@@ -475,9 +475,10 @@ dg_status dg_quantize_fp8(int64_t rows, int64_t K, dg_dtype dtype_x, const void 
  *     N .. ldd - 1 are never touched).  bias: [N] of dtype_d, read only by the
  *     bias epilogues.  Epilogues as dg_gemm.
  *   M == 0 or N == 0 is a no-op; K == 0 gives epilogue(beta * D).
- * Few rows (M <= 32) run a kernel that streams the weights through shared
- * memory into warp-level MMAs; more run on tcgen05 with the block sums scaled
- * and added in registers.  Results are bit-stable; nothing is allocated.
+ * Few rows (up to 8, or to 32 where N and K are small enough) run a kernel that
+ * streams the weights through shared memory into warp-level MMAs; more run on
+ * tcgen05 with the block sums scaled and added in registers.  Results are
+ * bit-stable; nothing is allocated.
  * Errors: as dg_gemm, with these rules. */
 dg_status dg_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
                       const float *scale_a, int64_t lds_a, const void *B, int64_t ldb,

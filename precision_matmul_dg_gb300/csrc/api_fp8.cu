@@ -106,6 +106,36 @@ int64_t dispatch_scratch(int64_t tokens, int64_t width, int64_t rows) {
   return tokens * (ceil_div(width, 16) * 16 + 4 * ceil_div(width, kFp8Block));
 }
 
+// Whether a product of M rows goes to launch_fp8_skinny.  Its time grows with
+// the rounds of 64 weight rows over the SMs (smaller tiles where those are
+// few) and with each 8 rows; the tensor-core kernel's does not up to 128 rows,
+// and is longer with 1 x 128 blocks in B.  Measured in us, weights from HBM,
+// few-rows kernel / tensor-core kernel:
+//   8 rows: 4096 x 8192 8.8 / 13.0, 12288 x 4096 14.1 / 14.1, 28672 x 8192 37 / 45;
+//   16 rows: 8192 x 8192 17.1 / 19.2, 9600 x 4096 (150 tiles) 11.2 / 13.5, 9792 x
+//   4096 (153) 17.9 / 13.6, its 1 x 128 form 18.2 / 18.6;
+//   32 rows: 2400 x 8192 10.7 / 12.2, 4096 x 4096 10.2 / 10.3, 4096 x 8192 15.5 /
+//   13.3, 8960 x 1536 9.1 / 7.4, its 1 x 128 form 9.1 / 9.1.
+bool few_rows(int64_t M, int64_t N, int64_t K, int block_rows_b, int sm_count) {
+  const int64_t t64 = ceil_div(N, 64), t32 = ceil_div(N, 32);
+  if (M <= 8) return true;
+  if (block_rows_b == 1) return M <= 16 || (M <= 32 && t64 <= sm_count);
+  if (M <= 16) return t64 <= sm_count;
+  return M <= 32 && 2 * t64 < sm_count && (2 * t32 < sm_count || N * K <= (int64_t(1) << 24));
+}
+// The same for experts' rows, by their mean: an expert with more than 8, 16 or
+// 32 reads its weights again, the more often the more tiles there are.  Rows
+// each at random, us: 64 experts of 4096 x 2048, 2 rows each 74.8 / 77.2, 4 86.6 /
+// 89.0, 8 119 / 91.7, 16 160 / 93.6; 8 of 2048 x 2048 (256 tiles of 64), 6 8.6 /
+// 13.5, 8 11.5 / 10.1; 4 of 2048 x 2048 (128 tiles), 12 6.7 / 9.6, 16 11.0 / 9.1.
+// (Many experts of short K gain less: 128 of 2048 x 768, 2 rows each 48.7 / 40.8.)
+bool few_rows_each(int64_t count, int64_t rows, int64_t N, int64_t K, int sm_count) {
+  if (count == 1) return few_rows(rows, N, K, kFp8Block, sm_count);
+  const int64_t tiles = std::min(count, rows) * ceil_div(N, 64);
+  const int64_t most = tiles <= sm_count ? 12 : tiles <= 2 * sm_count ? 6 : 4;
+  return rows <= most * count;
+}
+
 void fill_context(Fp8Args* a, const CallContext& c) {
   a->status = c.status;
   a->timeout_ns = c.timeout_ns;
@@ -201,7 +231,8 @@ dg_status dg_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t ld
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   fill_context(&a, c);
   // K == 0 (only the epilogue is left) has no operands to describe to TMA
-  return launched(M <= kFp8SkinnyRows || K == 0 ? launch_fp8_skinny(a) : launch_fp8_tc(a),
+  return launched(K == 0 || few_rows(M, N, K, block_rows_b, c.sm_count) ? launch_fp8_skinny(a)
+                                                                       : launch_fp8_tc(a),
                   "kernel launch");
 }
 
@@ -262,8 +293,8 @@ dg_status dg_gemm_fp8_grouped(int64_t count, int64_t rows, int64_t N, int64_t K,
   a.beta = beta;
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   fill_context(&a, c);
-  return launched(rows <= kFp8SkinnyRowsEach * count || K == 0 ? launch_fp8_skinny(a)
-                                                           : launch_fp8_tc(a),
+  return launched(K == 0 || few_rows_each(count, rows, N, K, c.sm_count) ? launch_fp8_skinny(a)
+                                                                         : launch_fp8_tc(a),
                   "kernel launch");
 }
 

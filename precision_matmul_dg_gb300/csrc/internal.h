@@ -303,9 +303,6 @@ struct Fp8Args {
 };
 cudaError_t launch_fp8_tc(const Fp8Args& a);      // fp8_gemm.cu: tcgen05
 cudaError_t launch_fp8_skinny(const Fp8Args& a);  // fp8_skinny.cu: few rows (dense or kRows)
-// rows of a dense product, and per expert of a grouped one, up to which
-// launch_fp8_skinny is faster
-constexpr int64_t kFp8SkinnyRows = 32, kFp8SkinnyRowsEach = 16;
 constexpr int64_t kMaxExperts = 1024;
 
 // Expert routing (moe.cu).
