@@ -98,7 +98,7 @@ dg_status launched(cudaError_t e, const char* what) {
 // Bytes of scratch for a dispatch that quantizes the tokens before it copies
 // their rows; 0 where it quantizes row by row.  Each row quantized by itself
 // does a token's work up to top_k times, which for large calls is the larger
-// part (16384 tokens of 2048 to 139 thousand rows: 150 us, the tokens once 77;
+// part (16384 tokens of 2048 to 139 thousand rows: 145 us, the tokens once 77;
 // with the sort, 512 tokens to 4096 rows 11.9 us against 9.9, 256 to 2048 9.2
 // either way).
 int64_t dispatch_scratch(int64_t tokens, int64_t width, int64_t rows) {

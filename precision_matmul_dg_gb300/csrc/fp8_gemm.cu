@@ -27,13 +27,15 @@
 //               transposed, half of them each, or the halves' weight blocks'.
 //
 // What a K block of a 128 x 256 tile takes is about 830 clocks, where its MMAs
-// take 512 and its TMEM loads 560: with two buffers of 256 columns, an MMA waits
-// for the release of the buffer before last, a release for the loads of the
-// last column, and both for an mbarrier's way there (8192^3: 424 us, 67% of the
-// tensor rate; 32768 x 4096 x 2048: 231 us, 64 experts' 32768 rows of the same
-// sizes, whose last tiles are part-filled: 286 us, with GELU 338; FP32 gradients
-// of 64 experts, 4096 x 2048 each: 526 us, 4.07 TB/s of stores, what clearing
-// such a buffer reaches).  Measured with no gain: pairs of CTAs (cta_group::2, half of B
+// take 512 and its TMEM loads 560.  What fills the rest is not settled: an MMA
+// waits for the release of the buffer before last, a release for the loads of
+// the last column, and both for an mbarrier's way there; but the 128 x 128 tile
+// with four buffers takes 0.6 of these clocks, with half the MMAs (8192^3: 458 us
+// a call, 62% of the tensor rate, 425 in graph replays; 32768 x 4096 x 2048: 236
+// us, 64 experts' 32768 rows of the same sizes, whose last tiles are part-filled:
+// 287 us, with GELU 335; FP32 gradients of 64 experts, 4096 x 2048 each: 527 us,
+// 4.07 TB/s of stores, what clearing such a buffer reaches; BF16 gradients 429
+// us).  Measured with no gain: pairs of CTAs (cta_group::2, half of B
 // each), two CTAs per SM with 128 x 128 tiles, a fourth stage, loads of 32
 // columns.
 //
@@ -802,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (col_end == 0 || first >= p.N) continue;
         // Straight through all of the warp's columns, N's or not (experts' gradients
         // 527 us, were 687 in the loop below, 5900 clocks a tile; 2000^3, whose last
-        // tiles are cut, 17.2 us, 19.2 with those in the loop).
+        // tiles are cut, 2 us less than with those in the loop).
         float2 alpha = make_float2(p.alpha, p.alpha);
         if (Mode != Fp8Mode::kK && (p.flags & kEpiBias)) {
           // the biases to all lanes, by way of a box (each lane loading all of
@@ -1075,7 +1077,7 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
 
 // 128 x 256 tiles, except where 128 x 128 tiles take no more rounds over the
 // SMs: a K block of the narrow tile costs 0.6 of the wide one's time (4096^3, 512
-// wide tiles or 1024 narrow: 65 us or 77; 2000^3, 128 or 256: 14.6 us or 17.5;
+// wide tiles or 1024 narrow: 65 us or 77; 2000^3, 128 or 256: 15.0 us or 17.5;
 // 1000 x 2000 x 2000, 64 or 128: 18.0 us or 11.9).  A dense product's narrow
 // tiles are split along K over clusters of four CTAs, or of two where there are
 // not SMs for four, if that saves the longest share enough K blocks.  Shares are

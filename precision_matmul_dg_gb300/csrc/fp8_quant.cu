@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(kThreads)
 // reads 16 values of rows t / 8 + 32 i, makes their row-form codes, and puts
 // them in shared memory; then it takes two columns and a quarter of the rows
 // for the transposed form, whose codes go back through shared memory and out
-// as whole 128-byte lines.  (8192 x 4096, both forms: 29.7 us, 4520 GB/s, one
-// scale per tile 26.1; transposed alone 20.3 us, 4970 GB/s; 8191 rows, whose
-// transposed rows of codes are not aligned, 31.6.  Bound by the phases of a tile
+// as whole 128-byte lines.  (8192 x 4096, both forms: 29.1 us, 4610 GB/s, one
+// scale per tile 25.8; transposed alone 20.0 us, 5030 GB/s; 8191 rows, whose
+// transposed rows of codes are not aligned, 31.3.  Bound by the phases of a tile
 // more than by memory: instructions issue in 49% of the clocks.)
 constexpr int kPitch = kBlock + 8;       // 16-bit elements per shared row
 constexpr int kCodePitch = kBlock + 16;  // bytes per shared column of codes
