@@ -594,6 +594,83 @@ dg_status dg_moe_combine_backward(int64_t tokens, int64_t top_k, int64_t width, 
                                   const float *weights, void *dY, int64_t lddy, float *dweights,
                                   dg_stream_t stream);
 
+/* ------------------------------------- 4-bit float with E4M3 block scales
+ * NVF4 operands are E2M1 codes (sign | 2-bit exponent, bias 1 | 1-bit mantissa;
+ * magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6), two to a byte (k = 2p in the low
+ * nibble of byte p), with one E4M3 scale (a nonnegative E4M3 code) for each
+ * block of 16 values along K and one FP32 scale for each row: a code stands
+ * for e2m1(code) * e4m3(scale) * row_scale.  It is the second block-scaled
+ * 4-bit format of the tensor cores: against DG_MXF4's, half the block and a
+ * scale with a mantissa.
+ *   Codes: rows of ceil(K / 2) bytes (the high nibble after an odd K is 0),
+ *     pitch in bytes, a multiple of 16; 16-byte aligned base.
+ *   Scales: tiles of 128 rows x 4 blocks, 512 bytes each, 16-byte aligned, for
+ *     a matrix ceil(rows / 128) x ceil(K / 64) tiles, tiles along K first:
+ *     line l of a tile (16 bytes) holds the scales of its rows l, 32 + l,
+ *     64 + l and 96 + l, four bytes each.  Bytes of rows and blocks that are
+ *     not there are 0 (in an operand: any E4M3 code but NaN's).
+ *   Stacks of matrices: codes `stride` bytes apart, scales and row scales
+ *     (rows FP32 each) one matrix after another.
+ */
+
+/* Quantization of `count` matrices X (rows x K, FP16 or BF16; row pitch ldx and
+ * stride stride_x in elements, multiples of 8; 16-byte aligned).  A row's scale
+ * is the smallest power of two r >= 2^-100 with 2688 r >= its largest magnitude
+ * (2688 = 6 * 448; a block that holds a NaN or an infinity does not count), or
+ * given[i] where `given` is not NULL.  A block's scale is
+ * max(e4m3(amax / (6 r)), 2^-9), a code e2m1(v / (scale * r)), rounded to
+ * nearest, ties to even, saturated; every quotient and product is FP32.  A
+ * block that holds a NaN or an infinity gets codes 0 and the scale NaN (0x7F);
+ * so does every block of a row whose given scale is not in [2^-100, 2^100].
+ *   row_scales: count x rows FP32, written where `given` is NULL, else unused.
+ * One launch; nothing is allocated; a size of 0 is a no-op.
+ * Errors: DG_ERR_INVALID_ARG for sizes, pointers, pitches or strides that
+ * break these rules; DG_ERR_UNSUPPORTED for another type. */
+dg_status dg_quantize_nvf4(int64_t count, int64_t rows, int64_t K, dg_dtype dtype_x, const void *X,
+                           int64_t ldx, int64_t stride_x, const float *given, void *codes,
+                           int64_t ldq, int64_t stride_q, void *scales, float *row_scales,
+                           dg_stream_t stream);
+
+/* dg_moe_dispatch and dg_quantize_nvf4 in one: the rows of X gathered in sorted
+ * order and quantized, the operand of dg_gemm_nvf4_grouped (rows without a slot
+ * are rows of zeros). */
+dg_status dg_moe_dispatch_nvf4(int64_t tokens, int64_t top_k, int64_t width, dg_dtype dtype,
+                               const void *X, int64_t ldx, int64_t rows, const int32_t *row_slot,
+                               void *codes, int64_t ldq, void *scales, float *row_scales,
+                               dg_stream_t stream);
+
+/* The way back: D (count matrices of rows x K, FP16, BF16 or FP32, pitch ldd
+ * and stride stride_d in elements) = e2m1(code) * (scale * row_scale) in FP32,
+ * rounded once. */
+dg_status dg_dequantize_nvf4(int64_t count, int64_t rows, int64_t K, const void *codes, int64_t ldq,
+                             int64_t stride_q, const void *scales, const float *row_scales, void *D,
+                             dg_dtype dtype_d, int64_t ldd, int64_t stride_d, dg_stream_t stream);
+
+/* D = epilogue(alpha * A.B^T + beta * D) for NVF4 A (M x K) and B (N x K), with
+ * FP32 sums over all of K on the block-scaled MMA.  D, bias and epilogues as
+ * dg_gemm_fp8; K is at least 1.  M == 0 or N == 0 is a no-op.  Results are
+ * bit-stable; nothing is allocated. */
+dg_status dg_gemm_nvf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
+                       const void *scale_a, const float *row_a, const void *B, int64_t ldb,
+                       const void *scale_b, const float *row_b, void *D, dg_dtype dtype_d,
+                       int64_t ldd, const void *bias, float alpha, float beta,
+                       dg_epilogue epilogue, dg_stream_t stream);
+
+/* The product of a mixture of experts, one for each expert e of `count`, over
+ * `rows` rows sorted by expert, as dg_gemm_fp8_grouped.  B is a stack of count
+ * matrices (N x K; stride_b a multiple of ldb and at least N * ldb).  offsets:
+ * device array of count + 1 int32, each a multiple of 128 (dg_moe_sort with
+ * align 128) or `rows`: one that is not is rounded down to it and
+ * DG_ERR_INVALID_ARG is recorded in the status word.  Rows outside every
+ * segment are neither read nor written. */
+dg_status dg_gemm_nvf4_grouped(int64_t count, int64_t rows, int64_t N, int64_t K, const void *A,
+                               int64_t lda, const void *scale_a, const float *row_a, const void *B,
+                               int64_t ldb, int64_t stride_b, const void *scale_b,
+                               const float *row_b, const int32_t *offsets, void *D,
+                               dg_dtype dtype_d, int64_t ldd, const void *bias,
+                               int64_t stride_bias, float alpha, float beta, dg_epilogue epilogue,
+                               dg_stream_t stream);
+
 /* Message for the last failing call on this thread ("" if none).  Valid
  * until the next libdg call on the same thread. */
 const char *dg_last_error(void);

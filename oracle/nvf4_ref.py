@@ -1,0 +1,126 @@
+"""64-bit references of the 4-bit operators with E4M3 block scales and of the
+expert layer for a few tokens, written from their definitions in include/dg.h
+with numpy only.
+
+A value is e2m1(code) * e4m3(scale) * row_scale: one E4M3 scale per 16 values
+along K, one FP32 scale per row.  Codes are packed two to a byte; scales lie in
+tiles of 128 rows x 4 blocks.
+"""
+
+import numpy as np
+
+from . import fp8_ref
+
+GROUP = 16
+GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])  # magnitudes of codes 0 .. 7
+NAN = 0x7F
+
+
+def e2m1_codes(x):
+    """Nearest codes of x, ties to the even code, saturated at 6, signs kept."""
+    x = np.asarray(x, np.float64)
+    mag = np.minimum(np.abs(x), 6.0)
+    hi = np.clip(np.searchsorted(GRID, mag), 1, 7)
+    lo = hi - 1
+    down, up = mag - GRID[lo], GRID[hi] - mag
+    code = np.where(down < up, lo, np.where(up < down, hi, np.where(lo % 2 == 0, lo, hi)))
+    return (code | (np.signbit(x) * 8)).astype(np.uint8)
+
+
+def row_scale(amax):
+    """The smallest power of two r >= 2^-100 with 2688 r >= amax."""
+    e = -100
+    while 2688.0 * 2.0 ** e < amax:
+        e += 1
+    return np.float32(2.0 ** e)
+
+
+def quantize(x, given=None):
+    """(codes [rows, K], one to a byte, scale codes [rows, groups], row scales) of
+    x [rows, K]; quotients and products rounded to float32 as the definition says."""
+    x = np.asarray(x, np.float32)
+    rows, K = x.shape
+    groups = -(-K // GROUP)
+    codes = np.zeros((rows, K), np.uint8)
+    scales = np.zeros((rows, groups), np.uint8)
+    out = np.zeros(rows, np.float32)
+    for i in range(rows):
+        blocks = [x[i, GROUP * j:GROUP * (j + 1)] for j in range(groups)]
+        fine = [bool(np.isfinite(b).all()) for b in blocks]
+        if given is None:
+            r = row_scale(max([float(np.abs(b).max()) for b, f in zip(blocks, fine) if f] or [0.0]))
+        else:
+            r = np.float32(given[i])
+            if not 2.0 ** -100 <= r <= 2.0 ** 100:
+                out[i], scales[i] = r, NAN
+                continue
+        out[i] = r
+        for j, b in enumerate(blocks):
+            if not fine[j]:
+                scales[i, j] = NAN
+                continue
+            with np.errstate(over="ignore"):
+                t = np.abs(b).max() / (np.float32(6.0) * r)
+                s = max(int(fp8_ref.e4m3_codes(t)), 1)
+                u = np.float32(fp8_ref.VALUES[s]) * r
+                codes[i, GROUP * j:GROUP * (j + 1)] = e2m1_codes(b / u)
+            scales[i, j] = s
+    return codes, scales, out
+
+
+def pack(codes):
+    """Two codes to a byte, the even one in the low nibble."""
+    rows, K = codes.shape
+    full = np.zeros((rows, K + K % 2), np.uint8)
+    full[:, :K] = codes
+    return full[:, 0::2] | (full[:, 1::2] << 4)
+
+
+def unpack(packed, K):
+    codes = np.zeros(packed.shape[:-1] + (2 * packed.shape[-1],), np.uint8)
+    codes[..., 0::2] = packed & 15
+    codes[..., 1::2] = packed >> 4
+    return codes[..., :K]
+
+
+def tiles(scales):
+    """Scale codes [rows, groups] in tiles, one by one."""
+    rows, groups = scales.shape
+    out = np.zeros((-(-rows // 128), -(-groups // 4), 32, 16), np.uint8)
+    for r in range(rows):
+        for g in range(groups):
+            out[r // 128, g // 4, r % 32, 4 * (r % 128 // 32) + g % 4] = scales[r, g]
+    return out
+
+
+def values(codes, scales, rows_scale):
+    """What codes [rows, K] with scale codes [rows, groups] stand for, float64."""
+    mag = GRID[codes & 7]
+    v = np.where(codes > 7, -mag, mag)
+    s = np.repeat(fp8_ref.VALUES[scales], GROUP, 1)[:, :codes.shape[1]]
+    return v * s * np.asarray(rows_scale, np.float64)[:, None]
+
+
+def product(a, b, alpha=1.0, beta=0.0, d=None, bias=None, use_gelu=False):
+    """epilogue(alpha * a.b^T + beta * d) of values a [M, K], b [N, K], and the
+    error bound of an FP32 computation before its last rounding.
+
+    A product of two scaled values is exact in FP32 (at most 4 + 8 significant
+    bits).  The K of them are added in FP32 (truncation allowed: 2^-23 each) and
+    scaled by both rows' scales (two roundings, alpha's with the row's a third).
+    beta and bias add a rounding each; GELU's slope is at most 1.13 and its
+    evaluation good to 2e-7 of |t|."""
+    t = alpha * (a @ b.T)
+    mags = abs(alpha) * (np.abs(a) @ np.abs(b).T)
+    u = 2.0 ** -23
+    err = mags * (a.shape[1] + 4) * u
+    if beta != 0.0:
+        t = t + beta * d
+        err = err + (np.abs(t) + np.abs(beta * d)) * u
+    if bias is not None:
+        t = t + bias
+        err = err + (np.abs(t) + np.abs(bias)) * u
+    if use_gelu:
+        err = 1.13 * err + 2e-7 * np.abs(t)
+        t = fp8_ref.gelu(t)
+    return t, err

@@ -18,6 +18,8 @@ __all__ = [
     "EpilogueOp", "EpilogueProgram", "make_program",
     "quantize_fp8", "gemm_fp8", "gemm_fp8_grouped", "gemm_fp8_grouped_wgrad", "moe_rows",
     "moe_sort", "moe_dispatch", "moe_dispatch_fp8", "moe_combine", "moe_combine_backward",
+    "nvf4_buffers", "quantize_nvf4", "moe_dispatch_nvf4", "dequantize_nvf4", "gemm_nvf4",
+    "gemm_nvf4_grouped",
     "plan_tiles", "query_hw", "last_error", "check_status", "set_wait_timeout_ns",
     "selftest_wait_timeout", "launch_count", "shutdown", "HwDesc", "TilePlan", "EXPORTS",
 ]
@@ -41,6 +43,8 @@ EXPORTS = ["dg_query_hw", "dg_plan_tiles", "dg_gemm", "dg_gemm_planned", "dg_gem
            "dg_moe_rows", "dg_moe_sort", "dg_moe_dispatch", "dg_moe_dispatch_fp8",
            "dg_moe_dispatch_fp8_scratch", "dg_moe_dispatch_fp8_ex",
            "dg_moe_combine", "dg_moe_combine_backward",
+           "dg_quantize_nvf4", "dg_moe_dispatch_nvf4", "dg_dequantize_nvf4", "dg_gemm_nvf4",
+           "dg_gemm_nvf4_grouped",
            "dg_gemm_thin_noalloc", "dg_last_error",
            "dg_check_status", "dg_set_wait_timeout_ns", "dg_selftest_wait_timeout",
            "dg_launch_count", "dg_shutdown"]
@@ -167,6 +171,13 @@ def lib():
     L.dg_moe_combine.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, vp]
     L.dg_moe_combine_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, vp, vp,
                                           vp, i64, vp, vp]
+    L.dg_quantize_nvf4.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i64, vp, vp, vp]
+    L.dg_moe_dispatch_nvf4.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, vp, vp]
+    L.dg_dequantize_nvf4.argtypes = [i64, i64, i64, vp, i64, i64, vp, vp, vp, i32, i64, i64, vp]
+    L.dg_gemm_nvf4.argtypes = [i64, i64, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp, i32, i64, vp,
+                               f32, f32, i32, vp]
+    L.dg_gemm_nvf4_grouped.argtypes = [i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, vp, vp,
+                                       vp, vp, i32, i64, vp, i64, f32, f32, i32, vp]
     L.dg_last_error.restype = ctypes.c_char_p
     L.dg_last_error.argtypes = []
     L.dg_check_status.argtypes = [vp]
@@ -962,6 +973,176 @@ def moe_combine_backward(dD, Y, slot_row, row_slot, weights, dY, dweights=None, 
         _stream_of(stream, dD, None if dweights is None else Y, slot_row, row_slot, weights, dY,
                    dweights)))
     return dY, dweights
+
+
+# ------------------------------------- 4-bit float with E4M3 block scales
+
+def _nvf4_scale_shape(rows, K):
+    return (rows + 127) // 128, (K + 63) // 64, 32, 16
+
+
+def nvf4_buffers(*shape, device="cuda"):
+    """Room for the NVF4 form of a [rows, K] matrix or a [count, rows, K] stack:
+    (codes uint8 [..., rows, ceil(K / 2)], rows on 16-byte boundaries; scales
+    float8_e4m3fn [..., ceil(rows / 128), ceil(K / 64), 32, 16]; row scales
+    float32 [..., rows])."""
+    torch = (_FP or _fp())[0]
+    rows, K = shape[-2:]
+    lead = tuple(shape[:-2])
+    room = torch.empty(lead + (rows, (K + 31) // 32 * 16), dtype=torch.uint8, device=device)
+    return (room[..., :(K + 1) // 2],
+            torch.empty(lead + _nvf4_scale_shape(rows, K), dtype=torch.float8_e4m3fn,
+                        device=device),
+            torch.empty(lead + (rows,), dtype=torch.float32, device=device))
+
+
+def _nvf4_operand(torch, codes, scales, row_scales, what, K=None):
+    """(row stride, matrix stride) of the codes of an NVF4 matrix or stack."""
+    dim = codes.dim()
+    s = _rows(codes, torch.uint8, what, None, dim if dim in (2, 3) else 2)
+    rows, width = codes.shape[-2:]
+    if K is None:
+        K = 2 * width
+    elif width != (K + 1) // 2:
+        raise ValueError("%s must have rows of %d bytes, got %d" % (what, (K + 1) // 2, width))
+    lead = codes.shape[:-2]
+    _rows(scales, torch.float8_e4m3fn, "the scales of " + what,
+          lead + _nvf4_scale_shape(rows, K), dim + 2)
+    _rows(row_scales, torch.float32, "the row scales of " + what, lead + (rows,), dim - 1)
+    if not (scales.is_contiguous() and row_scales.is_contiguous()):
+        raise ValueError("the scales of %s must be contiguous" % what)
+    return _pitch(s[-2], rows, width, 16), s[0] if dim == 3 else 0
+
+
+def _pitch(stride, rows, width, multiple):
+    """The row pitch; of a matrix of one row, whose stride torch leaves open, any that is allowed."""
+    return stride if rows > 1 else -(-width // multiple) * multiple
+
+
+def quantize_nvf4(X, row_scales=None, out=None, stream=None):
+    """4-bit quantization of X [rows, K] or [count, rows, K] (float16 or
+    bfloat16): (codes, scales, row scales) as nvf4_buffers describes them.
+    row_scales: float32 [..., rows] to quantize with (calibrated ones), by
+    default found from each row.  out: buffers to write into; with row_scales
+    given, its third is not used and may be None."""
+    torch = (_FP or _fp())[0]
+    code = _float_code(X, "X")
+    dim = X.dim()
+    sx = _rows(X, X.dtype, "X", None, dim if dim in (2, 3) else 2)
+    rows, K = X.shape[-2:]
+    codes, scales, found = nvf4_buffers(*X.shape, device=X.device) if out is None else out
+    if row_scales is not None:
+        found = row_scales
+    ldq, stride_q = _nvf4_operand(torch, codes, scales, found, "out", K)
+    if codes.shape[:-1] != X.shape[:-1]:
+        raise ValueError("out is for %s rows, X has %s" % (
+            tuple(codes.shape[:-1]), tuple(X.shape[:-1])))
+    _check(lib().dg_quantize_nvf4(
+        X.shape[0] if dim == 3 else 1, rows, K, code, X.data_ptr(),
+        _pitch(sx[-2], rows, K, 8), sx[0] if dim == 3 else 0, None if row_scales is None else row_scales.data_ptr(),
+        codes.data_ptr(), ldq, stride_q, scales.data_ptr(),
+        found.data_ptr() if row_scales is None else None,
+        _stream_of(stream, X, codes, scales, found)))
+    return codes, scales, found
+
+
+def moe_dispatch_nvf4(X, row_slot, top_k, codes, scales, row_scales, stream=None):
+    """moe_dispatch and quantize_nvf4 in one, into the buffers of a [rows, width]
+    matrix (nvf4_buffers)."""
+    torch = (_FP or _fp())[0]
+    code = _float_code(X, "X")
+    sx = _rows(X, X.dtype, "X")
+    tokens, width = X.shape
+    rows = row_slot.shape[0]
+    _rows(row_slot, torch.int32, "row_slot", None, 1)
+    ldq, _ = _nvf4_operand(torch, codes, scales, row_scales, "codes", width)
+    if codes.shape != (rows, (width + 1) // 2):
+        raise ValueError("codes must be [%d, %d]" % (rows, (width + 1) // 2))
+    _check(lib().dg_moe_dispatch_nvf4(
+        tokens, top_k, width, code, X.data_ptr(), _pitch(sx[0], tokens, width, 8), rows,
+        row_slot.data_ptr(), codes.data_ptr(), ldq, scales.data_ptr(), row_scales.data_ptr(),
+        _stream_of(stream, X, row_slot, codes, scales, row_scales)))
+    return codes, scales, row_scales
+
+
+def dequantize_nvf4(codes, scales, row_scales, D, stream=None):
+    """D [..., rows, K] (float16, bfloat16 or float32) = the values that an NVF4
+    matrix or stack holds."""
+    torch = (_FP or _fp())[0]
+    dt = _float_code(D, "D", (F16, BF16, F32))
+    dim = D.dim()
+    sd = _rows(D, D.dtype, "D", None, dim if dim in (2, 3) else 2)
+    rows, K = D.shape[-2:]
+    ldq, stride_q = _nvf4_operand(torch, codes, scales, row_scales, "codes", K)
+    if codes.shape[:-1] != D.shape[:-1]:
+        raise ValueError("codes have %s rows, D %s" % (
+            tuple(codes.shape[:-1]), tuple(D.shape[:-1])))
+    _check(lib().dg_dequantize_nvf4(
+        D.shape[0] if dim == 3 else 1, rows, K, codes.data_ptr(), ldq, stride_q,
+        scales.data_ptr(), row_scales.data_ptr(), D.data_ptr(), dt, _pitch(sd[-2], rows, K, 1),
+        sd[0] if dim == 3 else 0, _stream_of(stream, codes, scales, row_scales, D)))
+    return D
+
+
+def gemm_nvf4(A, scale_a, row_a, B, scale_b, row_b, D, bias=None, alpha=1.0, beta=0.0,
+              epilogue="none", stream=None):
+    """D = epilogue(alpha * A.B^T + beta * D) for NVF4 operands, written into D.
+
+    A: [M, K] and B: [N, K] as quantize_nvf4 gives them; D: [M, N] float16,
+    bfloat16 or float32; bias: [N] of D's type.
+    """
+    torch = (_FP or _fp())[0]
+    lda, _ = _nvf4_operand(torch, A, scale_a, row_a, "A")
+    ldb, _ = _nvf4_operand(torch, B, scale_b, row_b, "B")
+    dt = _float_code(D, "D", (F16, BF16, F32))
+    sd = _rows(D, D.dtype, "D")
+    M, N = D.shape
+    if A.dim() != 2 or B.dim() != 2 or A.shape[0] != M or B.shape[0] != N or \
+            A.shape[1] != B.shape[1]:
+        raise ValueError("shape mismatch: A %s, B %s, D %s" % tuple(
+            tuple(t.shape) for t in (A, B, D)))
+    if bias is not None:
+        _rows(bias, D.dtype, "bias", (N,), 1)
+    _check(lib().dg_gemm_nvf4(
+        M, N, 2 * A.shape[1], A.data_ptr(), lda, scale_a.data_ptr(), row_a.data_ptr(),
+        B.data_ptr(), ldb, scale_b.data_ptr(), row_b.data_ptr(), D.data_ptr(), dt,
+        _pitch(sd[0], M, N, 1),
+        None if bias is None else bias.data_ptr(), alpha, beta, _epi_code(epilogue),
+        _stream_of(stream, A, scale_a, row_a, B, scale_b, row_b, D, bias)))
+    return D
+
+
+def gemm_nvf4_grouped(A, scale_a, row_a, B, scale_b, row_b, offsets, D, bias=None, alpha=1.0,
+                      beta=0.0, epilogue="none", stream=None):
+    """D[i] = epilogue(alpha * A[i].B[e]^T + beta * D[i]) for the rows i of each
+    expert e, offsets[e] <= i < offsets[e + 1] (int32 [count + 1] on the device,
+    multiples of 128: moe_sort with align=128).
+
+    A: NVF4 [rows, K]; B: NVF4 [count, N, K]; D: [rows, N]; bias: [count, N] of
+    D's type.
+    """
+    torch = (_FP or _fp())[0]
+    lda, _ = _nvf4_operand(torch, A, scale_a, row_a, "A")
+    ldb, stride_b = _nvf4_operand(torch, B, scale_b, row_b, "B")
+    dt = _float_code(D, "D", (F16, BF16, F32))
+    sd = _rows(D, D.dtype, "D")
+    rows, N = D.shape
+    if A.dim() != 2 or B.dim() != 3 or A.shape[0] != rows or B.shape[1] != N or \
+            A.shape[1] != B.shape[2]:
+        raise ValueError("shape mismatch: A %s, B %s, D %s" % tuple(
+            tuple(t.shape) for t in (A, B, D)))
+    count = B.shape[0]
+    _rows(offsets, torch.int32, "offsets", (count + 1,), 1)
+    stride_bias = 0
+    if bias is not None:
+        stride_bias = _rows(bias, D.dtype, "bias", (count, N))[0]
+    _check(lib().dg_gemm_nvf4_grouped(
+        count, rows, N, 2 * A.shape[1], A.data_ptr(), lda, scale_a.data_ptr(), row_a.data_ptr(),
+        B.data_ptr(), ldb, stride_b, scale_b.data_ptr(), row_b.data_ptr(), offsets.data_ptr(),
+        D.data_ptr(), dt, _pitch(sd[0], rows, N, 1), None if bias is None else bias.data_ptr(),
+        stride_bias, alpha, beta, _epi_code(epilogue),
+        _stream_of(stream, A, scale_a, row_a, B, scale_b, row_b, offsets, D, bias)))
+    return D
 
 
 def query_hw(device=0):

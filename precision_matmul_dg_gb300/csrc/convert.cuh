@@ -42,4 +42,22 @@ __device__ __forceinline__ uint4 e2m1x8_to_f16x8(uint32_t w) {
   return make_uint4(f[0], f[1], f[2], f[3]);
 }
 
+// Eight FP32 values -> four bytes of E2M1 codes (value 2i in the low nibble
+// of byte i), nearest with ties to even, saturated to the largest finite
+// code.  The conversion keeps the sign of negative values that round to zero
+// (code 8, -0), as the format's rounding asks (checked on GB300 for -0,
+// -1e-30, -0.1 and -0.2499).
+__device__ __forceinline__ uint32_t e2m1x8_from_f32(const float (&v)[8]) {
+  uint32_t out;
+  asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q3, %8, %7;\n\t"
+      "mov.b32 %0, {q0, q1, q2, q3};\n\t}"
+      : "=r"(out)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return out;
+}
+
 }  // namespace dg

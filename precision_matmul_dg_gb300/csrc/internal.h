@@ -305,6 +305,60 @@ cudaError_t launch_fp8_tc(const Fp8Args& a);      // fp8_gemm.cu: tcgen05
 cudaError_t launch_fp8_skinny(const Fp8Args& a);  // fp8_skinny.cu: few rows (dense or kRows)
 constexpr int64_t kMaxExperts = 1024;
 
+// 4-bit operands with E4M3 block scales and FP32 row scales (nvf4_quant.cu,
+// nvf4_gemm.cu).  A stack of `count` matrices; row_slot: rows gathered by
+// expert; given: the caller's row scales.
+struct Nvf4RowsJob {
+  bool bf16 = false;
+  const void* X = nullptr;
+  int64_t ldx = 0, stride_x = 0, count = 1, rows = 0, K = 0;
+  void* codes = nullptr;
+  int64_t ldq = 0, stride_q = 0;  // bytes
+  void* scales = nullptr;
+  float* row_scales = nullptr;
+  const float* given = nullptr;
+  const int32_t* row_slot = nullptr;
+  int64_t top_k = 1, tokens = 0;
+};
+cudaError_t launch_quantize_nvf4(const Nvf4RowsJob& j, cudaStream_t stream, int sm_count);
+struct Nvf4ValuesJob {
+  int64_t count, rows, K;
+  const void* codes;
+  int64_t ldq, stride_q;
+  const void* scales;
+  const float* row_scales;
+  void* D;
+  dg_dtype dtype_d;
+  int64_t ldd, stride_d;
+};
+cudaError_t launch_dequantize_nvf4(const Nvf4ValuesJob& j, cudaStream_t stream, int sm_count);
+// One dense product (offsets NULL) or one per expert over A's sorted rows.
+struct Nvf4Args {
+  int64_t M, N, K;
+  const void* A;
+  int64_t lda;
+  const void* sa;
+  const float* row_a;
+  const void* B;
+  int64_t ldb, stride_b;
+  const void* sb;
+  const float* row_b;
+  int64_t count;
+  const int32_t* offsets;
+  void* D;
+  dg_dtype dtype_d;
+  int64_t ldd;
+  const void* bias;
+  int64_t stride_bias;
+  float alpha, beta;
+  int epi;  // kEpiBias | kEpiGelu
+  cudaStream_t stream;
+  int* status;
+  uint64_t timeout_ns;
+  int sm_count;
+};
+cudaError_t launch_gemm_nvf4(const Nvf4Args& a);
+
 // Expert routing (moe.cu).
 struct MoeSortJob {
   int64_t tokens, top_k, count;

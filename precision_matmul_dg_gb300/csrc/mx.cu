@@ -32,6 +32,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "convert.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -44,24 +45,6 @@ constexpr int kMxBlock = 32;  // values per scale
 // ---------------------------------------------------------------------------
 // Quantization
 // ---------------------------------------------------------------------------
-
-// Eight FP32 values -> four bytes of E2M1 codes (value 2i in the low nibble
-// of byte i), nearest with ties to even, saturated to the largest finite
-// code.  The conversion keeps the sign of negative values that round to zero
-// (code 8, -0), as the format's rounding asks (checked on GB300 for -0,
-// -1e-30, -0.1 and -0.2499).
-__device__ __forceinline__ uint32_t e2m1x8_from_f32(const float (&v)[8]) {
-  uint32_t out;
-  asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 q0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 q1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 q2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 q3, %8, %7;\n\t"
-      "mov.b32 %0, {q0, q1, q2, q3};\n\t}"
-      : "=r"(out)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-  return out;
-}
 
 // 16-byte read-only load.
 __device__ __forceinline__ uint4 ld_nc16(const void* p) {
