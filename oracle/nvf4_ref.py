@@ -124,3 +124,61 @@ def product(a, b, alpha=1.0, beta=0.0, d=None, bias=None, use_gelu=False):
         err = 1.13 * err + 2e-7 * np.abs(t)
         t = fp8_ref.gelu(t)
     return t, err
+
+
+def silu(g):
+    with np.errstate(over="ignore"):
+        return g / (1.0 + np.exp(-g))
+
+
+def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
+    """(y, bound) of the expert layer on values: x [tokens, width], up [count,
+    hidden or 2 hidden, width], down [count, out, hidden]; the bound is of an
+    FP32 computation with x and h held as include/dg.h says, before the last
+    rounding.
+
+    A sum of K products errs by at most (K + 200) 2^-23 of the sum of magnitudes
+    (truncated FP32 additions; activations in three parts whose magnitudes add up
+    to at most 1.07 of them, the parts' and slices' sums and the scales a few
+    more), a value of x by 2^-25 of its row's largest, one of h by 2^-13 of itself
+    and 2^-25 of the largest of 32 around it.  GELU's and SiLU's slopes are at most
+    1.13, and they are evaluated to 2e-6."""
+    tokens, top_k = ids.shape
+    count, out = down.shape[0], down.shape[1]
+    u = 2.0 ** -23
+    y, bound = np.zeros((tokens, out)), np.zeros((tokens, out))
+
+    def product(W, v, verr, bias):
+        t = W @ v
+        mags = np.abs(W) @ np.abs(v)
+        err = 1.07 * mags * (len(v) + 200) * u + np.abs(W) @ verr
+        if bias is not None:
+            t = t + bias
+            err = err + (np.abs(t) + np.abs(bias)) * u
+        return t, err
+    for t in range(tokens):
+        for j in range(top_k):
+            e = ids[t, j]
+            if not 0 <= e < count:
+                continue
+            h, err = product(up[e], x[t], np.full(x.shape[1], np.abs(x[t]).max() * 2.0 ** -25),
+                             None if bias_up is None else bias_up[e])
+            if gated:
+                n = len(h) // 2
+                g, v = h[:n], h[n:]
+                eg, ev = err[:n], err[n:]
+                s = silu(g)
+                es = 1.13 * eg + 2e-6 * np.abs(s)
+                h = s * v
+                err = es * np.abs(v) + (np.abs(s) + es) * ev + np.abs(h) * u
+            else:
+                err = 1.13 * err + 2e-6 * np.abs(h)
+                h = fp8_ref.gelu(h)
+            pad = np.zeros(-len(h) % 32)
+            around = np.repeat(np.concatenate([np.abs(h) + err, pad]).reshape(-1, 32).max(1), 32)
+            err = err + 2.0 ** -13 * (np.abs(h) + err) + 2.0 ** -25 * around[:len(h)]
+            v, ev = product(down[e], h, err, None if bias_down is None else bias_down[e])
+            w = 1.0 if weights is None else float(weights[t, j])
+            y[t] += w * v
+            bound[t] += abs(w) * (ev + np.abs(v) * (top_k + 1) * u)
+    return y, bound

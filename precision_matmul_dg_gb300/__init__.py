@@ -19,7 +19,7 @@ __all__ = [
     "quantize_fp8", "gemm_fp8", "gemm_fp8_grouped", "gemm_fp8_grouped_wgrad", "moe_rows",
     "moe_sort", "moe_dispatch", "moe_dispatch_fp8", "moe_combine", "moe_combine_backward",
     "nvf4_buffers", "quantize_nvf4", "moe_dispatch_nvf4", "dequantize_nvf4", "gemm_nvf4",
-    "gemm_nvf4_grouped",
+    "gemm_nvf4_grouped", "moe_layer", "MoeWeights",
     "plan_tiles", "query_hw", "last_error", "check_status", "set_wait_timeout_ns",
     "selftest_wait_timeout", "launch_count", "shutdown", "HwDesc", "TilePlan", "EXPORTS",
 ]
@@ -44,7 +44,7 @@ EXPORTS = ["dg_query_hw", "dg_plan_tiles", "dg_gemm", "dg_gemm_planned", "dg_gem
            "dg_moe_dispatch_fp8_scratch", "dg_moe_dispatch_fp8_ex",
            "dg_moe_combine", "dg_moe_combine_backward",
            "dg_quantize_nvf4", "dg_moe_dispatch_nvf4", "dg_dequantize_nvf4", "dg_gemm_nvf4",
-           "dg_gemm_nvf4_grouped",
+           "dg_gemm_nvf4_grouped", "dg_moe_layer_scratch", "dg_moe_layer",
            "dg_gemm_thin_noalloc", "dg_last_error",
            "dg_check_status", "dg_set_wait_timeout_ns", "dg_selftest_wait_timeout",
            "dg_launch_count", "dg_shutdown"]
@@ -95,6 +95,13 @@ _lib = None
 
 class EpilogueOp(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int), ("a", ctypes.c_float), ("b", ctypes.c_float)]
+
+
+class MoeWeights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld", ctypes.c_int64), ("stride", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("lds", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("row_scales", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("stride_bias", ctypes.c_int64)]
 
 
 class EpilogueProgram(ctypes.Structure):
@@ -178,6 +185,11 @@ def lib():
                                f32, f32, i32, vp]
     L.dg_gemm_nvf4_grouped.argtypes = [i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, vp, vp,
                                        vp, vp, i32, i64, vp, i64, f32, f32, i32, vp]
+    L.dg_moe_layer_scratch.argtypes = [i64, i64, i64, i64]
+    L.dg_moe_layer_scratch.restype = ctypes.c_int64
+    L.dg_moe_layer.argtypes = [i64, i64, i64, i64, i64, i64, i32, vp, i64, vp, vp, i32,
+                               ctypes.POINTER(MoeWeights), ctypes.POINTER(MoeWeights), i32, vp,
+                               i64, vp, i64, vp]
     L.dg_last_error.restype = ctypes.c_char_p
     L.dg_last_error.argtypes = []
     L.dg_check_status.argtypes = [vp]
@@ -1142,6 +1154,85 @@ def gemm_nvf4_grouped(A, scale_a, row_a, B, scale_b, row_b, offsets, D, bias=Non
         D.data_ptr(), dt, _pitch(sd[0], rows, N, 1), None if bias is None else bias.data_ptr(),
         stride_bias, alpha, beta, _epi_code(epilogue),
         _stream_of(stream, A, scale_a, row_a, B, scale_b, row_b, offsets, D, bias)))
+    return D
+
+
+def _moe_weights(torch, w, bias, dtype, what):
+    """(format, MoeWeights, rows, K bytes) of one product's weights."""
+    nvf4 = len(w) == 3
+    codes, scales = w[0], w[1]
+    count, n, kb = codes.shape
+    if nvf4:
+        ld, stride = _nvf4_operand(torch, codes, scales, w[2], what)
+        z = (0, 0)
+    else:
+        s, z = _fp8_operand(torch, codes, scales, what, 3)
+        ld, stride = s[1], s[0]
+        if scales.shape[0] != count or scales.shape[1] != (n + 127) // 128 or \
+                scales.shape[2] < (kb + 127) // 128:
+            raise ValueError("shape mismatch: %s %s with %s" % (
+                what, tuple(codes.shape), tuple(scales.shape)))
+    sb = 0
+    if bias is not None:
+        sb = _rows(bias, dtype, "the bias of " + what, (count, n))[0]
+    return MoeWeights(codes.data_ptr(), ld, stride, scales.data_ptr(), z[1], z[0],
+                      w[2].data_ptr() if nvf4 else None,
+                      None if bias is None else bias.data_ptr(), sb)
+
+
+def moe_layer(X, ids, weights, up, down, D, activation="gelu", bias_up=None, bias_down=None,
+              stream=None):
+    """The expert layer of a few tokens in two kernels: D[t] = sum over j of
+    weights[t, j] * (W2[e] act(W1[e] X[t] + b1[e]) + b2[e]), e = ids[t, j].
+
+    X: [tokens, width] float16 or bfloat16, D: [tokens, out] of its type; ids:
+    int32 [tokens, top_k] (outside [0, count): dropped), weights: float32 like
+    ids, or None for ones.  up and down: FP8 (codes [count, n, k], scales of 128
+    x 128 blocks) or NVF4 stacks (codes, scales, row scales), n = hidden (twice
+    that, gate rows first, with activation "swiglu") and out.  Biases: [count,
+    n] of X's type.  Scratch comes from torch's allocator (dg_moe_layer).
+    """
+    torch = (_FP or _fp())[0]
+    code = _float_code(X, "X")
+    sx = _rows(X, X.dtype, "X")
+    tokens, width = X.shape
+    _rows(ids, torch.int32, "ids")
+    top_k = ids.shape[1]
+    sd = _rows(D, X.dtype, "D")
+    out = D.shape[1]
+    if weights is not None:
+        _rows(weights, torch.float32, "weights", ids.shape)
+    if not ids.is_contiguous() or not (weights is None or weights.is_contiguous()):
+        raise ValueError("ids and weights must be contiguous")
+    if activation not in ("gelu", "swiglu"):
+        raise ValueError("activation must be gelu or swiglu")
+    gated = activation == "swiglu"
+    if len(up) != len(down) or len(up) not in (2, 3):
+        raise ValueError("up and down are both (codes, scales) or (codes, scales, row scales)")
+    nvf4 = len(up) == 3
+    w1 = _moe_weights(torch, up, bias_up, X.dtype, "up")
+    w2 = _moe_weights(torch, down, bias_down, X.dtype, "down")
+    count, n1, k1 = up[0].shape
+    hidden = n1 // 2 if gated else n1
+    k2 = down[0].shape[2]
+    if nvf4:
+        width_codes, hidden_codes = (width + 1) // 2, (hidden + 1) // 2
+    else:
+        width_codes, hidden_codes = width, hidden
+    if ids.shape[0] != tokens or D.shape[0] != tokens or (gated and n1 % 2) or \
+            k1 != width_codes or down[0].shape[0] != count or down[0].shape[1] != out or \
+            k2 != hidden_codes:
+        raise ValueError("shape mismatch: X %s, ids %s, up %s, down %s, D %s" % tuple(
+            tuple(t.shape) for t in (X, ids, up[0], down[0], D)))
+    handle = _stream_of(stream, X, ids, weights, *up, *down, D, bias_up, bias_down)
+    nbytes = lib().dg_moe_layer_scratch(tokens, top_k, hidden, out)
+    scratch = _scratch(torch, max(nbytes, 16), X.device, stream)
+    _check(lib().dg_moe_layer(
+        tokens, top_k, count, width, hidden, out, code, X.data_ptr(),
+        _pitch(sx[0], tokens, width, 8), ids.data_ptr(),
+        None if weights is None else weights.data_ptr(), 1 if nvf4 else 0, ctypes.byref(w1),
+        ctypes.byref(w2), 1 if gated else 0, D.data_ptr(), _pitch(sd[0], tokens, out, 8),
+        scratch.data_ptr(), nbytes, handle))
     return D
 
 

@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libdg.so")
 SOURCES = ["api.cu", "planner.cpp", "gemv.cu", "gemm_tc.cu", "gemm_conv.cu", "widen.cu",
            "skinny.cu", "mx.cu", "gemm_w4t.cu", "api_fp8.cu", "fp8_quant.cu",
            "fp8_gemm.cu", "fp8_skinny.cu", "moe.cu", "api_nvf4.cu", "nvf4_quant.cu",
-           "nvf4_gemm.cu"]
+           "nvf4_gemm.cu", "moe_layer.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "-I", INCLUDE, "-I", CSRC]

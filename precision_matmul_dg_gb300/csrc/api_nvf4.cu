@@ -1,5 +1,5 @@
-// C ABI of the 4-bit operators with E4M3 block scales: argument checks and
-// dispatch.
+// C ABI of the 4-bit operators with E4M3 block scales and of the expert layer
+// for few tokens: argument checks and dispatch.
 #include <math.h>
 
 #include <algorithm>
@@ -44,6 +44,62 @@ dg_status check_counts(int64_t count, int64_t rows, int64_t K) {
   if (s != DG_OK) return s;
   if (count > 0 && ceil_div(rows, 128) * 128 > (int64_t(1) << 40) / count)
     return set_error(DG_ERR_UNSUPPORTED, "more than 2^40 rows in all");
+  return DG_OK;
+}
+
+constexpr int64_t kFp8Block = 128;
+
+// A product's weights: count matrices of n rows of k values.
+dg_status check_moe_weights(const char* name, const dg_moe_weights* w, bool nvf4, int64_t count,
+                            int64_t n, int64_t k) {
+  if (!w) return set_errorf(DG_ERR_INVALID_ARG, "%s is null", name);
+  if (nvf4) {
+    const dg_status s = check_nvf4(name, w->codes, w->ld, k, w->scales, w->row_scales);
+    if (s != DG_OK) return s;
+  } else {
+    if (!w->codes || !w->scales)
+      return set_errorf(DG_ERR_INVALID_ARG, "%s or its scales is null", name);
+    if (!aligned16(w->codes) || !aligned4(w->scales))
+      return set_errorf(DG_ERR_INVALID_ARG, "%s or its scales is not aligned", name);
+    if (w->ld < k || w->ld % 16 != 0)
+      return set_errorf(DG_ERR_INVALID_ARG,
+                        "%s: row pitch %lld must be >= %lld bytes and a multiple of 16", name,
+                        (long long)w->ld, (long long)k);
+    if (w->lds < ceil_div(k, kFp8Block))
+      return set_errorf(DG_ERR_INVALID_ARG, "%s: %lld scales per row, need %lld", name,
+                        (long long)w->lds, (long long)ceil_div(k, kFp8Block));
+    if (count > 1 && w->stride_s < ceil_div(n, kFp8Block) * w->lds)
+      return set_errorf(DG_ERR_INVALID_ARG, "%s: stride_s must be at least ceil(n / 128) * lds",
+                        name);
+  }
+  if (count > 1 && (w->stride % w->ld != 0 || w->stride / w->ld < n))
+    return set_errorf(DG_ERR_INVALID_ARG, "%s: stride must be a multiple of ld and at least n * ld",
+                      name);
+  if ((count > 1 ? (count - 1) * (w->stride / w->ld) : 0) + n > INT32_MAX ||
+      count * ceil_div(n, 128) * ceil_div(k, 64) > INT32_MAX)
+    return set_errorf(DG_ERR_UNSUPPORTED, "%s: more than 2^31 rows or scale tiles", name);
+  if (w->bias && (reinterpret_cast<uintptr_t>(w->bias) & 1u))
+    return set_errorf(DG_ERR_INVALID_ARG, "%s: bias is not aligned to its type", name);
+  if (w->bias && w->stride_bias < 0)
+    return set_errorf(DG_ERR_INVALID_ARG, "%s: negative stride_bias", name);
+  return DG_OK;
+}
+
+MoeWeights moe_weights(const dg_moe_weights& w, int64_t count) {
+  return {w.codes,        w.ld,        count > 1 ? w.stride : 0, w.scales,
+          w.lds,          count > 1 ? w.stride_s : 0,            w.row_scales,
+          w.bias,         w.stride_bias};
+}
+
+// Sizes of a layer call; the kernels' unit numbers are 32-bit.
+dg_status check_layer(int64_t tokens, int64_t top_k, int64_t hidden, int64_t out) {
+  dg_status s = check_routing(tokens, top_k, 0);
+  if (s == DG_OK) s = check_sizes(hidden, out, 0);
+  if (s != DG_OK) return s;
+  if (tokens * top_k > kMaxLayerSlots)
+    return set_errorf(DG_ERR_UNSUPPORTED, "more than %lld slots", (long long)kMaxLayerSlots);
+  if (std::max(hidden, out) > (int64_t(1) << 24))
+    return set_error(DG_ERR_UNSUPPORTED, "hidden or out above 2^24");
   return DG_OK;
 }
 
@@ -247,6 +303,82 @@ dg_status dg_gemm_nvf4_grouped(int64_t count, int64_t rows, int64_t N, int64_t K
   a.timeout_ns = c.timeout_ns;
   a.sm_count = c.sm_count;
   return launched(launch_gemm_nvf4(a), "kernel launch");
+}
+
+int64_t dg_moe_layer_scratch(int64_t tokens, int64_t top_k, int64_t hidden, int64_t out) {
+  clear_error();
+  if (check_layer(tokens, top_k, hidden, out) != DG_OK) return -1;
+  MoeLayerArgs a{};
+  a.tokens = tokens;
+  a.top_k = top_k;
+  a.hidden = hidden;
+  a.out = out;
+  return moe_layer_scratch(a);
+}
+
+dg_status dg_moe_layer(int64_t tokens, int64_t top_k, int64_t count, int64_t width, int64_t hidden,
+                       int64_t out, dg_dtype dtype, const void* X, int64_t ldx, const int32_t* ids,
+                       const float* weights, dg_moe_format format, const dg_moe_weights* up,
+                       const dg_moe_weights* down, dg_moe_activation activation, void* D,
+                       int64_t ldd, void* scratch, int64_t scratch_bytes, dg_stream_t stream) {
+  clear_error();
+  dg_status s = check_layer(tokens, top_k, hidden, out);
+  if (s == DG_OK) s = check_sizes(width, 0, 0);
+  if (s != DG_OK) return s;
+  if (count < 1) return bad("count must be >= 1");
+  if (count > kMaxExperts)
+    return set_errorf(DG_ERR_UNSUPPORTED, "more than %lld experts", (long long)kMaxExperts);
+  if (!type16(dtype))
+    return set_errorf(DG_ERR_UNSUPPORTED, "X and D are F16 or BF16, not %d",
+                      static_cast<int>(dtype));
+  if (format != DG_MOE_FP8 && format != DG_MOE_NVF4) return bad("unknown format");
+  if (activation != DG_MOE_GELU && activation != DG_MOE_SWIGLU) return bad("unknown activation");
+  if (tokens == 0 || out == 0) return DG_OK;
+  if (width < 1 || hidden < 1) return bad("width and hidden must be at least 1");
+  const bool gated = activation == DG_MOE_SWIGLU, nvf4 = format == DG_MOE_NVF4;
+  if (gated && nvf4 && hidden % 128 != 0)
+    return set_error(DG_ERR_UNSUPPORTED, "SwiGLU on NVF4 weights needs hidden a multiple of 128");
+  if ((s = check_rows16("X", X, ldx, width)) != DG_OK) return s;
+  if ((s = check_rows16("D", D, ldd, out)) != DG_OK) return s;
+  if (!ids || !aligned4(ids)) return bad("ids is null or not 4-byte aligned");
+  if (!aligned4(weights)) return bad("weights is not 4-byte aligned");
+  if ((s = check_moe_weights("up", up, nvf4, count, hidden * (gated ? 2 : 1), width)) != DG_OK)
+    return s;
+  if ((s = check_moe_weights("down", down, nvf4, count, out, hidden)) != DG_OK) return s;
+  MoeLayerArgs a{};
+  a.nvf4 = nvf4;
+  a.gated = gated;
+  a.bf16 = dtype == DG_BF16;
+  a.tokens = tokens;
+  a.top_k = top_k;
+  a.count = count;
+  a.width = width;
+  a.hidden = hidden;
+  a.out = out;
+  if (!moe_layer_fits(a))
+    return set_error(DG_ERR_UNSUPPORTED, "tokens x width do not fit a CTA's shared memory: "
+                                         "dg_moe_sort and the grouped products take them");
+  const int64_t need = moe_layer_scratch(a);
+  if (!scratch || !aligned16(scratch)) return bad("the scratch is null or not 16-byte aligned");
+  if (scratch_bytes < need)
+    return set_errorf(DG_ERR_INVALID_ARG, "%lld bytes of scratch, need %lld",
+                      (long long)scratch_bytes, (long long)need);
+  CallContext c;
+  if ((s = call_context(&c)) != DG_OK) return s;
+  a.X = X;
+  a.ldx = ldx;
+  a.ids = ids;
+  a.weights = weights;
+  a.up = moe_weights(*up, count);
+  a.down = moe_weights(*down, count);
+  a.D = D;
+  a.ldd = ldd;
+  a.scratch = scratch;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  a.status = c.status;
+  a.timeout_ns = c.timeout_ns;
+  a.sm_count = c.sm_count;
+  return launched(launch_moe_layer(a), "layer launch");
 }
 
 }  // extern "C"

@@ -384,6 +384,37 @@ struct MoeRowsJob {
 cudaError_t launch_moe_dispatch(const MoeRowsJob& j, cudaStream_t stream, int sm_count);
 cudaError_t launch_moe_combine(const MoeRowsJob& j, cudaStream_t stream);
 cudaError_t launch_moe_combine_backward(const MoeRowsJob& j, cudaStream_t stream);
+// The expert layer for a few tokens (moe_layer.cu).
+struct MoeWeights {
+  const void* codes;
+  int64_t ld, stride;  // bytes
+  const void* scales;  // FP8: FP32 block scales (lds, stride_s); NVF4: scale tiles
+  int64_t lds, stride_s;
+  const float* row_scales;  // NVF4
+  const void* bias;  // or NULL
+  int64_t stride_bias;
+};
+struct MoeLayerArgs {
+  bool nvf4, gated;
+  int bf16;
+  int64_t tokens, top_k, count, width, hidden, out;
+  const void* X;
+  int64_t ldx;
+  const int32_t* ids;
+  const float* weights;
+  MoeWeights up, down;
+  void* D;
+  int64_t ldd;
+  void* scratch;
+  cudaStream_t stream;
+  int* status;
+  uint64_t timeout_ns;
+  int sm_count;
+};
+constexpr int64_t kMaxLayerSlots = 512;
+int64_t moe_layer_scratch(const MoeLayerArgs& a);
+bool moe_layer_fits(const MoeLayerArgs& a);
+cudaError_t launch_moe_layer(const MoeLayerArgs& a);
 cudaError_t launch_wait_selftest(cudaStream_t stream, int* status, uint64_t timeout_ns);
 
 // Whether the split-K GEMV reduces `split` splits inside a thread-block
