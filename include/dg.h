@@ -676,12 +676,12 @@ dg_status dg_gemm_nvf4_grouped(int64_t count, int64_t rows, int64_t N, int64_t K
  *   D[t,:] = sum over j of weights[t,j] * (W2_e h + b2_e),  e = ids[t,j],
  *   h = act(W1_e x_t + b1_e)
  * on weights quantized in 8 bits (E4M3 codes with 128 x 128 FP32 scales, as
- * dg_gemm_fp8_grouped's B) or 4 bits (NVF4 stacks).  X is not quantized: sums
- * are FP32, X is exact (a row's values below 2^-25 of its largest are not told
- * from zero), and h, FP32 otherwise, is held with an error of at most 2^-13 of
- * each value or 2^-25 of the largest of 32 around it.  The used experts' weights
- * are read once for up to 8 slots each.  For a decoding step; many tokens are
- * faster through dg_moe_sort and the grouped products.
+ * dg_gemm_fp8_grouped's B) or 4 bits (NVF4 stacks).  X is not quantized: it is
+ * exact (but for values below 2^-31 of their row's largest, which may lose
+ * bits), sums are FP32, and h is rounded once, to 11 bits (FP16 times a power of
+ * two for each 32 of its values).  Infinities and NaNs propagate.  The used
+ * experts' weights are read once for up to 8 slots each.  For a decoding step;
+ * many tokens are faster through dg_moe_sort and the grouped products.
  */
 typedef enum { DG_MOE_FP8 = 0, DG_MOE_NVF4 = 1 } dg_moe_format;
 /* GELU: W1 has `hidden` rows.  SwiGLU: W1 has 2 * hidden rows, gate first;
@@ -703,7 +703,7 @@ typedef struct {
  * tokens x out, FP16 or BF16 (one type), 16-byte aligned, pitches multiples of
  * 8.  up: W1 (hidden or 2 * hidden rows of width), down: W2 (out rows of
  * hidden).  A token without any expert gets zeros; one that names an expert
- * twice has it added twice; a token that holds an infinity or a NaN gets NaN.
+ * twice has it added twice.
  *   scratch: device memory, 16-byte aligned, of at least
  *     dg_moe_layer_scratch(tokens, top_k, hidden, out) bytes (-1 for invalid
  *     sizes), overwritten; it must stay until the stream has passed the call,
@@ -713,9 +713,9 @@ typedef struct {
  * Errors: DG_ERR_INVALID_ARG for sizes, pointers, pitches or strides that break
  * these rules or too little scratch; DG_ERR_UNSUPPORTED for another type, more
  * than 1024 experts, more than 512 slots, more tokens than a CTA's shared
- * memory holds (3 * tokens * (width rounded up to 256, and 16), 12 bytes for
- * each expert and 24 for each slot are at most 146 KiB), or SwiGLU on NVF4
- * weights with hidden not a multiple of 128. */
+ * memory holds (for each token 2 * (width rounded up to a multiple of 256) and 64
+ * bytes, 12 bytes for each token and expert and 28 for each slot are at most 160
+ * KiB, less 32), or SwiGLU on NVF4 weights with hidden not a multiple of 128. */
 int64_t dg_moe_layer_scratch(int64_t tokens, int64_t top_k, int64_t hidden, int64_t out);
 dg_status dg_moe_layer(int64_t tokens, int64_t top_k, int64_t count, int64_t width, int64_t hidden,
                        int64_t out, dg_dtype dtype, const void *X, int64_t ldx, const int32_t *ids,

@@ -138,11 +138,10 @@ def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
     rounding.
 
     A sum of K products errs by at most (K + 200) 2^-23 of the sum of magnitudes
-    (truncated FP32 additions; activations in three parts whose magnitudes add up
-    to at most 1.07 of them, the parts' and slices' sums and the scales a few
-    more), a value of x by 2^-25 of its row's largest, one of h by 2^-13 of itself
-    and 2^-25 of the largest of 32 around it.  GELU's and SiLU's slopes are at most
-    1.13, and they are evaluated to 2e-6."""
+    (truncated FP32 additions, the slices' sums and the scales a few more), a value
+    of x by 2^-39 of its row's largest, one of h by 2^-11 of itself and 2^-39 of the
+    largest of 32 around it.  GELU's and SiLU's slopes are at most 1.13, and they
+    are evaluated to 2e-6."""
     tokens, top_k = ids.shape
     count, out = down.shape[0], down.shape[1]
     u = 2.0 ** -23
@@ -151,7 +150,7 @@ def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
     def product(W, v, verr, bias):
         t = W @ v
         mags = np.abs(W) @ np.abs(v)
-        err = 1.07 * mags * (len(v) + 200) * u + np.abs(W) @ verr
+        err = mags * (len(v) + 200) * u + np.abs(W) @ verr
         if bias is not None:
             t = t + bias
             err = err + (np.abs(t) + np.abs(bias)) * u
@@ -161,7 +160,7 @@ def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
             e = ids[t, j]
             if not 0 <= e < count:
                 continue
-            h, err = product(up[e], x[t], np.full(x.shape[1], np.abs(x[t]).max() * 2.0 ** -25),
+            h, err = product(up[e], x[t], np.full(x.shape[1], np.abs(x[t]).max() * 2.0 ** -39),
                              None if bias_up is None else bias_up[e])
             if gated:
                 n = len(h) // 2
@@ -176,7 +175,7 @@ def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
                 h = fp8_ref.gelu(h)
             pad = np.zeros(-len(h) % 32)
             around = np.repeat(np.concatenate([np.abs(h) + err, pad]).reshape(-1, 32).max(1), 32)
-            err = err + 2.0 ** -13 * (np.abs(h) + err) + 2.0 ** -25 * around[:len(h)]
+            err = err + 2.0 ** -11 * (np.abs(h) + err) + 2.0 ** -39 * around[:len(h)]
             v, ev = product(down[e], h, err, None if bias_down is None else bias_down[e])
             w = 1.0 if weights is None else float(weights[t, j])
             y[t] += w * v

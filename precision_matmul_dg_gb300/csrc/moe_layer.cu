@@ -6,28 +6,36 @@
 // The job is to read the used experts' weights once, at the rate of HBM: 8-bit
 // codes (FP8) or 4-bit codes and their scales (NVF4).  Both kernels are the same
 // machine: a persistent CTA per SM takes units (32 weight rows of one expert, up
-// to 8 of its slots), one thread keeps a ring of TMA loads in flight across
-// units, and 8 warps multiply with warp-level E4M3 MMAs (m16n8k32, weights as the
-// 16-row operand).
+// to 8 of its slots), one thread keeps a ring of loads in flight across units, 8
+// warps multiply with warp-level FP16 MMAs (m16n8k16, weights as the 16-row
+// operand, slots as the 8 columns), and 3 warps take the units' sums in turn and
+// finish them.
 //
-// Activations stay exact: a value times a power of two is split into three E4M3
-// parts, p0 = e4m3(v), p1 = e4m3(16 (v - p0)), p2 = e4m3(16 (16 (v - p0) - p1)),
-// v = p0 + p1 / 16 + p2 / 256.  Each part carries 4 bits and a sign, so 16-bit
-// inputs are represented exactly down to 2^-25 of their row's largest value, and
-// h, FP32 before, with an error of at most 2^-13 of each value or 2^-25 of the
-// largest of 32.  The parts are columns of the MMA of their own, and with a slot
-// or two per expert they cost nothing: the 8 columns are there anyway.
+// Codes become FP16 exactly (an E4M3 value; an E2M1 value times its block's E4M3
+// scale, 6 significant bits) by the pair conversions.  (E4M3 MMAs, which take FP8
+// codes as they are, want the activations in three parts, and 4-bit codes' two
+// blocks in columns of their own: 1340 clocks a stage of NVF4 against the 780 that
+// HBM needs for it.)  Activations are FP16 times a power of two: x exactly, h
+// rounded once, each 32 of its values with a power of their own, so that h has
+// FP32's range.
 //
-// 4-bit codes become E4M3 by two shifts and masks per four codes (e2m1 = 64
-// times the E4M3 value with the same bits) and keep their order in memory, so 32
-// values of an MMA lie in two blocks with a scale each.  Each part therefore
-// takes two columns, one for each block, with zeros in the other block's place.
+// What a lane needs for 32 values of K is then 16 bytes: in a 16-byte piece of a
+// weight row as ldmatrix hands it out, lane q of a row's four has 4 (FP8) or 8
+// (NVF4) codes, and the order of K inside an MMA is free as long as both operands
+// share it.  FP8's 32 values are two pieces, so activations are stored with 4 of
+// the one beside 4 of the other.
 //
-// Units that end in the same outputs meet in fixed order: slots' sums go to
-// scratch, and whichever warp finishes the last slot of a token (counted by
-// atomics that the results do not depend on) adds them in the order of j.
+// h lies in scratch as the second kernel reads it: by K stage, then slot in
+// sorted order, so that one bulk copy brings a unit's slots of a stage, values
+// and scales.  Few copies matter: a TMA copy costs the issuing thread about 80
+// clocks (with one for each K block and 8 rows, 990 clocks a stage).
+//
+// Slots' sums go to scratch, and whichever warp finishes the last slot of a token
+// (counted by atomics that the results do not depend on) adds them in the order
+// of j.
 #include <algorithm>
 
+#include "convert.cuh"
 #include "epilogue.cuh"
 #include "fp8.cuh"
 #include "tc_common.cuh"
@@ -37,18 +45,47 @@ namespace {
 
 using namespace fp8;
 
-constexpr int kMmaWarps = 8;
-constexpr int kThreads = (kMmaWarps + 1) * 32;
+constexpr int kMmaWarps = 8, kTmaWarp = 8, kEpiWarp = 9, kEpiWarps = 3;
+constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;
+constexpr int kOtherThreads = kThreads - kMmaWarps * 32;  // they build the routing
 constexpr int kTileRows = 32;  // weight rows per unit (twice as many where gated)
 constexpr int kMaxChunk = 8;   // slots per unit
+constexpr int kMaxStages = 8;
 
 enum : int { kFp8 = 0, kNvf4 = 1 };
+
+// What differs between the kernels: row groups of 16, the warps that share a
+// group's K blocks (the blocks of a stage), values in a K block (128 bytes of each
+// weight row), bytes of a stage's weights and of their scales.
+template <int Fmt, bool Down, bool Gated>
+struct Shape {
+  static constexpr int RG = Gated ? 4 : 2;
+  static constexpr int kSlices = kMmaWarps / RG;
+  static constexpr int kBlockK = Fmt == kFp8 ? 128 : 256;
+  static constexpr int kBlockW = kTileRows * 128;
+  static constexpr int kW = (Gated ? 2 : 1) * kSlices * kBlockW;
+  static constexpr int kS = Fmt == kNvf4 ? (Gated ? 2 : 1) * kSlices * 2048 : 0;
+  static constexpr int kRed = kEpiWarps * kMmaWarps * 4 * 32 * 4;
+  static constexpr int kBars = (2 * kMaxStages + 2 * kEpiWarps) * 8 + 8;
+};
+// A slot's share of a stage of the second product: FP16 values, then a scale for
+// each 32 of them.  Rows are 64 bytes apart in their banks: two rows' 64-byte
+// reads do not meet.
+template <int Fmt>
+struct HRow {
+  static constexpr int kK =
+      Shape<Fmt, true, false>::kSlices * Shape<Fmt, true, false>::kBlockK;
+  static constexpr int kScales = 2 * kK;
+  static constexpr int kBytes = kScales + kK / 32 * 4 + (Fmt == kNvf4 ? 64 : 0);
+  static_assert(kBytes % 128 == 64, "banks");
+};
 
 struct LayerParams {
   const int32_t* ids;
   int tokens, top_k, slots, count, chunk;
-  // the phase's product: K values (k_blocks of 128 bytes), `rows` results
-  int K, k_blocks, k_tiles, rows, tiles, up0;
+  // the phase's product: K values (k_blocks of 128 bytes, full_blocks of them whole,
+  // k_tiles scale tiles), `rows` results
+  int K, k_blocks, full_blocks, k_tiles, rows, tiles, up0;
   int w_rows, sf_rows;       // weight rows, scale tile rows from one expert to the next
   const float* sw;           // FP8 block scales
   int64_t lds_w, stride_sw;
@@ -59,18 +96,16 @@ struct LayerParams {
   int bf16;                  // X, D and the biases
   const uint16_t* X;
   int64_t ldx;
-  int x_pitch;               // bytes of a row of parts in shared memory
-  uint8_t* h;                // parts of h, 3 rows per slot in sorted order, ldh bytes each
-  int64_t ldh;
-  float* hs;                 // their scales, one per 32 values, hs_ld per slot
-  int hs_ld;
+  int x_pitch;               // bytes of a token in shared memory
+  uint8_t* h;                // [K stage][slot][HRow]
+  int h_stages;
   float* part;               // slots' sums of the second product
   unsigned* done;            // [tiles][tokens]: slots finished
   int done_words;
   const float* weights;
   uint16_t* D;
   int64_t ldd;
-  int stages, act_boxes, block_bytes;
+  int stages, stage_bytes;
   int off_x, off_red, off_route;
   int* status;
   uint64_t timeout_ns;
@@ -79,24 +114,26 @@ struct LayerParams {
 // The routing in shared memory: slots sorted by expert (stable), cut into
 // chunks of at most `chunk` slots of one expert.
 struct Route {
-  int *pos, *slot;         // slot -> sorted place (-1: dropped), and back
-  int *expert, *first, *n; // per chunk
-  int *valid;              // per token: its slots that are not dropped
-  float* fx;               // per token: what its parts are multiplied by
-  unsigned* amax;          // per token
+  int *pos, *token;          // slot -> sorted place (-1: dropped); sorted place -> token
+  int *expert, *first, *n;   // per chunk
+  float* weight;             // per slot
+  int* valid;                // per token: its slots that are not dropped
+  float* fx;                 // per token: what its values are multiplied by
+  unsigned* amax;            // per token
   int* ids;
-  int *cnt, *start, *base; // per expert
-  int* chunks;             // their number
+  int *cnt, *start, *base;   // per expert
+  int* chunks;               // their number
 };
 __device__ __forceinline__ Route route_at(int* m, const LayerParams& p) {
   Route r;
   r.ids = m;
   r.pos = r.ids + (p.slots + 3) / 4 * 4;
-  r.slot = r.pos + p.slots;
-  r.expert = r.slot + p.slots;
+  r.token = r.pos + p.slots;
+  r.expert = r.token + p.slots;
   r.first = r.expert + p.slots;
   r.n = r.first + p.slots;
-  r.valid = r.n + p.slots;
+  r.weight = reinterpret_cast<float*>(r.n + p.slots);
+  r.valid = r.n + 2 * p.slots;
   r.fx = reinterpret_cast<float*>(r.valid + p.tokens);
   r.amax = reinterpret_cast<unsigned*>(r.fx + p.tokens);
   r.cnt = reinterpret_cast<int*>(r.amax + p.tokens);
@@ -106,97 +143,110 @@ __device__ __forceinline__ Route route_at(int* m, const LayerParams& p) {
   return r;
 }
 int route_bytes(int64_t slots, int64_t tokens, int64_t count) {
-  return static_cast<int>(4 * ((slots + 3) / 4 * 4 + 5 * slots + 3 * tokens + 3 * count + 4));
+  return static_cast<int>(4 * ((slots + 3) / 4 * 4 + 6 * slots + 3 * tokens + 3 * count + 4));
 }
 
-// All threads of the CTA; ends with a barrier.
-__device__ __forceinline__ void build_route(const Route& r, const LayerParams& p) {
-  for (int e = threadIdx.x; e < p.count; e += kThreads) r.cnt[e] = 0;
-  for (int t = threadIdx.x; t < p.tokens; t += kThreads) r.valid[t] = 0, r.amax[t] = 0u;
-  for (int s = threadIdx.x; s < (p.slots + 3) / 4 * 4; s += kThreads) {
+__device__ __forceinline__ void others_sync() {
+  asm volatile("bar.sync 2, %0;" ::"n"(kOtherThreads) : "memory");
+}
+
+// By the kOtherThreads threads that do not multiply, numbered i.
+__device__ __forceinline__ void build_route(const Route& r, const LayerParams& p, int i) {
+  for (int e = i; e < p.count; e += kOtherThreads) r.cnt[e] = 0;
+  for (int t = i; t < p.tokens; t += kOtherThreads) r.valid[t] = 0;
+  for (int s = i; s < (p.slots + 3) / 4 * 4; s += kOtherThreads) {
     const int e = s < p.slots ? __ldg(p.ids + s) : -1;
     r.ids[s] = e >= 0 && e < p.count ? e : -1;
+    if (s < p.slots) r.weight[s] = p.weights ? __ldg(p.weights + s) : 1.0f;
   }
-  __syncthreads();
-  for (int s = threadIdx.x; s < p.slots; s += kThreads) {
+  others_sync();
+  for (int s = i; s < p.slots; s += kOtherThreads) {
     const int e = r.ids[s];
     int rank = -1;
     if (e >= 0) {
       rank = 0;  // slots of this expert before s
       const int4* v = reinterpret_cast<const int4*>(r.ids);
-      for (int i = 0; i <= s / 4; ++i) {
-        const int4 w = v[i];
-        rank += (4 * i < s && w.x == e) + (4 * i + 1 < s && w.y == e) + (4 * i + 2 < s && w.z == e) +
-                (4 * i + 3 < s && w.w == e);
+      for (int k = 0; k <= s / 4; ++k) {
+        const int4 w = v[k];
+        rank += (4 * k < s && w.x == e) + (4 * k + 1 < s && w.y == e) + (4 * k + 2 < s && w.z == e) +
+                (4 * k + 3 < s && w.w == e);
       }
       atomicAdd(&r.cnt[e], 1);  // counts: the order does not matter
       atomicAdd(&r.valid[s / p.top_k], 1);
     }
     r.pos[s] = rank;
   }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
+  others_sync();
+  if (i < 32) {
     int run = 0, run_c = 0;
     for (int e0 = 0; e0 < p.count; e0 += 32) {
-      const int e = e0 + lane;
+      const int e = e0 + i;
       const int c = e < p.count ? r.cnt[e] : 0, k = (c + p.chunk - 1) / p.chunk;
-      int v = c, w = k;
+      int v = c | k << 16;  // (at most 512 each)
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, v, d), b = __shfl_up_sync(0xffffffffu, w, d);
-        if (lane >= d) v += a, w += b;
+        const int a = __shfl_up_sync(0xffffffffu, v, d);
+        if (i >= d) v += a;
       }
-      if (e < p.count) r.start[e] = run + v - c, r.base[e] = run_c + w - k;
-      run += __shfl_sync(0xffffffffu, v, 31);
-      run_c += __shfl_sync(0xffffffffu, w, 31);
+      if (e < p.count) r.start[e] = run + (v & 0xFFFF) - c, r.base[e] = run_c + (v >> 16) - k;
+      const int last = __shfl_sync(0xffffffffu, v, 31);
+      run += last & 0xFFFF;
+      run_c += last >> 16;
     }
-    if (lane == 0) *r.chunks = run_c;
+    if (i == 0) *r.chunks = run_c;
   }
-  __syncthreads();
-  for (int s = threadIdx.x; s < p.slots; s += kThreads)
+  others_sync();
+  for (int s = i; s < p.slots; s += kOtherThreads)
     if (r.ids[s] >= 0) {
       const int at = r.start[r.ids[s]] + r.pos[s];
       r.pos[s] = at;
-      r.slot[at] = s;
+      r.token[at] = s / p.top_k;
     }
-  for (int e = threadIdx.x; e < p.count; e += kThreads) {
+  for (int e = i; e < p.count; e += kOtherThreads) {
     const int c = r.cnt[e];
-    for (int i = 0, k = r.base[e]; i < c; i += p.chunk, ++k) {
+    for (int at = 0, k = r.base[e]; at < c; at += p.chunk, ++k) {
       r.expert[k] = e;
-      r.first[k] = r.start[e] + i;
-      r.n[k] = min(p.chunk, c - i);
+      r.first[k] = r.start[e] + at;
+      r.n[k] = min(p.chunk, c - at);
     }
   }
-  __syncthreads();
 }
 
-// The power of two f with amax f in (224, 448], as its inverse; 1 for zero.
-__device__ __forceinline__ float parts_factor(float amax, float& inverse) {
-  const uint32_t b = __float_as_uint(amax);
-  // 448 = 1.75 * 2^8
-  int e = 127 + 8 - static_cast<int>(b >> 23) - ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  e = min(max(e, -120), 120);
-  if (amax == 0.0f) e = 0;
+// A CTA's units, chunk by chunk of a tile (neighbours share a tile's place in
+// different experts, or the weights).
+struct UnitWalk {
+  int tile, u, chunks, d_tile, d_u;
+  __device__ __forceinline__ void start(int first, int step, int chunks_) {
+    chunks = max(chunks_, 1);
+    tile = first / chunks;
+    u = first - tile * chunks;
+    d_tile = step / chunks;
+    d_u = step - d_tile * chunks;
+  }
+  __device__ __forceinline__ void next() {
+    tile += d_tile;
+    u += d_u;
+    if (u >= chunks) {
+      u -= chunks;
+      ++tile;
+    }
+  }
+};
+
+// The power of two that brings amax into [2^14, 2^15), and its inverse; 1 for
+// zero.
+__device__ __forceinline__ float half_factor(float amax, float& inverse) {
+  int e = 127 + 14 - static_cast<int>(__float_as_uint(amax) >> 23);
+  e = amax == 0.0f ? 0 : min(max(e, -120), 120);
   inverse = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
-__device__ __forceinline__ float2 e4m3x2_values(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  return F16::unpack(h);
-}
-// Four scaled values -> their three parts, four codes each.
-__device__ __forceinline__ void split4(float (&v)[4], uint32_t (&part)[3]) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    part[i] = e4m3x4(v[0], v[1], v[2], v[3]);
-    if (i == 2) break;
-    const float2 a = e4m3x2_values(part[i] & 0xFFFFu), b = e4m3x2_values(part[i] >> 16);
-    v[0] = 16.0f * (v[0] - a.x), v[1] = 16.0f * (v[1] - a.y);
-    v[2] = 16.0f * (v[2] - b.x), v[3] = 16.0f * (v[3] - b.y);
-  }
+// Where value k of 32 lies: NVF4's in order, FP8's 4 of the first 16 beside 4 of
+// the second.
+template <int Fmt>
+__device__ __forceinline__ int place_of(int k) {
+  return Fmt == kNvf4 ? k : (k & 12) << 1 | (k & 16) >> 2 | (k & 3);
 }
 
 // Eight 16-bit values of a row of K from k on, zeros past its end.
@@ -211,56 +261,76 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int K) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// The largest finite magnitude of two bfloat16 values, as bits.
+__device__ __forceinline__ uint32_t finite_max(uint32_t w) {
+  const uint32_t a = w & 0x7FFFu, b = w >> 16 & 0x7FFFu;
+  return max(a < BF16::kInf ? a : 0u, b < BF16::kInf ? b : 0u);
+}
+__device__ __forceinline__ uint32_t scaled_half2(uint32_t w, float f) {
+  const float2 v = BF16::unpack(w);
+  return F16::pack(v.x * f, v.y * f);
+}
 
-// The tokens' parts in shared memory, three rows per token; 4-bit weights'
-// order: of each 32 values the even ones, then the odd ones.  A token with an
-// infinity or a NaN has parts of zeros and the factor NaN.
-template <int Fmt, typename T>
-__device__ __forceinline__ void load_tokens(const LayerParams& p, uint8_t* parts, const Route& r) {
-  const int padded = p.k_blocks * (Fmt == kFp8 ? 128 : 256);
-  const int per_row = (padded + 255) / 256 * 32;  // pieces of 8 values: whole warps
+// The tokens in shared memory as FP16, by the MMA warps: FP16 as it is, BF16
+// times a power of two per token that brings its largest finite value near the
+// top (infinities and NaNs stay what they are).
+template <int Fmt>
+__device__ __forceinline__ void load_tokens(const LayerParams& p, uint8_t* xs, const Route& r) {
+  constexpr int kAhead = 4;
+  const int per_row = p.k_blocks * Shape<Fmt, false, false>::kBlockK / 8;  // pieces, a multiple of 16
   const int pieces = p.tokens * per_row;
-  for (int i = threadIdx.x; i < pieces; i += kMmaWarps * 32) {
-    const int t = i / per_row, k = (i - t * per_row) * 8;
-    const uint4 v = load8(p.X + t * p.ldx, k, p.K);
-    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                          __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-    m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-    if ((threadIdx.x & 31) == 0) atomicMax(&r.amax[t], m);
+  if (p.bf16) {
+    for (int t = threadIdx.x; t < p.tokens; t += kMmaWarps * 32) r.amax[t] = 0u;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += kAhead * kMmaWarps * 32) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * kMmaWarps * 32, t = i / per_row;
+        v[j] = i < pieces ? load8(p.X + t * p.ldx, (i - t * per_row) * 8, p.K)
+                          : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * kMmaWarps * 32;
+        uint32_t m = max(max(finite_max(v[j].x), finite_max(v[j].y)),
+                         max(finite_max(v[j].z), finite_max(v[j].w)));
+        // (16 lanes share a token at least)
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(__activemask(), m, d));
+        if ((threadIdx.x & 15) == 0 && i < pieces) atomicMax(&r.amax[i / per_row], m);
+      }
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
   }
-  asm volatile("bar.sync 1, 256;" ::: "memory");
-  for (int i = threadIdx.x; i < pieces; i += kMmaWarps * 32) {
-    const int t = i / per_row, k = (i - t * per_row) * 8;
-    const unsigned bits = r.amax[t];
-    const bool odd = bits >= T::kInf;
-    float inv;
-    const float f = parts_factor(T::one(odd ? 0u : bits), inv);
-    if (k == 0) r.fx[t] = odd ? CUDART_NAN_F : inv;
-    const uint4 v = odd ? make_uint4(0u, 0u, 0u, 0u) : load8(p.X + t * p.ldx, k, p.K);
-    const float2 a = T::unpack(v.x), b = T::unpack(v.y), c = T::unpack(v.z), d = T::unpack(v.w);
-    if (k >= padded) continue;
-    uint8_t* row = parts + t * 3 * p.x_pitch;
-    uint32_t lo[3], hi[3];
-    if (Fmt == kFp8) {
-      float x[4] = {a.x * f, a.y * f, b.x * f, b.y * f}, y[4] = {c.x * f, c.y * f, d.x * f, d.y * f};
-      split4(x, lo);
-      split4(y, hi);
+  for (int i0 = threadIdx.x; i0 < pieces; i0 += kAhead * kMmaWarps * 32) {
+    uint4 v[kAhead];
 #pragma unroll
-      for (int i3 = 0; i3 < 3; ++i3)
-        *reinterpret_cast<uint2*>(row + i3 * p.x_pitch + k) = make_uint2(lo[i3], hi[i3]);
-    } else {
-      float x[4] = {a.x * f, b.x * f, c.x * f, d.x * f}, y[4] = {a.y * f, b.y * f, c.y * f, d.y * f};
-      split4(x, lo);
-      split4(y, hi);
-      const int at = (k & ~31) + (k & 31) / 2;
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j * kMmaWarps * 32, t = i / per_row;
+      if (i < pieces) v[j] = load8(p.X + t * p.ldx, (i - t * per_row) * 8, p.K);
+    }
 #pragma unroll
-      for (int i3 = 0; i3 < 3; ++i3) {
-        *reinterpret_cast<uint32_t*>(row + i3 * p.x_pitch + at) = lo[i3];
-        *reinterpret_cast<uint32_t*>(row + i3 * p.x_pitch + at + 16) = hi[i3];
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j * kMmaWarps * 32, t = i / per_row, k = (i - t * per_row) * 8;
+      if (i >= pieces) break;
+      float inv = 1.0f;
+      if (p.bf16) {
+        const float f = half_factor(BF16::one(r.amax[t]), inv);
+        v[j] = make_uint4(scaled_half2(v[j].x, f), scaled_half2(v[j].y, f),
+                          scaled_half2(v[j].z, f), scaled_half2(v[j].w, f));
+      }
+      if (k == 0) r.fx[t] = inv;
+      uint8_t* row = xs + t * p.x_pitch + (k & ~31) * 2;
+      if (Fmt == kNvf4) {
+        *reinterpret_cast<uint4*>(row + (k & 31) * 2) = v[j];
+      } else {
+        *reinterpret_cast<uint2*>(row + place_of<kFp8>(k & 31) * 2) = make_uint2(v[j].x, v[j].y);
+        *reinterpret_cast<uint2*>(row + place_of<kFp8>((k & 31) + 4) * 2) =
+            make_uint2(v[j].z, v[j].w);
       }
     }
   }
-  asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -269,22 +339,50 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-// c += a (16 x 32, weights) . b (32 x 8, activations)
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ uint32_t ld_shared1(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// c += a (16 x 16, weights) . b (16 x 8, activations)
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The low (high) nibbles of four bytes of E2M1 codes as E4M3 codes of 1/64 of
-// their values: sign to bit 7, exponent and mantissa to bits 4 .. 2.
-__device__ __forceinline__ uint32_t e4m3_of_low(uint32_t w) {
-  return ((w << 4) & 0x80808080u) | ((w << 2) & 0x1C1C1C1Cu);
+// Four E4M3 codes -> two FP16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-__device__ __forceinline__ uint32_t e4m3_of_high(uint32_t w) {
-  return (w & 0x80808080u) | ((w >> 2) & 0x1C1C1C1Cu);
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// The scales (E4M3 codes in bytes `at` and at + 2 of a word) as FP16 pairs of
+// the same value.
+__device__ __forceinline__ void scale_pairs(uint32_t word, uint32_t at, uint32_t (&s)[2]) {
+  const uint32_t two = __byte_perm(word, 0u, 0x4420u + 0x0011u * at);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  s[0] = __byte_perm(h, 0u, 0x1010);
+  s[1] = __byte_perm(h, 0u, 0x3232);
 }
 
 __device__ __forceinline__ float as_f32(const void* p, int64_t i, int bf16) {
@@ -296,32 +394,28 @@ __device__ __forceinline__ float silu(float g) {
   return __fdividef(g, 1.0f + ex2_approx(-kLog2e * g));
 }
 
-// Down: the second product (its activations come with the ring's stages).  NT:
-// tiles of 8 columns that a unit can have.
-template <int Fmt, bool Down, bool Gated, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+// Down: the second product (its activations come with the ring's stages).
+template <int Fmt, bool Down, bool Gated>
+__global__ void __launch_bounds__(kThreads, 2)
     moe_layer_kernel(const __grid_constant__ CUtensorMap tmap_w,
+                     const __grid_constant__ CUtensorMap tmap_tail,
                      const __grid_constant__ CUtensorMap tmap_sf,
-                     const __grid_constant__ CUtensorMap tmap_h,
                      const __grid_constant__ LayerParams p) {
   static_assert(!(Down && Gated), "the second product has no gate");
-  constexpr int RG = Gated ? 4 : 2;        // groups of 16 rows
-  constexpr int kSlices = kMmaWarps / RG;  // warps that share a group's K blocks
-  constexpr int kBlockW = 16 * RG * 128;
-  constexpr int kBlockS = Fmt == kNvf4 ? RG / 2 * 2048 : 0;
-  constexpr int kAcc = Fmt == kFp8 ? 4 : 2;         // sums per lane and column tile
-  constexpr int kPerTile = Fmt == kFp8 ? 8 : 4;     // parts per column tile
-  constexpr int kActHalves = Fmt == kFp8 ? 1 : 2;   // 128-byte pieces of a block's activations
+  using S = Shape<Fmt, Down, Gated>;
+  using H = HRow<Fmt>;
+  constexpr int RG = S::RG, kSlices = S::kSlices;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int stage_bytes = kSlices * p.block_bytes;
-  uint8_t* xparts = smem + p.off_x;
-  float* red = reinterpret_cast<float*>(smem + p.off_red);  // [2][warp][NT * kAcc][lane]
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(red + 2 * kMmaWarps * NT * kAcc * 32);
-  uint64_t* empty_bar = full_bar + p.stages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty_bar + p.stages);
+  uint8_t* xs = smem + p.off_x;
+  float* red = reinterpret_cast<float*>(smem + p.off_red);  // [kEpiWarps][warp][4][lane]
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + p.off_red + S::kRed);
+  uint64_t* empty_bar = full_bar + kMaxStages;
+  uint64_t* red_full = empty_bar + kMaxStages;
+  uint64_t* red_empty = red_full + kEpiWarps;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(red_empty + kEpiWarps);
   const Route r = route_at(reinterpret_cast<int*>(smem + p.off_route), p);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -329,24 +423,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], kMmaWarps);
     }
+    for (int b = 0; b < kEpiWarps; ++b) {
+      mbar_init(&red_full[b], kMmaWarps);
+      mbar_init(&red_empty[b], 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarps && lane == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tmap_w);
+    tma_prefetch_desc(&tmap_tail);
     if (Fmt == kNvf4) tma_prefetch_desc(&tmap_sf);
-    if (Down) tma_prefetch_desc(&tmap_h);
   }
   // The second kernel starts while the first one runs: what it reads before it
-  // waits (choices and weights) was there before the first, which waited for
-  // every kernel before it ahead of letting this one start.
+  // waits (choices, routing weights and weights) was there before the first, which
+  // waited for every kernel before it ahead of letting this one start.
   if (!Down) grid_dependency_wait();
-  build_route(r, p);
+  if (warp >= kMmaWarps)
+    build_route(r, p, static_cast<int>(threadIdx.x) - kMmaWarps * 32);
+  else if (!Down)
+    load_tokens<Fmt>(p, xs, r);
+  __syncthreads();
   const int chunks = *r.chunks;
   const int units = chunks * p.tiles;
   const int k_stages = (p.k_blocks + kSlices - 1) / kSlices;
+  const int step = static_cast<int>(gridDim.x);
+  UnitWalk walk{};
 
-  if (warp == kMmaWarps) {
+  if (warp == kTmaWarp) {
     // ------------------------------------------------------------ producer
     if (!elect_one_lane()) return;
     const uint64_t stream = policy_evict_first(), keep = policy_evict_last();
@@ -354,59 +458,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    // the loads of K stage ks of unit t: weights, or activations
-    auto load = [&](int t, int ks, int st, bool weights, bool acts) {
-      const int tile = t / chunks, u = t - tile * chunks;
-      const int e = r.expert[u];
-      const int b0 = ks * kSlices, n = min(kSlices, p.k_blocks - b0);
-      const int boxes = Down ? (3 * r.n[u] + 7) / 8 : 0;
-      uint8_t* dst = smem + st * stage_bytes;
-      if (weights)
-        mbar_arrive_expect_tx(&full_bar[st], static_cast<uint32_t>(
-                                                 n * (kBlockW + kBlockS + boxes * kActHalves * 1024)));
-      for (int j = 0; j < n; ++j, dst += p.block_bytes) {
-        const int kb = b0 + j;
-        if (weights) {
-          const int row = e * p.w_rows + tile * kTileRows;
-          tma_load_2d(&tmap_w, &full_bar[st], dst, kb * 128, row, stream);
-          if (Gated)
-            tma_load_2d(&tmap_w, &full_bar[st], dst + kBlockW / 2, kb * 128, row + p.up0, stream);
-          if (Fmt == kNvf4) {
-            const int sf = (e * p.sf_rows + (tile >> 2)) * p.k_tiles + 4 * kb;
-            tma_load_2d(&tmap_sf, &full_bar[st], dst + kBlockW, 0, sf, keep);
-            if (Gated)
-              tma_load_2d(&tmap_sf, &full_bar[st], dst + kBlockW + 2048, 0,
-                          sf + (p.up0 >> 7) * p.k_tiles, keep);
-          }
-        }
-        if (Down && acts)
-          for (int b = 0; b < boxes; ++b)
+    // the loads of K stage ks of a unit: weights, or activations
+    auto load = [&](int ks, int st, int e, bool weights, bool acts) {
+      uint8_t* dst = smem + st * p.stage_bytes;
+      uint64_t* bar = &full_bar[st];
+      const int b0 = ks * kSlices;
+      const int h_bytes = Down ? r.n[walk.u] * H::kBytes : 0;
+      if (weights) {
+        const int row = e * p.w_rows + walk.tile * kTileRows;
+        const bool whole = b0 + kSlices <= p.full_blocks;
+        const int n = whole ? kSlices : min(kSlices, p.k_blocks - b0);
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * (S::kW / kSlices) + S::kS + h_bytes));
 #pragma unroll
-            for (int h = 0; h < kActHalves; ++h)
-              tma_load_2d(&tmap_h, &full_bar[st],
-                          dst + kBlockW + kBlockS + (b * kActHalves + h) * 1024,
-                          (kb * kActHalves + h) * 128, 3 * r.first[u] + 8 * b, keep);
+        for (int g = 0; g < (Gated ? 2 : 1); ++g) {
+          uint8_t* to = dst + g * kSlices * S::kBlockW;
+          if (whole) {
+            tma_load_3d(&tmap_w, bar, to, 0, row + g * p.up0, b0, stream);
+          } else {
+            for (int j = 0; j < n; ++j)
+              tma_load_2d(&tmap_tail, bar, to + j * S::kBlockW, (b0 + j) * 128, row + g * p.up0,
+                          stream);
+          }
+          if (Fmt == kNvf4)
+            tma_load_2d(&tmap_sf, bar, dst + S::kW + g * kSlices * 2048, 0,
+                        (e * p.sf_rows + (walk.tile >> 2) + g * (p.up0 >> 7)) * p.k_tiles + 4 * b0,
+                        keep);
+        }
       }
+      if (Down && acts)
+        bulk_load_g2s(dst + S::kW + S::kS,
+                      p.h + (static_cast<int64_t>(ks) * p.slots + r.first[walk.u]) * H::kBytes,
+                      static_cast<uint32_t>(h_bytes), bar, keep);
     };
     int64_t ahead = 0;
     if (Down) {
       // the first stages' weights before the first kernel has finished
-      int st = 0;
-      for (int t = blockIdx.x; t < units && st < p.stages; t += gridDim.x)
-        for (int ks = 0; ks < k_stages && st < p.stages; ++ks, ++st) load(t, ks, st, true, false);
-      ahead = st;
-      grid_dependency_wait();
-      st = 0;
-      for (int t = blockIdx.x; t < units && st < ahead; t += gridDim.x)
-        for (int ks = 0; ks < k_stages && st < ahead; ++ks, ++st) load(t, ks, st, false, true);
+      for (int pass = 0; pass < 2; ++pass) {
+        int st = 0;
+        walk.start(blockIdx.x, step, chunks);
+        for (; walk.tile < p.tiles && units > 0 && st < p.stages; walk.next()) {
+          const int e = r.expert[walk.u];
+          for (int ks = 0; ks < k_stages && st < p.stages; ++ks, ++st)
+            load(ks, st, e, pass == 0, pass == 1);
+        }
+        ahead = st;
+        if (pass == 0) grid_dependency_wait();
+      }
     }
-    for (int t = blockIdx.x; t < units && ok; t += gridDim.x)
+    walk.start(blockIdx.x, step, chunks);
+    for (; walk.tile < p.tiles && units > 0 && ok; walk.next()) {
+      const int e = r.expert[walk.u];
       for (int ks = 0; ks < k_stages; ++ks) {
         if (issued >= ahead) {
           ok = mbar_wait_abortable(&empty_bar[stage], phase ^ 1, p.timeout_ns, p.status,
                                    abort_flag);
           if (!ok) break;
-          load(t, ks, stage, true, true);
+          load(ks, stage, e, true, true);
         }
         ++issued;
         if (++stage == p.stages) {
@@ -414,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1;
         }
       }
+    }
     grid_launch_dependents();
     if (!ok) *abort_flag = 1;
     // the copies land before the CTA goes away, whoever gave up
@@ -424,189 +532,286 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  // ------------------------------------------------------------------- MMAs
-  if (Down) {
-    grid_dependency_wait();
-    // tokens without an expert
-    for (int t = 0; t < p.tokens; ++t)
-      if (r.valid[t] == 0)
-        for (int n = blockIdx.x * 256 + threadIdx.x; n < p.rows; n += gridDim.x * 256)
-          p.D[t * p.ldd + n] = 0;
-  } else {
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < p.done_words; i += gridDim.x * 256)
-      p.done[i] = 0u;
-    if (p.bf16)
-      load_tokens<Fmt, BF16>(p, xparts, r);
-    else
-      load_tokens<Fmt, F16>(p, xparts, r);
-  }
-  const int g = lane >> 2, q = lane & 3;
-  const int group = warp % RG, slice = warp / RG;
-  // ldmatrix: lanes 8 i .. 8 i + 7 give the rows of matrix i
-  const int mat = lane >> 3, mrow = lane & 7;
-  // weights: matrices (rows 0-7, piece), (rows 8-15, piece), and of the next piece
-  const int a_row = mrow + 8 * (mat & 1);
-  const uint32_t a_base = static_cast<uint32_t>((group * 16 + a_row) * 128);
-  const uint32_t a_swz = static_cast<uint32_t>(a_row & 7);
-  const uint32_t b_mask = (q >> 1) == (g & 1) ? 0xffffffffu : 0u;  // NVF4: the column's block
-  const uint32_t smem0 = smem_addr(smem);
-  int stage = 0, turn = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  for (int t = blockIdx.x; t < units; t += gridDim.x) {
-    const int tile = t / chunks, u = t - tile * chunks;
-    const int e = r.expert[u], n = r.n[u], first = r.first[u];
-    const int cols = (3 * n + kPerTile - 1) / kPerTile;  // column tiles in use
-    float acc[NT][kAcc];
-    uint32_t b_base[NT];   // this lane's row of activations for ldmatrix
-    const float* hs[NT][2];
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-#pragma unroll
-      for (int i = 0; i < kAcc; ++i) acc[c][i] = 0.0f;
-      // the part of this lane's column (past the last: the last's)
-      const int part = min(c * kPerTile + (Fmt == kFp8 ? mrow : mrow >> 1), 3 * n - 1);
-      if (!Down)
-        b_base[c] = smem_addr(xparts) +
-                    static_cast<uint32_t>((r.slot[first + part / 3] / p.top_k * 3 + part % 3) * p.x_pitch);
-      else
-        b_base[c] = static_cast<uint32_t>((part >> 3) * kActHalves * 1024 + (part & 7) * 128);
-      if (Down)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int mine = min(c * kPerTile + (Fmt == kFp8 ? 2 * q + i : q), 3 * n - 1);
-          hs[c][i] = p.hs + static_cast<int64_t>(first + mine / 3) * p.hs_ld;
-        }
+  if (warp >= kEpiWarp) {
+    // ------------------------------------------------------------ epilogue
+    // The CTA's i-th unit is this warp's where i = mine modulo kEpiWarps; lane =
+    // row of the tile.
+    const int mine = warp - kEpiWarp;
+    const int first_word = (static_cast<int>(blockIdx.x) * kEpiWarps + mine) * 32 + lane;
+    if (Down) {
+      grid_dependency_wait();
+      // tokens without an expert
+      for (int t = 0; t < p.tokens; ++t)
+        if (r.valid[t] == 0)
+          for (int n = first_word; n < p.rows; n += step * kEpiWarps * 32) p.D[t * p.ldd + n] = 0;
+    } else {
+      for (int i = first_word; i < p.done_words; i += step * kEpiWarps * 32) p.done[i] = 0u;
     }
-    // FP8: the scales of this lane's rows' weight blocks
-    const float *swa = nullptr, *swb = nullptr;
-    if (Fmt == kFp8) {
-      const int row = (Gated && group >= 2 ? p.up0 - 32 : 0) + tile * kTileRows + group * 16 + g;
-      const int last = p.rows - 1 + (Gated && group >= 2 ? p.up0 : 0);
-      const float* sw = p.sw + e * p.stride_sw;
-      swa = sw + static_cast<int64_t>(min(row, last) / 128) * p.lds_w;
-      swb = sw + static_cast<int64_t>(min(row + 8, last) / 128) * p.lds_w;
-    }
-    // the block's scales (of weights, and of h), loaded a stage ahead
-    float sa = 0.0f, sb = 0.0f, sa_next = 0.0f, sb_next = 0.0f;
-    float hv[NT][2][Fmt == kFp8 ? 4 : 8], hv_next[NT][2][Fmt == kFp8 ? 4 : 8];
-    auto load_scales = [&](int kb) {
-      kb = min(kb, p.k_blocks - 1);
-      if (Fmt == kFp8) {
-        sa_next = __ldg(swa + kb);
-        sb_next = __ldg(swb + kb);
+    const float* all = red + mine * kMmaWarps * 4 * 32;
+    uint32_t phase = 0;
+    walk.start(blockIdx.x + mine * step, kEpiWarps * step, chunks);
+    for (; walk.tile < p.tiles && units > 0; walk.next(), phase ^= 1) {
+      const int tile = walk.tile, u = walk.u;
+      const int e = r.expert[u], n = r.n[u], first = r.first[u];
+      const int row = tile * kTileRows + lane;
+      const bool there = row < p.rows;
+      // the rows' scales and biases, on their way while the unit is multiplied
+      float of_row[2] = {1.0f, 1.0f}, bias[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < (Gated ? 2 : 1); ++h) {
+        if (Fmt == kNvf4 && there) of_row[h] = __ldg(p.row_w + e * p.stride_row + row + h * p.up0);
+        if (p.bias && there) bias[h] = as_f32(p.bias, e * p.stride_bias + row + h * p.up0, p.bf16);
       }
-      if (Down)
+      const bool got = mbar_wait_abortable(&red_full[mine], phase, p.timeout_ns, p.status,
+                                           abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        *abort_flag = 1;
+        break;
+      }
+      // the sum of row `lane` (of row group pair h) for the unit's slot j
+      auto total = [&](int h, int j) {
+        const float* at = all + ((2 * h + (lane >> 4)) * 4 + (j & 1) + 2 * ((lane >> 3) & 1)) * 32 +
+                          (lane & 7) * 4 + (j >> 1);
+        float s[kSlices];
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          if (c >= cols) break;
-#pragma unroll
-          for (int i = 0; i < (Fmt == kFp8 ? 2 : 1); ++i)
-#pragma unroll
-            for (int k = 0; k < (Fmt == kFp8 ? 1 : 2); ++k) {
-              const float4 v =
-                  *reinterpret_cast<const float4*>(hs[c][i] + kb * (Fmt == kFp8 ? 4 : 8) + 4 * k);
-              hv_next[c][i][4 * k] = v.x, hv_next[c][i][4 * k + 1] = v.y;
-              hv_next[c][i][4 * k + 2] = v.z, hv_next[c][i][4 * k + 3] = v.w;
+        for (int k = 0; k < kSlices; ++k) s[k] = at[k * RG * 4 * 32];
+        return kSlices == 4 ? (s[0] + s[1]) + (s[2] + s[kSlices - 1]) : s[0] + s[kSlices - 1];
+      };
+      if (!Down) {
+        const int ks = tile * kTileRows / H::kK, in_stage = tile * kTileRows % H::kK;
+        for (int j = 0; j < n; ++j) {
+          const int pos = first + j;
+          const float fx = r.fx[r.token[pos]];
+          float v = fmaf(total(0, j), of_row[0] * fx, bias[0]);
+          if (Gated) {
+            const float up = fmaf(total(1, j), of_row[1] * fx, bias[1]);
+            v = silu(v) * up;
+          } else {
+            v = gelu2(make_float2(v, v)).x;
+          }
+          if (!there) v = 0.0f;
+          const uint32_t bits = __float_as_uint(v) & 0x7FFFFFFFu;
+          const uint32_t most = __reduce_max_sync(0xffffffffu, bits < 0x7F800000u ? bits : 0u);
+          float inv;
+          const float f = half_factor(__uint_as_float(most), inv);
+          uint8_t* to = p.h + (static_cast<int64_t>(ks) * p.slots + pos) * H::kBytes;
+          reinterpret_cast<uint16_t*>(to)[in_stage + place_of<Fmt>(lane)] =
+              static_cast<uint16_t>(F16::pack(v * f, 0.0f));
+          if (lane == 0) reinterpret_cast<float*>(to + H::kScales)[in_stage / 32] = inv;
+          if (tile == p.tiles - 1)  // zeros to the end of the last stage
+            for (int i = in_stage + 32; i < H::kK; i += 32) {
+              reinterpret_cast<uint16_t*>(to)[i + lane] = 0;
+              if (lane == 0) reinterpret_cast<float*>(to + H::kScales)[i / 32] = 0.0f;
             }
         }
-    };
-    load_scales(slice);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&red_empty[mine]);
+      } else {
+        for (int j = 0; j < n; ++j) {
+          const float v = fmaf(total(0, j), of_row[0], bias[0]);
+          if (there) __stcg(p.part + static_cast<int64_t>(first + j) * p.rows + row, v);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&red_empty[mine]);
+        __threadfence();
+        __syncwarp();
+        // slot j is lane j's to count; a token's last slot to be finished adds
+        // all of them, in order
+        int token = 0;
+        bool last = false;
+        if (lane < n) {
+          token = r.token[first + lane];
+          last = static_cast<int>(atomicAdd(
+                     p.done + static_cast<int64_t>(tile) * p.tokens + token, 1u)) ==
+                 r.valid[token] - 1;
+        }
+        unsigned todo = __ballot_sync(0xffffffffu, last);
+        if (todo) __threadfence();
+        while (todo) {
+          const int tok = __shfl_sync(0xffffffffu, token, __ffs(todo) - 1);
+          todo &= todo - 1;
+          if (!there) continue;
+          float y = 0.0f;
+          for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+            float v[8], w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int s = tok * p.top_k + min(j0 + j, p.top_k - 1);
+              const int at = j0 + j < p.top_k ? r.pos[s] : -1;
+              w[j] = at >= 0 ? r.weight[s] : 0.0f;
+              v[j] = at >= 0 ? __ldcg(p.part + static_cast<int64_t>(at) * p.rows + row) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y = fmaf(w[j], v[j], y);
+          }
+          p.D[tok * p.ldd + row] =
+              static_cast<uint16_t>(p.bf16 ? BF16::pack(y, 0.0f) : F16::pack(y, 0.0f));
+        }
+      }
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------- MMAs
+  const int g = lane >> 2, q = lane & 3;
+  const int group = warp % RG, slice = warp / RG;
+  // ldmatrix: lanes 8 i .. 8 i + 7 give the rows of matrix i, which are (rows 0-7
+  // of the group, a piece), (rows 8-15, that piece), and of the next piece
+  const int mat = lane >> 3, mrow = lane & 7;
+  const uint32_t smem0 = smem_addr(smem);
+  // this warp's weights in a stage: its half (gate or up), block and rows
+  const uint32_t a_base = smem0 +
+      static_cast<uint32_t>(((group >> 1) * kSlices + slice) * S::kBlockW +
+                            ((group & 1) * 16 + mrow + 8 * (mat & 1)) * 128);
+  int stage = 0, buf = 0;
+  uint32_t phase = 0, buf_phase = 0;
+  bool ok = true;
+  // FP8: the scales of the unit's weight blocks that this warp will meet, those
+  // of stage ks in lane ks, for the group's first and last row (a group may
+  // straddle two blocks); loaded a unit ahead.
+  float sw0 = 0.0f, sw1 = 0.0f, sw0_next = 0.0f, sw1_next = 0.0f;
+  const int group_row = (Gated && group >= 2 ? p.up0 - 32 : 0) + group * 16;
+  const int group_end = p.rows - 1 + (Gated && group >= 2 ? p.up0 : 0);
+  auto load_sw = [&](const UnitWalk& w, int ks0) {
+    if (Fmt != kFp8 || w.tile >= p.tiles) return;
+    const int row = group_row + w.tile * kTileRows;
+    const int kb = min((ks0 + lane) * kSlices + slice, p.k_blocks - 1);
+    const float* sw = p.sw + r.expert[w.u] * p.stride_sw + kb;
+    sw0_next = __ldg(sw + static_cast<int64_t>(min(row, group_end) >> 7) * p.lds_w);
+    sw1_next = __ldg(sw + static_cast<int64_t>(min(row + 15, group_end) >> 7) * p.lds_w);
+  };
+  walk.start(blockIdx.x, step, chunks);
+  if (units > 0) load_sw(walk, 0);
+  while (walk.tile < p.tiles && units > 0) {
+    const int tile = walk.tile, n = r.n[walk.u], first = r.first[walk.u];
+    // this lane's column of the activations, and its two columns of the sums
+    // (past the last: the last)
+    const int col = min(g, n - 1);
+    const uint32_t b_base =
+        Down ? smem0 + static_cast<uint32_t>(S::kW + S::kS + col * H::kBytes + slice * S::kBlockK * 2 +
+                                             q * 16)
+             : smem_addr(xs) + static_cast<uint32_t>(r.token[first + col] * p.x_pitch + q * 16);
+    const uint32_t h_base = smem0 + static_cast<uint32_t>(S::kW + S::kS + H::kScales +
+                                                          slice * (S::kBlockK / 32) * 4);
+    const uint32_t h0 = h_base + static_cast<uint32_t>(min(2 * q, n - 1) * H::kBytes);
+    const uint32_t h1 = h_base + static_cast<uint32_t>(min(2 * q + 1, n - 1) * H::kBytes);
+    sw0 = sw0_next, sw1 = sw1_next;
+    walk.next();
+    load_sw(walk, 0);
+    const int row_g = group_row + tile * kTileRows;
+    const bool second_a = Fmt == kFp8 && (row_g + g) >> 7 != row_g >> 7;
+    const bool second_b = Fmt == kFp8 && (row_g + g + 8) >> 7 != row_g >> 7;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int ks = 0; ks < k_stages; ++ks) {
-      sa = sa_next, sb = sb_next;
-      if (Down)
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < (Fmt == kFp8 ? 4 : 8); ++k) hv[c][i][k] = hv_next[c][i][k];
+      if (Fmt == kFp8 && ks > 0 && (ks & 31) == 0) {  // beyond the 32 that lanes hold
+        const float keep0 = sw0_next, keep1 = sw1_next;
+        UnitWalk now = walk;
+        now.tile = tile;
+        now.u = walk.u - walk.d_u;
+        if (now.u < 0) now.u += walk.chunks;
+        load_sw(now, ks);
+        sw0 = sw0_next, sw1 = sw1_next, sw0_next = keep0, sw1_next = keep1;
+      }
       const int kb = ks * kSlices + slice;
-      load_scales(kb + kSlices);
       if (ok) {
         ok = __all_sync(0xffffffffu, mbar_wait_abortable(&full_bar[stage], phase, p.timeout_ns,
                                                          p.status, abort_flag));
         if (!ok) *abort_flag = 1;
       }
+      float sa = 1.0f, sb = 1.0f;
+      if (Fmt == kFp8) {
+        const float s0 = __shfl_sync(0xffffffffu, sw0, ks & 31);
+        const float s1 = __shfl_sync(0xffffffffu, sw1, ks & 31);
+        sa = second_a ? s1 : s0;
+        sb = second_b ? s1 : s0;
+      }
       if (ok && kb < p.k_blocks) {
-        const uint32_t block = smem0 + static_cast<uint32_t>(stage * stage_bytes + slice * p.block_bytes);
-        const uint32_t acts = block + kBlockW + kBlockS;
+        const uint32_t at = static_cast<uint32_t>(stage * p.stage_bytes);
+        const uint32_t b_at = Down ? b_base + at : b_base + static_cast<uint32_t>(kb * S::kBlockK * 2);
+        uint32_t w[4][4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          ldmatrix4(w[m], a_base + at + (((2 * m + (mat >> 1)) ^ mrow) << 4));
         if (Fmt == kFp8) {
-          float c4[NT][4];
-          uint32_t b[NT][4];
+          uint4 b[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) b[m] = ld_shared4(b_at + m * 64);
+          float c[Down ? 4 : 2][4];
+#pragma unroll
+          for (int m = 0; m < (Down ? 4 : 2); ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[m][i] = 0.0f;
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            uint32_t a[4];
-            ldmatrix4(a, block + a_base + (((2 * m + (mat >> 1)) ^ a_swz) << 4));
+            uint32_t a[8];
 #pragma unroll
-            for (int c = 0; c < NT; ++c) {
-              if (c >= cols) break;
-              if (m % 2 == 0) {
-                // pieces 2 m .. 2 m + 3: two MMAs' worth
-                const uint32_t piece = static_cast<uint32_t>(2 * m + mat);
-                ldmatrix4(b[c], Down ? acts + b_base[c] + ((piece ^ ((b_base[c] >> 7) & 7)) << 4)
-                                     : b_base[c] + static_cast<uint32_t>(kb * 128) + (piece << 4));
-              }
-              if (Down || m == 0)
+            for (int i = 0; i < 4; ++i) e4m3x4_to_f16(w[m][i], a[2 * i], a[2 * i + 1]);
+            float(&d)[4] = c[Down ? m : m & 1];
+            mma_f16(d, a[0], a[2], a[1], a[3], b[m].x, b[m].y);
+            mma_f16(d, a[4], a[6], a[5], a[7], b[m].z, b[m].w);
+          }
+          if (Down) {
+            const uint4 u0 = ld_shared4(h0 + at), u1 = ld_shared4(h1 + at);
+            const uint32_t v0[4] = {u0.x, u0.y, u0.z, u0.w}, v1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) c4[c][i] = 0.0f;
-              mma_e4m3(c4[c], a[0], a[1], a[2], a[3], b[c][2 * (m & 1)], b[c][2 * (m & 1) + 1]);
-              if (Down) {
+            for (int i = 0; i < 4; ++i) {
+              float v = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  acc[c][i] = fmaf(c4[c][i], (i < 2 ? sa : sb) * hv[c][i & 1][m], acc[c][i]);
-              } else if (m == 3) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[c][i] = fmaf(c4[c][i], i < 2 ? sa : sb, acc[c][i]);
-              }
+              for (int m = 0; m < 4; ++m)
+                v = fmaf(c[Down ? m : 0][i], __uint_as_float(i & 1 ? v1[m] : v0[m]), v);
+              acc[i] = fmaf(v, i < 2 ? sa : sb, acc[i]);
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[i] = fmaf(c[0][i] + c[1][i], i < 2 ? sa : sb, acc[i]);
           }
         } else {
-          // this lane's scale words: rows g and g + 8 of the group, four blocks each
-          const int line = (group & 1) * 16 + g;
-          const uint32_t sf = block + kBlockW + (group >> 1) * 2048 +
-                              static_cast<uint32_t>(line * 16 + (tile & 3) * 4);
+          // this lane's scale words: rows g and g + 8 of the group, four blocks each,
+          // of which its codes lie in blocks q / 2 and 2 + q / 2
+          const uint32_t sf = smem0 + at +
+              static_cast<uint32_t>(S::kW + ((group >> 1) * kSlices + slice) * 2048 +
+                                    ((group & 1) * 16 + g) * 16 + (tile & 3) * 4);
+          float c[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
           for (int mm = 0; mm < 4; ++mm) {
-            if (4 * kb + mm >= p.k_tiles) break;  // (a scale tile past the last is another's)
-            uint32_t w[4], sg, sh;
-            ldmatrix4(w, block + a_base + (((2 * mm + (mat >> 1)) ^ a_swz) << 4));
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sg) : "r"(sf + mm * 512));
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sh) : "r"(sf + mm * 512 + 128));
+            // (a scale tile past the last is another's: its codes are zeros, NaNs not)
+            const bool in = 4 * kb + mm < p.k_tiles;
+            uint32_t sg[2], sh[2];
+            scale_pairs(in ? ld_shared1(sf + mm * 512) : 0u, q >> 1, sg);
+            scale_pairs(in ? ld_shared1(sf + mm * 512 + 128) : 0u, q >> 1, sh);
+            uint32_t hv0[2], hv1[2];
+            if (Down) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float2 s0 = e4m3x2_values((sg >> (16 * half)) & 0xFFFFu);
-              const float2 s1 = e4m3x2_values((sh >> (16 * half)) & 0xFFFFu);
-              const uint32_t a0 = e4m3_of_low(w[2 * half]), a2 = e4m3_of_high(w[2 * half]);
-              const uint32_t a1 = e4m3_of_low(w[2 * half + 1]), a3 = e4m3_of_high(w[2 * half + 1]);
-#pragma unroll
-              for (int c = 0; c < NT; ++c) {
-                if (c >= cols) break;
-                uint32_t b[2];
-                // 32 values of a part: pieces 4 mm + 2 half (even ones) and the next (odd)
-                const uint32_t piece = static_cast<uint32_t>(4 * mm + 2 * half + (mat & 1));
-                const uint32_t at =
-                    Down ? acts + b_base[c] + (piece >> 3) * 1024 +
-                               (((piece & 7) ^ ((b_base[c] >> 7) & 7)) << 4)
-                         : b_base[c] + static_cast<uint32_t>(kb * 256) + (piece << 4);
-                asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];"
-                             : "=r"(b[0]), "=r"(b[1])
-                             : "r"(at)
-                             : "memory");
-                float c4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_e4m3(c4, a0, a1, a2, a3, b[0] & b_mask, b[1] & b_mask);
-                const float t0 = fmaf(c4[1], s0.y, c4[0] * s0.x);
-                const float t1 = fmaf(c4[3], s1.y, c4[2] * s1.x);
-                if (Down) {
-                  acc[c][0] = fmaf(t0, hv[c][0][2 * mm + half], acc[c][0]);
-                  acc[c][1] = fmaf(t1, hv[c][0][2 * mm + half], acc[c][1]);
-                } else {
-                  acc[c][0] += t0;
-                  acc[c][1] += t1;
-                }
+              for (int i = 0; i < 2; ++i) {
+                hv0[i] = ld_shared1(h0 + at + (2 * mm + i) * 4);
+                hv1[i] = ld_shared1(h1 + at + (2 * mm + i) * 4);
               }
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 b = ld_shared4(b_at + (2 * mm + i) * 64);
+              uint32_t x[4], y[4];
+              e2m1x8_to_f16x2x4(w[mm][2 * i], x);
+              e2m1x8_to_f16x2x4(w[mm][2 * i + 1], y);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] = mul_half2(x[k], sg[i]), y[k] = mul_half2(y[k], sh[i]);
+              if (Down)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) c[i][k] = 0.0f;
+              mma_f16(c[i], x[0], y[0], x[1], y[1], b.x, b.y);
+              mma_f16(c[i], x[2], y[2], x[3], y[3], b.z, b.w);
+            }
+            if (Down) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                acc[k] = fmaf(c[1][k], __uint_as_float(k & 1 ? hv1[1] : hv0[1]),
+                              fmaf(c[0][k], __uint_as_float(k & 1 ? hv1[0] : hv0[0]), acc[k]));
+            }
           }
+          if (!Down)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[k] += c[0][k] + c[1][k];
         }
       }
       __syncwarp();
@@ -616,92 +821,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1;
       }
     }
-    // The slices' sums meet in shared memory.  Two buffers: every warp has read
-    // one when it comes to the barrier of the next unit, which the others pass
-    // before they write it again.  (A warp that gave up still comes there.)
-    float* mine = red + (turn * kMmaWarps + warp) * NT * kAcc * 32 + lane;
-    const float* all = red + turn * kMmaWarps * NT * kAcc * 32;
-    turn ^= 1;
+    // the slices' sums go to the unit's epilogue warp
+    if (ok) {
+      ok = __all_sync(0xffffffffu, mbar_wait_abortable(&red_empty[buf], buf_phase ^ 1, p.timeout_ns,
+                                                       p.status, abort_flag));
+      if (!ok) *abort_flag = 1;
+    }
+    if (!ok) break;
+    float* mine = red + (buf * kMmaWarps + warp) * 4 * 32 + lane;
 #pragma unroll
-    for (int i = 0; i < NT * kAcc; ++i)
-      if (i / kAcc < cols) mine[i * 32] = acc[i / kAcc][i % kAcc];
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (!ok || warp >= n) continue;
-    // warp: slot of the unit; lane: row of the tile
-    auto total = [&](int rows_group) {
-      float v = 0.0f;
-#pragma unroll
-      for (int i = 2; i >= 0; --i) {
-        const int part = 3 * warp + i;
-        const int c = part / kPerTile, in = part % kPerTile;
-        // the lane and register that hold row `lane` of the tile
-        const int who = Fmt == kFp8 ? (lane & 7) * 4 + in / 2 : (lane & 7) * 4 + in;
-        const int reg = Fmt == kFp8 ? (in & 1) + 2 * ((lane >> 3) & 1) : (lane >> 3) & 1;
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kSlices; ++k)
-          s += all[((k * RG + rows_group + (lane >> 4)) * NT * kAcc + c * kAcc + reg) * 32 + who];
-        v = fmaf(v, 0.0625f, s);
-      }
-      return v;
-    };
-    const int row = tile * kTileRows + lane;
-    const int pos = first + warp, slot = r.slot[pos], token = slot / p.top_k;
-    const bool there = row < p.rows;
-    // what the code's bits stand for beside their E4M3 value, and the row's scale
-    auto scaled = [&](float v, int of_row) {
-      if (Fmt == kNvf4) v *= 64.0f * (there ? __ldg(p.row_w + e * p.stride_row + of_row) : 0.0f);
-      if (!Down) v *= r.fx[token];
-      if (p.bias && there) v += as_f32(p.bias, e * p.stride_bias + of_row, p.bf16);
-      return v;
-    };
-    if (!Down) {
-      float v = scaled(total(0), row);
-      if (Gated) {
-        const float up = scaled(total(2), row + p.up0);
-        v = silu(v) * up;
-      } else {
-        v = gelu2(make_float2(v, v)).x;
-      }
-      if (!there) v = 0.0f;
-      const uint32_t bits = __float_as_uint(v) & 0x7FFFFFFFu;
-      const uint32_t most = __reduce_max_sync(0xffffffffu, bits);
-      const bool odd = most >= 0x7F800000u;
-      float inv;
-      const float f = parts_factor(__uint_as_float(odd ? 0u : most), inv);
-      float x[4] = {odd ? 0.0f : v * f, 0.0f, 0.0f, 0.0f};
-      uint32_t code[3];
-      split4(x, code);
-      const int at = Fmt == kFp8 ? lane : (lane & 1) * 16 + (lane >> 1);
-      uint8_t* h = p.h + static_cast<int64_t>(3 * pos) * p.ldh + tile * kTileRows + at;
-#pragma unroll
-      for (int i = 0; i < 3; ++i) h[i * p.ldh] = static_cast<uint8_t>(code[i]);
-      // (the last tile also fills what the second product reads past it)
-      const int more = tile == p.tiles - 1 ? p.hs_ld - tile : 1;
-      if (lane < more)
-        p.hs[static_cast<int64_t>(pos) * p.hs_ld + tile + lane] =
-            lane == 0 ? (odd ? CUDART_NAN_F : inv) : 0.0f;
-    } else {
-      float v = scaled(total(0), row);
-      if (there) __stcg(p.part + static_cast<int64_t>(pos) * p.rows + row, v);
-      __threadfence();
-      __syncwarp();
-      unsigned before = 0;
-      if (lane == 0) before = atomicAdd(p.done + static_cast<int64_t>(tile) * p.tokens + token, 1u);
-      before = __shfl_sync(0xffffffffu, before, 0);
-      if (static_cast<int>(before) != r.valid[token] - 1) continue;
-      // the token's last slot: its slots in order
-      __threadfence();
-      if (!there) continue;
-      float y = 0.0f;
-      for (int j = 0; j < p.top_k; ++j) {
-        const int at = r.pos[token * p.top_k + j];
-        if (at < 0) continue;
-        const float w = p.weights ? __ldg(p.weights + token * p.top_k + j) : 1.0f;
-        y = fmaf(w, __ldcg(p.part + static_cast<int64_t>(at) * p.rows + row), y);
-      }
-      p.D[token * p.ldd + row] =
-          static_cast<uint16_t>(p.bf16 ? BF16::pack(y, 0.0f) : F16::pack(y, 0.0f));
+    for (int i = 0; i < 4; ++i) mine[i * 32] = acc[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&red_full[buf]);
+    if (++buf == kEpiWarps) {
+      buf = 0;
+      buf_phase ^= 1;
     }
   }
 }
@@ -710,35 +844,51 @@ constexpr int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
 // Where the scratch's parts lie.
 struct LayerScratch {
-  int64_t ldh, hs_ld, h, hs, part, done, bytes;
+  int64_t h, part, done, bytes;
 };
 LayerScratch scratch_of(const MoeLayerArgs& a) {
   LayerScratch s;
   const int64_t slots = a.tokens * a.top_k;
-  s.ldh = round_up(a.hidden, 256);
-  s.hs_ld = s.ldh / 32;
+  // (either format's: the caller names none)
+  const int64_t h8 = (a.hidden + HRow<kFp8>::kK - 1) / HRow<kFp8>::kK * HRow<kFp8>::kBytes;
+  const int64_t h4 = (a.hidden + HRow<kNvf4>::kK - 1) / HRow<kNvf4>::kK * HRow<kNvf4>::kBytes;
   s.h = 0;
-  s.hs = s.h + 3 * slots * s.ldh;
-  s.part = s.hs + slots * s.hs_ld * 4;
+  s.part = round_up(slots * std::max(h8, h4), 16);
   s.done = s.part + round_up(slots * a.out * 4, 16);
   s.bytes = s.done + round_up((a.out + kTileRows - 1) / kTileRows * a.tokens * 4, 16);
   return s;
 }
 
-// Shared memory besides the ring, and the ring's stages in `room` bytes.
-template <int NT, int kAcc>
-int red_bytes() {
-  return 2 * kMmaWarps * NT * kAcc * 32 * 4;
+// Bytes of a token in shared memory: rows are 64 bytes apart in their banks.
+int64_t token_bytes(const MoeLayerArgs& a) {
+  return round_up(a.width, 256) * 2 + 64;
 }
 
-template <int Fmt, bool Down, bool Gated, int NT>
+cudaError_t weights_map(CUtensorMap* map, const MoeWeights& w, int64_t rows, int64_t blocks,
+                        int box_blocks) {
+  tc::EncodeTiledFn fn = tc::encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(w.ld), 128};
+  const cuuint32_t box[3] = {128, kTileRows, static_cast<cuuint32_t>(box_blocks)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w.codes), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int Fmt, bool Down, bool Gated>
 cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
-  constexpr int RG = Gated ? 4 : 2, kSlices = kMmaWarps / RG, kAcc = Fmt == kFp8 ? 4 : 2;
+  using S = Shape<Fmt, Down, Gated>;
+  static_assert(S::kBars <= 256, "barriers");
   constexpr int kMaxSmem = 227 * 1024;
   const MoeWeights& w = Down ? a.down : a.up;
   const int64_t n_rows = Down ? a.out : a.hidden * (Gated ? 2 : 1);
   const int64_t bytes_k = Fmt == kFp8 ? p.K : (p.K + 1) / 2;
   p.k_blocks = static_cast<int>((bytes_k + 127) / 128);
+  p.full_blocks = static_cast<int>(bytes_k / 128);
   p.k_tiles = static_cast<int>((p.K + 63) / 64);
   p.tiles = (p.rows + kTileRows - 1) / kTileRows;
   const int64_t pitch = a.count > 1 ? w.stride / w.ld : n_rows;
@@ -751,44 +901,39 @@ cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   p.stride_row = n_rows;
   p.bias = w.bias;
   p.stride_bias = w.stride_bias;
-  p.act_boxes = Down ? (3 * p.chunk + 7) / 8 : 0;
-  p.block_bytes = 16 * RG * 128 + (Fmt == kNvf4 ? RG / 2 * 2048 : 0) +
-                  p.act_boxes * (Fmt == kNvf4 ? 2 : 1) * 1024;
-  const int stage = kSlices * p.block_bytes;
-  const int red = red_bytes<NT, kAcc>();
+  const int stage = static_cast<int>(
+      round_up(S::kW + S::kS + (Down ? p.chunk * HRow<Fmt>::kBytes : 0), 1024));
+  p.stage_bytes = stage;
   const int route = route_bytes(p.slots, p.tokens, p.count);
-  const int fixed = static_cast<int>(round_up(x_bytes, 16)) + red + 256 + route + 1024;
-  // Two CTAs' worth of ring where the rest leaves room: the second kernel's
-  // starts to fill while the first one's ends.
-  int room = 112 * 1024 - fixed;
-  if (room < 4 * stage) room = kMaxSmem - fixed;
-  p.stages = std::min(8, room / stage);
+  const int fixed = static_cast<int>(round_up(x_bytes, 16)) + S::kRed + 256 + route + 1024;
+  // Half an SM's shared memory where that holds enough of a ring: the second
+  // kernel's then starts to fill while the first one ends.
+  int room = 113 * 1024 - fixed;
+  if (room < 3 * stage) room = kMaxSmem - fixed;
+  p.stages = std::min(kMaxStages, room / stage);
   if (p.stages < 2) return cudaErrorInvalidValue;
   p.off_x = p.stages * stage;
   p.off_red = p.off_x + static_cast<int>(round_up(x_bytes, 16));
-  p.off_route = p.off_red + red + 256;
+  p.off_route = p.off_red + S::kRed + 256;
   const int smem = p.off_route + route + 1024;
 
-  CUtensorMap tw{}, ts{}, th{};
-  cudaError_t e = tc::encode_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes,
-                                    (a.count - 1) * pitch + n_rows, bytes_k, w.ld, kTileRows, 128,
-                                    CU_TENSOR_MAP_SWIZZLE_128B);
+  CUtensorMap tw{}, tt{}, ts{};
+  const int64_t all_rows = (a.count - 1) * pitch + n_rows;
+  cudaError_t e = tc::encode_map_2d(&tt, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, all_rows, bytes_k,
+                                    w.ld, kTileRows, 128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  ts = th = tw;  // not used by every variant
+  tw = ts = tt;  // not used without whole blocks, or by FP8
+  if (p.full_blocks > 0) {
+    e = weights_map(&tw, w, all_rows, p.full_blocks, S::kSlices);
+    if (e != cudaSuccess) return e;
+  }
   if (Fmt == kNvf4) {
     e = tc::encode_map_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT32, w.scales,
-                          static_cast<int64_t>(p.sf_rows) * p.k_tiles * a.count, 128, 512, 4, 128,
-                          CU_TENSOR_MAP_SWIZZLE_NONE);
+                          static_cast<int64_t>(p.sf_rows) * p.k_tiles * a.count, 128, 512,
+                          4 * S::kSlices, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
   }
-  if (Down) {
-    // what the first kernel writes: whole tiles of 32 values
-    e = tc::encode_map_2d(&th, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.h, 3 * a.tokens * a.top_k,
-                          round_up(a.hidden, kTileRows), p.ldh, 8, 128,
-                          CU_TENSOR_MAP_SWIZZLE_128B);
-    if (e != cudaSuccess) return e;
-  }
-  auto kern = moe_layer_kernel<Fmt, Down, Gated, NT>;
+  auto kern = moe_layer_kernel<Fmt, Down, Gated>;
   int dev = 0;
   cudaGetDevice(&dev);
   static std::atomic<uint64_t> attr_set{0};
@@ -796,42 +941,37 @@ cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   });
   if (e != cudaSuccess) return e;
-  const int64_t most = std::min<int64_t>(p.slots, int64_t(1) << 20) * p.tiles;
+  const int64_t most = static_cast<int64_t>(p.slots) * p.tiles;
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(most, a.sm_count));
   e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                       static_cast<size_t>(smem), a.stream, tw, ts, th, p);
+                       static_cast<size_t>(smem), a.stream, tw, tt, ts, p);
   count_launches(1);
   return e;
 }
 
-template <int Fmt, int NT>
+template <int Fmt>
 cudaError_t run_layer(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   p.K = static_cast<int>(a.width);
   p.rows = static_cast<int>(a.hidden);
   p.up0 = static_cast<int>(a.hidden);
-  const cudaError_t e = a.gated ? run_phase<Fmt, false, true, NT>(a, p, x_bytes)
-                                : run_phase<Fmt, false, false, NT>(a, p, x_bytes);
+  const cudaError_t e = a.gated ? run_phase<Fmt, false, true>(a, p, x_bytes)
+                                : run_phase<Fmt, false, false>(a, p, x_bytes);
   if (e != cudaSuccess) return e;
   p.K = static_cast<int>(a.hidden);
   p.rows = static_cast<int>(a.out);
-  return run_phase<Fmt, true, false, NT>(a, p, 0);
+  return run_phase<Fmt, true, false>(a, p, 0);
 }
 
 }  // namespace
 
 int64_t moe_layer_scratch(const MoeLayerArgs& a) { return scratch_of(a).bytes; }
 
-// Bytes of the tokens' parts in shared memory: rows of whole 256-value blocks,
-// 16 bytes apart in their banks.
-static int64_t parts_bytes(int64_t tokens, int64_t width) {
-  return 3 * tokens * (round_up(width, 256) + 16);
-}
 // What is left of a CTA's shared memory beside a ring of two stages, its sums
-// and the routing.
+// and the barriers.
 bool moe_layer_fits(const MoeLayerArgs& a) {
   const int64_t slots = a.tokens * a.top_k;
   return slots <= kMaxLayerSlots &&
-         parts_bytes(a.tokens, a.width) + route_bytes(slots, a.tokens, a.count) <= 146 * 1024;
+         a.tokens * token_bytes(a) + route_bytes(slots, a.tokens, a.count) <= 160 * 1024;
 }
 
 cudaError_t launch_moe_layer(const MoeLayerArgs& a) {
@@ -843,14 +983,14 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a) {
   p.top_k = static_cast<int>(a.top_k);
   p.slots = static_cast<int>(a.tokens * a.top_k);
   p.count = static_cast<int>(a.count);
+  // Slots per unit: as many as there are tokens can meet in one expert (a token
+  // that names an expert twice gets a unit more), at most an MMA's columns.
+  p.chunk = static_cast<int>(std::min<int64_t>(a.tokens, kMaxChunk));
   p.bf16 = a.bf16;
   p.X = static_cast<const uint16_t*>(a.X);
   p.ldx = a.ldx;
-  p.x_pitch = static_cast<int>(round_up(a.width, 256)) + 16;
+  p.x_pitch = static_cast<int>(token_bytes(a));
   p.h = base + s.h;
-  p.ldh = s.ldh;
-  p.hs = reinterpret_cast<float*>(base + s.hs);
-  p.hs_ld = static_cast<int>(s.hs_ld);
   p.part = reinterpret_cast<float*>(base + s.part);
   p.done = reinterpret_cast<unsigned*>(base + s.done);
   p.done_words = static_cast<int>((a.out + kTileRows - 1) / kTileRows * a.tokens);
@@ -859,13 +999,8 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a) {
   p.ldd = a.ldd;
   p.status = a.status;
   p.timeout_ns = a.timeout_ns;
-  const int x_bytes = static_cast<int>(parts_bytes(a.tokens, a.width));
-  // Slots per unit: as many as there are tokens can meet in one expert (a token
-  // that names an expert twice gets a unit more), at most 8.
-  const bool few = a.tokens <= 2;
-  p.chunk = few ? 2 : kMaxChunk;
-  if (a.nvf4) return few ? run_layer<kNvf4, 2>(a, p, x_bytes) : run_layer<kNvf4, 6>(a, p, x_bytes);
-  return few ? run_layer<kFp8, 1>(a, p, x_bytes) : run_layer<kFp8, 3>(a, p, x_bytes);
+  const int x_bytes = static_cast<int>(a.tokens * token_bytes(a));
+  return a.nvf4 ? run_layer<kNvf4>(a, p, x_bytes) : run_layer<kFp8>(a, p, x_bytes);
 }
 
 }  // namespace dg

@@ -143,6 +143,18 @@ __device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint64_t* ba
       : "memory");
 }
 
+// The same from a 3-D tensor, at coordinates (x = inner, y, z).
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst,
+                                            int32_t x, int32_t y, int32_t z,
+                                            uint64_t cache_policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z),
+      "l"(cache_policy)
+      : "memory");
+}
+
 // 2-D tiled store of a shared-memory box to global memory at (x, y); the
 // tensor map clips what falls outside the tensor.  Tracked per thread in
 // bulk async-groups (bulk_commit_group / bulk_wait_group*).
