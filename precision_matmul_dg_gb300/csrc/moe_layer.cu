@@ -45,9 +45,9 @@ namespace {
 
 using namespace fp8;
 
-constexpr int kMmaWarps = 8, kTmaWarp = 8, kEpiWarp = 9, kEpiWarps = 3;
-constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;
-constexpr int kOtherThreads = kThreads - kMmaWarps * 32;  // they build the routing
+constexpr int kTeamWarps = 8;  // that share a stage
+constexpr int kEpiWarps = 3;
+constexpr int kOtherThreads = (1 + kEpiWarps) * 32;  // they build the routing
 constexpr int kTileRows = 32;  // weight rows per unit (twice as many where gated)
 constexpr int kMaxChunk = 8;   // slots per unit
 constexpr int kMaxStages = 8;
@@ -57,10 +57,19 @@ enum : int { kFp8 = 0, kNvf4 = 1 };
 // What differs between the kernels: row groups of 16, the warps that share a
 // group's K blocks (the blocks of a stage), values in a K block (128 bytes of each
 // weight row), bytes of a stage's weights and of their scales.
-template <int Fmt, bool Down, bool Gated>
+//
+// A team of 8 warps takes whole stages.  What hides a stage's latencies (a chain
+// of loads, conversions and MMAs of 600 to 1200 clocks, where HBM brings a stage
+// in 700 to 780) is a second team: two CTAs of one on an SM, where half its shared
+// memory holds a ring, or two in a CTA, which take turns (8 tokens gated FP8: 82
+// us, with one team 117).
+template <int Fmt, bool Down, bool Gated, int Teams = 1>
 struct Shape {
+  static constexpr int kMmaWarps = Teams * kTeamWarps;
+  static constexpr int kTmaWarp = kMmaWarps, kEpiWarp = kMmaWarps + 1;
+  static constexpr int kThreads = kMmaWarps * 32 + kOtherThreads;
   static constexpr int RG = Gated ? 4 : 2;
-  static constexpr int kSlices = kMmaWarps / RG;
+  static constexpr int kSlices = kTeamWarps / RG;
   static constexpr int kBlockK = Fmt == kFp8 ? 128 : 256;
   static constexpr int kBlockW = kTileRows * 128;
   static constexpr int kW = (Gated ? 2 : 1) * kSlices * kBlockW;
@@ -150,7 +159,7 @@ __device__ __forceinline__ void others_sync() {
   asm volatile("bar.sync 2, %0;" ::"n"(kOtherThreads) : "memory");
 }
 
-// By the kOtherThreads threads that do not multiply, numbered i.
+// By the threads that do not multiply, numbered i.
 __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p, int i) {
   for (int e = i; e < p.count; e += kOtherThreads) r.cnt[e] = 0;
   for (int t = i; t < p.tokens; t += kOtherThreads) r.valid[t] = 0;
@@ -274,25 +283,25 @@ __device__ __forceinline__ uint32_t scaled_half2(uint32_t w, float f) {
 // The tokens in shared memory as FP16, by the MMA warps: FP16 as it is, BF16
 // times a power of two per token that brings its largest finite value near the
 // top (infinities and NaNs stay what they are).
-template <int Fmt>
+template <int Fmt, int kThreads>
 __device__ __forceinline__ void load_tokens(const LayerParams& p, uint8_t* xs, const Route& r) {
   constexpr int kAhead = 4;
   const int per_row = p.k_blocks * Shape<Fmt, false, false>::kBlockK / 8;  // pieces, a multiple of 16
   const int pieces = p.tokens * per_row;
   if (p.bf16) {
-    for (int t = threadIdx.x; t < p.tokens; t += kMmaWarps * 32) r.amax[t] = 0u;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    for (int i0 = threadIdx.x; i0 < pieces; i0 += kAhead * kMmaWarps * 32) {
+    for (int t = threadIdx.x; t < p.tokens; t += kThreads) r.amax[t] = 0u;
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += kAhead * kThreads) {
       uint4 v[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j * kMmaWarps * 32, t = i / per_row;
+        const int i = i0 + j * kThreads, t = i / per_row;
         v[j] = i < pieces ? load8(p.X + t * p.ldx, (i - t * per_row) * 8, p.K)
                           : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j * kMmaWarps * 32;
+        const int i = i0 + j * kThreads;
         uint32_t m = max(max(finite_max(v[j].x), finite_max(v[j].y)),
                          max(finite_max(v[j].z), finite_max(v[j].w)));
         // (16 lanes share a token at least)
@@ -301,18 +310,18 @@ __device__ __forceinline__ void load_tokens(const LayerParams& p, uint8_t* xs, c
         if ((threadIdx.x & 15) == 0 && i < pieces) atomicMax(&r.amax[i / per_row], m);
       }
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
   }
-  for (int i0 = threadIdx.x; i0 < pieces; i0 += kAhead * kMmaWarps * 32) {
+  for (int i0 = threadIdx.x; i0 < pieces; i0 += kAhead * kThreads) {
     uint4 v[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j * kMmaWarps * 32, t = i / per_row;
+      const int i = i0 + j * kThreads, t = i / per_row;
       if (i < pieces) v[j] = load8(p.X + t * p.ldx, (i - t * per_row) * 8, p.K);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j * kMmaWarps * 32, t = i / per_row, k = (i - t * per_row) * 8;
+      const int i = i0 + j * kThreads, t = i / per_row, k = (i - t * per_row) * 8;
       if (i >= pieces) break;
       float inv = 1.0f;
       if (p.bf16) {
@@ -395,16 +404,17 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 // Down: the second product (its activations come with the ring's stages).
-template <int Fmt, bool Down, bool Gated>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int Fmt, bool Down, bool Gated, int Teams>
+__global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Teams == 1 ? 2 : 1)
     moe_layer_kernel(const __grid_constant__ CUtensorMap tmap_w,
                      const __grid_constant__ CUtensorMap tmap_tail,
                      const __grid_constant__ CUtensorMap tmap_sf,
                      const __grid_constant__ LayerParams p) {
   static_assert(!(Down && Gated), "the second product has no gate");
-  using S = Shape<Fmt, Down, Gated>;
+  using S = Shape<Fmt, Down, Gated, Teams>;
   using H = HRow<Fmt>;
-  constexpr int RG = S::RG, kSlices = S::kSlices;
+  constexpr int RG = S::RG, kSlices = S::kSlices, kMmaWarps = S::kMmaWarps;
+  constexpr int kTmaWarp = S::kTmaWarp, kEpiWarp = S::kEpiWarp;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -421,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], kMmaWarps);
+      mbar_init(&empty_bar[s], kTeamWarps);
     }
     for (int b = 0; b < kEpiWarps; ++b) {
       mbar_init(&red_full[b], kMmaWarps);
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp >= kMmaWarps)
     build_route(r, p, static_cast<int>(threadIdx.x) - kMmaWarps * 32);
   else if (!Down)
-    load_tokens<Fmt>(p, xs, r);
+    load_tokens<Fmt, kMmaWarps * 32>(p, xs, r);
   __syncthreads();
   const int chunks = *r.chunks;
   const int units = chunks * p.tiles;
@@ -572,10 +582,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       auto total = [&](int h, int j) {
         const float* at = all + ((2 * h + (lane >> 4)) * 4 + (j & 1) + 2 * ((lane >> 3) & 1)) * 32 +
                           (lane & 7) * 4 + (j >> 1);
-        float s[kSlices];
+        float s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kSlices; ++k) s[k] = at[k * RG * 4 * 32];
-        return kSlices == 4 ? (s[0] + s[1]) + (s[2] + s[kSlices - 1]) : s[0] + s[kSlices - 1];
+        for (int k = 0; k < Teams * kSlices; ++k) s += at[k * RG * 4 * 32];
+        return s;
       };
       if (!Down) {
         const int ks = tile * kTileRows / H::kK, in_stage = tile * kTileRows % H::kK;
@@ -654,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // ------------------------------------------------------------------- MMAs
   const int g = lane >> 2, q = lane & 3;
-  const int group = warp % RG, slice = warp / RG;
+  const int group = warp % RG, slice = warp % kTeamWarps / RG, team = warp / kTeamWarps;
   // ldmatrix: lanes 8 i .. 8 i + 7 give the rows of matrix i, which are (rows 0-7
   // of the group, a piece), (rows 8-15, that piece), and of the next piece
   const int mat = lane >> 3, mrow = lane & 7;
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t a_base = smem0 +
       static_cast<uint32_t>(((group >> 1) * kSlices + slice) * S::kBlockW +
                             ((group & 1) * 16 + mrow + 8 * (mat & 1)) * 128);
-  int stage = 0, buf = 0;
+  int stage = 0, buf = 0, turn = 0;  // turn: the team whose stage it is
   uint32_t phase = 0, buf_phase = 0;
   bool ok = true;
   // FP8: the scales of the unit's weight blocks that this warp will meet, those
@@ -713,7 +723,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         sw0 = sw0_next, sw1 = sw1_next, sw0_next = keep0, sw1_next = keep1;
       }
       const int kb = ks * kSlices + slice;
-      if (ok) {
+      const bool ours = Teams == 1 || turn == team;
+      if (Teams > 1) turn ^= 1;
+      if (ok && ours) {
         ok = __all_sync(0xffffffffu, mbar_wait_abortable(&full_bar[stage], phase, p.timeout_ns,
                                                          p.status, abort_flag));
         if (!ok) *abort_flag = 1;
@@ -725,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         sa = second_a ? s1 : s0;
         sb = second_b ? s1 : s0;
       }
-      if (ok && kb < p.k_blocks) {
+      if (ok && ours && kb < p.k_blocks) {
         const uint32_t at = static_cast<uint32_t>(stage * p.stage_bytes);
         const uint32_t b_at = Down ? b_base + at : b_base + static_cast<uint32_t>(kb * S::kBlockK * 2);
         uint32_t w[4][4];
@@ -815,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(&empty_bar[stage]);
+      if (lane == 0 && ok && ours) mbar_arrive(&empty_bar[stage]);
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1;
@@ -879,11 +891,10 @@ cudaError_t weights_map(CUtensorMap* map, const MoeWeights& w, int64_t rows, int
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int Fmt, bool Down, bool Gated>
+template <int Fmt, bool Down, bool Gated, int Teams>
 cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
-  using S = Shape<Fmt, Down, Gated>;
+  using S = Shape<Fmt, Down, Gated, Teams>;
   static_assert(S::kBars <= 256, "barriers");
-  constexpr int kMaxSmem = 227 * 1024;
   const MoeWeights& w = Down ? a.down : a.up;
   const int64_t n_rows = Down ? a.out : a.hidden * (Gated ? 2 : 1);
   const int64_t bytes_k = Fmt == kFp8 ? p.K : (p.K + 1) / 2;
@@ -906,11 +917,11 @@ cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   p.stage_bytes = stage;
   const int route = route_bytes(p.slots, p.tokens, p.count);
   const int fixed = static_cast<int>(round_up(x_bytes, 16)) + S::kRed + 256 + route + 1024;
-  // Half an SM's shared memory where that holds enough of a ring: the second
-  // kernel's then starts to fill while the first one ends.
-  int room = 113 * 1024 - fixed;
-  if (room < 3 * stage) room = kMaxSmem - fixed;
-  p.stages = std::min(kMaxStages, room / stage);
+  constexpr int kMaxSmem = Teams == 1 ? 113 * 1024 : 227 * 1024;
+  p.stages = std::min(kMaxStages, (kMaxSmem - fixed) / stage);
+  if (Teams == 1 && p.stages < 3) return run_phase<Fmt, Down, Gated, 2>(a, p, x_bytes);
+  // two teams: a slot of the ring is one team's, whose waits then see its every phase
+  if (Teams == 2) p.stages &= ~1;
   if (p.stages < 2) return cudaErrorInvalidValue;
   p.off_x = p.stages * stage;
   p.off_red = p.off_x + static_cast<int>(round_up(x_bytes, 16));
@@ -933,7 +944,7 @@ cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
                           4 * S::kSlices, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e != cudaSuccess) return e;
   }
-  auto kern = moe_layer_kernel<Fmt, Down, Gated>;
+  auto kern = moe_layer_kernel<Fmt, Down, Gated, Teams>;
   int dev = 0;
   cudaGetDevice(&dev);
   static std::atomic<uint64_t> attr_set{0};
@@ -942,8 +953,9 @@ cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   });
   if (e != cudaSuccess) return e;
   const int64_t most = static_cast<int64_t>(p.slots) * p.tiles;
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(most, a.sm_count));
-  e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+  const int64_t ctas = static_cast<int64_t>(a.sm_count) * (Teams == 1 ? 2 : 1);
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(most, ctas));
+  e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(S::kThreads),
                        static_cast<size_t>(smem), a.stream, tw, tt, ts, p);
   count_launches(1);
   return e;
@@ -954,12 +966,12 @@ cudaError_t run_layer(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   p.K = static_cast<int>(a.width);
   p.rows = static_cast<int>(a.hidden);
   p.up0 = static_cast<int>(a.hidden);
-  const cudaError_t e = a.gated ? run_phase<Fmt, false, true>(a, p, x_bytes)
-                                : run_phase<Fmt, false, false>(a, p, x_bytes);
+  const cudaError_t e = a.gated ? run_phase<Fmt, false, true, 1>(a, p, x_bytes)
+                                : run_phase<Fmt, false, false, 1>(a, p, x_bytes);
   if (e != cudaSuccess) return e;
   p.K = static_cast<int>(a.hidden);
   p.rows = static_cast<int>(a.out);
-  return run_phase<Fmt, true, false>(a, p, 0);
+  return run_phase<Fmt, true, false, 1>(a, p, 0);
 }
 
 }  // namespace
@@ -971,7 +983,7 @@ int64_t moe_layer_scratch(const MoeLayerArgs& a) { return scratch_of(a).bytes; }
 bool moe_layer_fits(const MoeLayerArgs& a) {
   const int64_t slots = a.tokens * a.top_k;
   return slots <= kMaxLayerSlots &&
-         a.tokens * token_bytes(a) + route_bytes(slots, a.tokens, a.count) <= 160 * 1024;
+         a.tokens * token_bytes(a) + route_bytes(slots, a.tokens, a.count) <= 150 * 1024;
 }
 
 cudaError_t launch_moe_layer(const MoeLayerArgs& a) {

@@ -279,7 +279,7 @@ def test_inputs_written_just_before(dg, fmt):
 def test_largest_tokens_by_width(dg, fmt):
     # as many tokens of a width as shared memory takes, and one more
     width = 2048
-    fits = max(t for t in range(1, 64) if t * (2 * width + 64) + 12 * (t + 4) + 28 * t <= 160 * 1024 - 32)
+    fits = max(t for t in range(1, 64) if t * (2 * width + 64) + 12 * (t + 4) + 28 * t <= 150 * 1024 - 32)
     c = Case(fmt, fits, 1, 4, width, 64, 40, "bf16", seed=14)
     c.run(dg)
     c.check()
