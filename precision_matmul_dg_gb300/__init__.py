@@ -1010,20 +1010,27 @@ def nvf4_buffers(*shape, device="cuda"):
 
 def _nvf4_operand(torch, codes, scales, row_scales, what, K=None):
     """(row stride, matrix stride) of the codes of an NVF4 matrix or stack."""
-    dim = codes.dim()
-    s = _rows(codes, torch.uint8, what, None, dim if dim in (2, 3) else 2)
-    rows, width = codes.shape[-2:]
-    if K is None:
-        K = 2 * width
-    elif width != (K + 1) // 2:
-        raise ValueError("%s must have rows of %d bytes, got %d" % (what, (K + 1) // 2, width))
-    lead = codes.shape[:-2]
-    _rows(scales, torch.float8_e4m3fn, "the scales of " + what,
-          lead + _nvf4_scale_shape(rows, K), dim + 2)
-    _rows(row_scales, torch.float32, "the row scales of " + what, lead + (rows,), dim - 1)
-    if not (scales.is_contiguous() and row_scales.is_contiguous()):
-        raise ValueError("the scales of %s must be contiguous" % what)
-    return _pitch(s[-2], rows, width, 16), s[0] if dim == 3 else 0
+    s, shape = codes.stride(), codes.shape
+    dim = len(s)
+    rows, width = shape[-2:] if dim in (2, 3) else (0, 0)
+    of = K or 2 * width
+    tiles = ((rows + 127) // 128, (of + 63) // 64, 32, 16)
+    lead = () if dim == 2 else (shape[0],)
+    if not (codes.dtype is torch.uint8 and scales.dtype is torch.float8_e4m3fn and
+            row_scales.dtype is torch.float32 and (dim == 2 or dim == 3) and s[-1] == 1 and
+            width == (of + 1) // 2 and scales.shape == lead + tiles and
+            row_scales.shape == lead + (rows,) and scales.is_contiguous() and
+            row_scales.is_contiguous() and codes.is_cuda and scales.is_cuda and
+            row_scales.is_cuda):
+        # what is wrong
+        _rows(codes, torch.uint8, what, None, dim if dim in (2, 3) else 2)
+        if width != (of + 1) // 2:
+            raise ValueError("%s must have rows of %d bytes, got %d" % (what, (of + 1) // 2, width))
+        _rows(scales, torch.float8_e4m3fn, "the scales of " + what, lead + tiles, dim + 2)
+        _rows(row_scales, torch.float32, "the row scales of " + what, lead + (rows,), dim - 1)
+        if not (scales.is_contiguous() and row_scales.is_contiguous()):
+            raise ValueError("the scales of %s must be contiguous" % what)
+    return (s[-2] if rows > 1 else (width + 15) // 16 * 16), s[0]
 
 
 def _pitch(stride, rows, width, multiple):
@@ -1158,26 +1165,28 @@ def gemm_nvf4_grouped(A, scale_a, row_a, B, scale_b, row_b, offsets, D, bias=Non
 
 
 def _moe_weights(torch, w, bias, dtype, what):
-    """(format, MoeWeights, rows, K bytes) of one product's weights."""
-    nvf4 = len(w) == 3
+    """MoeWeights of one product's weights."""
     codes, scales = w[0], w[1]
-    count, n, kb = codes.shape
-    if nvf4:
+    if len(w) == 3:
         ld, stride = _nvf4_operand(torch, codes, scales, w[2], what)
-        z = (0, 0)
+        if codes.dim() != 3:
+            raise ValueError("%s must be a stack of matrices" % what)
+        m = MoeWeights(codes.data_ptr(), ld, stride, scales.data_ptr(), 0, 0, w[2].data_ptr())
     else:
         s, z = _fp8_operand(torch, codes, scales, what, 3)
-        ld, stride = s[1], s[0]
+        count, n, k = codes.shape
         if scales.shape[0] != count or scales.shape[1] != (n + 127) // 128 or \
-                scales.shape[2] < (kb + 127) // 128:
+                scales.shape[2] < (k + 127) // 128:
             raise ValueError("shape mismatch: %s %s with %s" % (
                 what, tuple(codes.shape), tuple(scales.shape)))
-    sb = 0
+        m = MoeWeights(codes.data_ptr(), s[1], s[0], scales.data_ptr(), z[1], z[0])
     if bias is not None:
-        sb = _rows(bias, dtype, "the bias of " + what, (count, n))[0]
-    return MoeWeights(codes.data_ptr(), ld, stride, scales.data_ptr(), z[1], z[0],
-                      w[2].data_ptr() if nvf4 else None,
-                      None if bias is None else bias.data_ptr(), sb)
+        m.stride_bias = _rows(bias, dtype, "the bias of " + what, codes.shape[:2])[0]
+        m.bias = bias.data_ptr()
+    return m
+
+
+_layer_scratch = {}  # sizes -> dg_moe_layer_scratch
 
 
 def moe_layer(X, ids, weights, up, down, D, activation="gelu", bias_up=None, bias_down=None,
@@ -1214,25 +1223,25 @@ def moe_layer(X, ids, weights, up, down, D, activation="gelu", bias_up=None, bia
     w2 = _moe_weights(torch, down, bias_down, X.dtype, "down")
     count, n1, k1 = up[0].shape
     hidden = n1 // 2 if gated else n1
-    k2 = down[0].shape[2]
-    if nvf4:
-        width_codes, hidden_codes = (width + 1) // 2, (hidden + 1) // 2
-    else:
-        width_codes, hidden_codes = width, hidden
     if ids.shape[0] != tokens or D.shape[0] != tokens or (gated and n1 % 2) or \
-            k1 != width_codes or down[0].shape[0] != count or down[0].shape[1] != out or \
-            k2 != hidden_codes:
+            k1 != ((width + 1) // 2 if nvf4 else width) or \
+            down[0].shape != (count, out, (hidden + 1) // 2 if nvf4 else hidden):
         raise ValueError("shape mismatch: X %s, ids %s, up %s, down %s, D %s" % tuple(
             tuple(t.shape) for t in (X, ids, up[0], down[0], D)))
     handle = _stream_of(stream, X, ids, weights, *up, *down, D, bias_up, bias_down)
-    nbytes = lib().dg_moe_layer_scratch(tokens, top_k, hidden, out)
+    sizes = (tokens, top_k, hidden, out)
+    nbytes = _layer_scratch.get(sizes)
+    if nbytes is None:
+        nbytes = lib().dg_moe_layer_scratch(*sizes)
+        if len(_layer_scratch) < 4096:
+            _layer_scratch[sizes] = nbytes
     scratch = _scratch(torch, max(nbytes, 16), X.device, stream)
     _check(lib().dg_moe_layer(
         tokens, top_k, count, width, hidden, out, code, X.data_ptr(),
         _pitch(sx[0], tokens, width, 8), ids.data_ptr(),
-        None if weights is None else weights.data_ptr(), 1 if nvf4 else 0, ctypes.byref(w1),
-        ctypes.byref(w2), 1 if gated else 0, D.data_ptr(), _pitch(sd[0], tokens, out, 8),
-        scratch.data_ptr(), nbytes, handle))
+        None if weights is None else weights.data_ptr(), 1 if nvf4 else 0, w1, w2,
+        1 if gated else 0, D.data_ptr(), _pitch(sd[0], tokens, out, 8), scratch.data_ptr(), nbytes,
+        handle))
     return D
 
 

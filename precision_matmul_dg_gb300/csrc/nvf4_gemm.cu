@@ -377,21 +377,36 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
     const int box_cols = p.dtype_d == DG_F32 ? 32 : 64;
     int acc = 0;
     uint32_t acc_phase = 0;
-    while (ok && next_tile<Grouped, BN, CG>(walk, p, units, rank, off, pre, tile)) {
-      // the rows' scales and the biases, on their way while the tile is multiplied
-      const int col0 = tile.n0 + first;
-      const int row = min(tile.row0 + in_tile + lane, p.M - 1);
-      const float s = p.alpha * __ldg(p.row_a + row);
+    // a tile's row scale, and the column scales and biases of two columns a lane,
+    // loaded a tile ahead
+    float row_next = 0.0f, col_next[2] = {0.0f, 0.0f}, bias_next[2] = {0.0f, 0.0f};
+    auto load_ahead = [&]() {
+      if (!next_tile<Grouped, BN, CG>(walk, p, units, rank, off, pre, tile)) return false;
+      row_next = __ldg(p.row_a + min(tile.row0 + in_tile + lane, p.M - 1));
       const float* rb = p.row_b + static_cast<int64_t>(tile.expert) * p.N;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = min(tile.n0 + first + 32 * i + lane, p.N - 1);
+        col_next[i] = __ldg(rb + c);
+        if (p.flags & kEpiBias)
+          bias_next[i] = load_as_f32(p.bias, tile.expert * p.stride_bias + c, p.dtype_d);
+      }
+      return true;
+    };
+    bool more = load_ahead();
+    while (ok && more) {
+      const N4Tile now = tile;
+      const int col0 = now.n0 + first;
+      const int row = min(now.row0 + in_tile + lane, p.M - 1);
+      const float s = p.alpha * row_next;
       __syncwarp();  // the last tile's have been read
 #pragma unroll
-      for (int i = 0; i < 64; i += 32) {
-        const int c = min(col0 + i + lane, p.N - 1);
-        col[i + lane] = __ldg(rb + c);
-        if (p.flags & kEpiBias)
-          col[64 + i + lane] = load_as_f32(p.bias, tile.expert * p.stride_bias + c, p.dtype_d);
+      for (int i = 0; i < 2; ++i) {
+        col[32 * i + lane] = col_next[i];
+        if (p.flags & kEpiBias) col[64 + 32 * i + lane] = bias_next[i];
       }
       __syncwarp();
+      more = load_ahead();
       const bool got = mbar_wait_abortable(&tmem_full[acc], acc_phase, p.timeout_ns, p.status,
                                            abort_flag);
       ok = __all_sync(0xffffffffu, got);
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
       tc_fence_after_sync();
       const uint32_t src = tmem_base + (static_cast<uint32_t>(in_tile) << 16) +
                            static_cast<uint32_t>(acc * BN + first);
-      const bool stored = tile.rows > in_tile && col0 < p.N;
+      const bool stored = now.rows > in_tile && col0 < p.N;
       const int64_t drow = static_cast<int64_t>(row) * p.ldd;
 #pragma unroll 1
       for (int c = 0; c < 64; c += 32) {
@@ -410,8 +425,10 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) {
+            // (a cluster-scope release would wait for the warp's stores: there is
+            // nothing in memory to release)
             if (CG == 2)
-              mbar_arrive_cluster(empty0 + static_cast<uint32_t>(acc * 8));
+              mbar_arrive_remote(empty0 + static_cast<uint32_t>(acc * 8));
             else
               mbar_arrive(&tmem_empty[acc]);
           }
@@ -477,9 +494,9 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
         }
         // the box is full, or ends with D
         if (box_cols == 32)
-          send_box(&tmap_d, box, p, tile, in_tile, col0 + c, 8, 0, lane);
+          send_box(&tmap_d, box, p, now, in_tile, col0 + c, 8, 0, lane);
         else if (c == 32 || col0 + 32 >= p.N)
-          send_box(&tmap_d, box, p, tile, in_tile, col0, c == 32 ? 8 : 4, 0, lane);
+          send_box(&tmap_d, box, p, now, in_tile, col0, c == 32 ? 8 : 4, 0, lane);
       }
       if (++acc == 2) {
         acc = 0;
