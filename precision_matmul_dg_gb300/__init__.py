@@ -1202,25 +1202,28 @@ def moe_layer(X, ids, weights, up, down, D, activation="gelu", bias_up=None, bia
     n] of X's type.  Scratch comes from torch's allocator (dg_moe_layer).
     """
     torch = (_FP or _fp())[0]
+    dtype = X.dtype
     code = _float_code(X, "X")
-    sx = _rows(X, X.dtype, "X")
+    sx = _rows(X, dtype, "X")
     tokens, width = X.shape
     _rows(ids, torch.int32, "ids")
     top_k = ids.shape[1]
-    sd = _rows(D, X.dtype, "D")
+    sd = _rows(D, dtype, "D")
     out = D.shape[1]
     if weights is not None:
         _rows(weights, torch.float32, "weights", ids.shape)
-    if not ids.is_contiguous() or not (weights is None or weights.is_contiguous()):
-        raise ValueError("ids and weights must be contiguous")
-    if activation not in ("gelu", "swiglu"):
-        raise ValueError("activation must be gelu or swiglu")
+        if not weights.is_contiguous():
+            raise ValueError("weights must be contiguous")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
     gated = activation == "swiglu"
+    if not gated and activation != "gelu":
+        raise ValueError("activation must be gelu or swiglu")
+    nvf4 = len(up) == 3
     if len(up) != len(down) or len(up) not in (2, 3):
         raise ValueError("up and down are both (codes, scales) or (codes, scales, row scales)")
-    nvf4 = len(up) == 3
-    w1 = _moe_weights(torch, up, bias_up, X.dtype, "up")
-    w2 = _moe_weights(torch, down, bias_down, X.dtype, "down")
+    w1 = _moe_weights(torch, up, bias_up, dtype, "up")
+    w2 = _moe_weights(torch, down, bias_down, dtype, "down")
     count, n1, k1 = up[0].shape
     hidden = n1 // 2 if gated else n1
     if ids.shape[0] != tokens or D.shape[0] != tokens or (gated and n1 % 2) or \
@@ -1228,20 +1231,22 @@ def moe_layer(X, ids, weights, up, down, D, activation="gelu", bias_up=None, bia
             down[0].shape != (count, out, (hidden + 1) // 2 if nvf4 else hidden):
         raise ValueError("shape mismatch: X %s, ids %s, up %s, down %s, D %s" % tuple(
             tuple(t.shape) for t in (X, ids, up[0], down[0], D)))
-    handle = _stream_of(stream, X, ids, weights, *up, *down, D, bias_up, bias_down)
+    if _gpus != 1:
+        _same_gpu(torch, (X, ids, weights, *up, *down, D, bias_up, bias_down))
+    handle = _stream_of(stream, X)
     sizes = (tokens, top_k, hidden, out)
     nbytes = _layer_scratch.get(sizes)
     if nbytes is None:
         nbytes = lib().dg_moe_layer_scratch(*sizes)
         if len(_layer_scratch) < 4096:
             _layer_scratch[sizes] = nbytes
-    scratch = _scratch(torch, max(nbytes, 16), X.device, stream)
+    scratch = X.new_empty(max(nbytes, 16), dtype=torch.uint8) if stream is None else \
+        _scratch(torch, max(nbytes, 16), X.device, stream)
     _check(lib().dg_moe_layer(
         tokens, top_k, count, width, hidden, out, code, X.data_ptr(),
-        _pitch(sx[0], tokens, width, 8), ids.data_ptr(),
-        None if weights is None else weights.data_ptr(), 1 if nvf4 else 0, w1, w2,
-        1 if gated else 0, D.data_ptr(), _pitch(sd[0], tokens, out, 8), scratch.data_ptr(), nbytes,
-        handle))
+        sx[0] if tokens > 1 else -(-width // 8) * 8, ids.data_ptr(),
+        None if weights is None else weights.data_ptr(), nvf4, w1, w2, gated, D.data_ptr(),
+        sd[0] if tokens > 1 else -(-out // 8) * 8, scratch.data_ptr(), nbytes, handle))
     return D
 
 

@@ -204,7 +204,7 @@ def test_scratch_is_left_alone_past_its_size(dg, fmt):
     keep = dg._scratch
     dg._scratch = lambda torch, n, device, stream: room
     try:
-        c.run(dg)
+        c.run(dg, stream=torch.cuda.current_stream())
     finally:
         dg._scratch = keep
     dg.check_status()
