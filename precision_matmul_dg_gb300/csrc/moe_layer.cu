@@ -75,7 +75,7 @@ struct Shape {
   static constexpr int kW = (Gated ? 2 : 1) * kSlices * kBlockW;
   static constexpr int kS = Fmt == kNvf4 ? (Gated ? 2 : 1) * kSlices * 2048 : 0;
   static constexpr int kRed = kEpiWarps * kMmaWarps * 4 * 32 * 4;
-  static constexpr int kBars = (2 * kMaxStages + 2 * kEpiWarps) * 8 + 8;
+  static constexpr int kBars = (2 * kMaxStages + 2 * kEpiWarps + 1) * 8 + 8;
 };
 // A slot's share of a stage of the second product: FP16 values, then a scale for
 // each 32 of them.  Rows are 64 bytes apart in their banks: two rows' 64-byte
@@ -128,7 +128,6 @@ struct Route {
   float* weight;             // per slot
   int* valid;                // per token: its slots that are not dropped
   float* fx;                 // per token: what its values are multiplied by
-  unsigned* amax;            // per token
   int* ids;
   int *cnt, *start, *base;   // per expert
   int* chunks;               // their number
@@ -144,22 +143,60 @@ __device__ __forceinline__ Route route_at(int* m, const LayerParams& p) {
   r.weight = reinterpret_cast<float*>(r.n + p.slots);
   r.valid = r.n + 2 * p.slots;
   r.fx = reinterpret_cast<float*>(r.valid + p.tokens);
-  r.amax = reinterpret_cast<unsigned*>(r.fx + p.tokens);
-  r.cnt = reinterpret_cast<int*>(r.amax + p.tokens);
+  r.cnt = reinterpret_cast<int*>(r.fx + p.tokens);
   r.start = r.cnt + p.count;
   r.base = r.start + p.count;
   r.chunks = r.base + p.count;
   return r;
 }
 int route_bytes(int64_t slots, int64_t tokens, int64_t count) {
-  return static_cast<int>(4 * ((slots + 3) / 4 * 4 + 6 * slots + 3 * tokens + 3 * count + 4));
+  return static_cast<int>(4 * ((slots + 3) / 4 * 4 + 6 * slots + 2 * tokens + 3 * count + 4));
 }
 
 __device__ __forceinline__ void others_sync() {
   asm volatile("bar.sync 2, %0;" ::"n"(kOtherThreads) : "memory");
 }
 
-// By the threads that do not multiply, numbered i.
+// Up to 32 slots: by one warp, a slot per lane, which has them without a barrier.
+__device__ __forceinline__ void build_route_warp(const Route& r, const LayerParams& p, int lane) {
+  int e = lane < p.slots ? __ldg(p.ids + lane) : -1;
+  if (lane < p.slots) r.weight[lane] = p.weights ? __ldg(p.weights + lane) : 1.0f;
+  if (lane < p.tokens) r.valid[lane] = 0;
+  if (e >= p.count) e = -1;
+  int less = 0, same = 0, before = 0;  // slots of smaller experts, of this one, and of those before
+  for (int j = 0; j < p.slots; ++j) {
+    const int f = __shfl_sync(0xffffffffu, e, j);
+    less += f >= 0 && f < e;
+    same += f == e;
+    before += f == e && j < lane;
+  }
+  const bool there = e >= 0;
+  const int at = there ? less + before : -1;
+  const bool starts = there && before % p.chunk == 0;
+  const unsigned all = __ballot_sync(0xffffffffu, starts);
+  int k = 0;  // chunks before this slot's
+  for (int j = 0; j < p.slots; ++j) {
+    const int f = __shfl_sync(0xffffffffu, at, j);
+    k += (all >> j & 1u) && f < at;
+  }
+  if (lane < p.slots) {
+    r.pos[lane] = at;
+    if (there) {
+      const int t = lane / p.top_k;
+      r.token[at] = t;
+      atomicAdd(&r.valid[t], 1);
+    }
+  }
+  if (starts) {
+    r.expert[k] = e;
+    r.first[k] = at;
+    r.n[k] = min(p.chunk, same - before);
+  }
+  if (lane == 0) *r.chunks = __popc(all);
+  __syncwarp();
+}
+
+// More: by the threads that do not multiply, numbered i.
 __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p, int i) {
   for (int e = i; e < p.count; e += kOtherThreads) r.cnt[e] = 0;
   for (int t = i; t < p.tokens; t += kOtherThreads) r.valid[t] = 0;
@@ -219,6 +256,7 @@ __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p
       r.n[k] = min(p.chunk, c - at);
     }
   }
+  others_sync();
 }
 
 // A CTA's units, chunk by chunk of a tile (neighbours share a tile's place in
@@ -258,18 +296,6 @@ __device__ __forceinline__ int place_of(int k) {
   return Fmt == kNvf4 ? k : (k & 12) << 1 | (k & 16) >> 2 | (k & 3);
 }
 
-// Eight 16-bit values of a row of K from k on, zeros past its end.
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int K) {
-  if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0u;
-    const uint32_t hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0u;
-    w[i] = lo | (hi << 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 // The largest finite magnitude of two bfloat16 values, as bits.
 __device__ __forceinline__ uint32_t finite_max(uint32_t w) {
   const uint32_t a = w & 0x7FFFu, b = w >> 16 & 0x7FFFu;
@@ -280,66 +306,70 @@ __device__ __forceinline__ uint32_t scaled_half2(uint32_t w, float f) {
   return F16::pack(v.x * f, v.y * f);
 }
 
-// The tokens in shared memory as FP16, by the MMA warps: FP16 as it is, BF16
-// times a power of two per token that brings its largest finite value near the
-// top (infinities and NaNs stay what they are).
-template <int Fmt, int kThreads>
-__device__ __forceinline__ void load_tokens(const LayerParams& p, uint8_t* xs, const Route& r) {
-  constexpr int kAhead = 4;
-  const int per_row = p.k_blocks * Shape<Fmt, false, false>::kBlockK / 8;  // pieces, a multiple of 16
-  const int pieces = p.tokens * per_row;
-  if (p.bf16) {
-    for (int t = threadIdx.x; t < p.tokens; t += kThreads) r.amax[t] = 0u;
-    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-    for (int i0 = threadIdx.x; i0 < pieces; i0 += kAhead * kThreads) {
-      uint4 v[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j * kThreads, t = i / per_row;
-        v[j] = i < pieces ? load8(p.X + t * p.ldx, (i - t * per_row) * 8, p.K)
-                          : make_uint4(0u, 0u, 0u, 0u);
+// The tokens in shared memory as FP16: FP16 as it is, BF16 times a power of two
+// per token that brings its largest finite value near the top (infinities and
+// NaNs stay what they are).  Bulk copies bring them (all CTAs want all of them: by
+// loads into registers 16 tokens of 2048 took 9.5 us); an MMA warp per token then
+// converts it in place.
+__device__ __forceinline__ void copy_tokens(const LayerParams& p, uint8_t* xs, uint64_t* bar) {
+  const uint32_t bytes = static_cast<uint32_t>(p.K / 8 * 16);
+  if (bytes == 0) return;
+  const uint64_t keep = policy_evict_last();
+  mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.tokens) * bytes);
+  for (int t = 0; t < p.tokens; ++t)
+    bulk_load_g2s(xs + t * p.x_pitch, p.X + t * p.ldx, bytes, bar, keep);
+}
+template <int Fmt, int kWarps>
+__device__ __forceinline__ bool convert_tokens(const LayerParams& p, uint8_t* xs, const Route& r,
+                                               uint64_t* bar, int warp, int lane) {
+  const int padded = p.k_blocks * Shape<Fmt, false, false>::kBlockK, whole = p.K / 8 * 8;
+  // what the bulk copies leave: the last values, and zeros past them
+  for (int t = warp; t < p.tokens; t += kWarps)
+    for (int k = whole + lane; k < padded; k += 32)
+      reinterpret_cast<uint16_t*>(xs + t * p.x_pitch)[k] = k < p.K ? p.X[t * p.ldx + k] : 0;
+  if (whole > 0 && !__all_sync(0xffffffffu, mbar_wait(bar, 0, p.timeout_ns, p.status))) return false;
+  __syncwarp();
+  for (int t = warp; t < p.tokens; t += kWarps) {
+    uint8_t* row = xs + t * p.x_pitch;
+    float f = 1.0f, inv = 1.0f;
+    if (p.bf16) {
+      uint32_t m = 0;
+      for (int k = lane * 8; k < padded; k += 256) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + k * 2);
+        m = max(max(m, max(finite_max(v.x), finite_max(v.y))),
+                max(finite_max(v.z), finite_max(v.w)));
       }
+      f = half_factor(BF16::one(__reduce_max_sync(0xffffffffu, m)), inv);
+    }
+    if (lane == 0) r.fx[t] = inv;
+    if (Fmt == kNvf4) {
+      if (p.bf16)
+        for (int k = lane * 8; k < padded; k += 256) {
+          uint4* at = reinterpret_cast<uint4*>(row + k * 2);
+          const uint4 v = *at;
+          *at = make_uint4(scaled_half2(v.x, f), scaled_half2(v.y, f), scaled_half2(v.z, f),
+                           scaled_half2(v.w, f));
+        }
+    } else {
+      for (int k = lane * 32; k < padded; k += 1024) {
+        uint4* at = reinterpret_cast<uint4*>(row + k * 2);
+        uint4 v[4];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j * kThreads;
-        uint32_t m = max(max(finite_max(v[j].x), finite_max(v[j].y)),
-                         max(finite_max(v[j].z), finite_max(v[j].w)));
-        // (16 lanes share a token at least)
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(__activemask(), m, d));
-        if ((threadIdx.x & 15) == 0 && i < pieces) atomicMax(&r.amax[i / per_row], m);
+        for (int i = 0; i < 4; ++i) {
+          v[i] = at[i];
+          if (p.bf16)
+            v[i] = make_uint4(scaled_half2(v[i].x, f), scaled_half2(v[i].y, f),
+                              scaled_half2(v[i].z, f), scaled_half2(v[i].w, f));
+        }
+        // values 4 q .. 4 q + 3 beside 16 + 4 q ..
+        at[0] = make_uint4(v[0].x, v[0].y, v[2].x, v[2].y);
+        at[1] = make_uint4(v[0].z, v[0].w, v[2].z, v[2].w);
+        at[2] = make_uint4(v[1].x, v[1].y, v[3].x, v[3].y);
+        at[3] = make_uint4(v[1].z, v[1].w, v[3].z, v[3].w);
       }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
   }
-  for (int i0 = threadIdx.x; i0 < pieces; i0 += kAhead * kThreads) {
-    uint4 v[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j * kThreads, t = i / per_row;
-      if (i < pieces) v[j] = load8(p.X + t * p.ldx, (i - t * per_row) * 8, p.K);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j * kThreads, t = i / per_row, k = (i - t * per_row) * 8;
-      if (i >= pieces) break;
-      float inv = 1.0f;
-      if (p.bf16) {
-        const float f = half_factor(BF16::one(r.amax[t]), inv);
-        v[j] = make_uint4(scaled_half2(v[j].x, f), scaled_half2(v[j].y, f),
-                          scaled_half2(v[j].z, f), scaled_half2(v[j].w, f));
-      }
-      if (k == 0) r.fx[t] = inv;
-      uint8_t* row = xs + t * p.x_pitch + (k & ~31) * 2;
-      if (Fmt == kNvf4) {
-        *reinterpret_cast<uint4*>(row + (k & 31) * 2) = v[j];
-      } else {
-        *reinterpret_cast<uint2*>(row + place_of<kFp8>(k & 31) * 2) = make_uint2(v[j].x, v[j].y);
-        *reinterpret_cast<uint2*>(row + place_of<kFp8>((k & 31) + 4) * 2) =
-            make_uint2(v[j].z, v[j].w);
-      }
-    }
-  }
+  return true;
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -425,7 +455,8 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
   uint64_t* empty_bar = full_bar + kMaxStages;
   uint64_t* red_full = empty_bar + kMaxStages;
   uint64_t* red_empty = red_full + kEpiWarps;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(red_empty + kEpiWarps);
+  uint64_t* x_bar = red_empty + kEpiWarps;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(x_bar + 1);
   const Route r = route_at(reinterpret_cast<int*>(smem + p.off_route), p);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -437,6 +468,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
       mbar_init(&red_full[b], kMmaWarps);
       mbar_init(&red_empty[b], 1);
     }
+    mbar_init(x_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -445,15 +477,27 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
     tma_prefetch_desc(&tmap_tail);
     if (Fmt == kNvf4) tma_prefetch_desc(&tmap_sf);
   }
+  __syncthreads();
   // The second kernel starts while the first one runs: what it reads before it
   // waits (choices, routing weights and weights) was there before the first, which
   // waited for every kernel before it ahead of letting this one start.
   if (!Down) grid_dependency_wait();
-  if (warp >= kMmaWarps)
+  bool ok = true;
+  if (warp == kTmaWarp && !Down && elect_one_lane()) copy_tokens(p, xs, x_bar);
+  if (p.slots <= 32) {
+    if (warp == kTmaWarp) build_route_warp(r, p, lane);
+  } else if (warp >= kMmaWarps) {
     build_route(r, p, static_cast<int>(threadIdx.x) - kMmaWarps * 32);
-  else if (!Down)
-    load_tokens<Fmt, kMmaWarps * 32>(p, xs, r);
-  __syncthreads();
+  }
+  if (!Down && warp < kMmaWarps) ok = convert_tokens<Fmt, kMmaWarps>(p, xs, r, x_bar, warp, lane);
+  // the routing and the tokens are there; who loads needs only the first, which
+  // that warp has
+  if (warp == kTmaWarp) {
+    __syncwarp();
+    asm volatile("bar.arrive 3, %0;" ::"n"(S::kThreads) : "memory");
+  } else {
+    asm volatile("bar.sync 3, %0;" ::"n"(S::kThreads) : "memory");
+  }
   const int chunks = *r.chunks;
   const int units = chunks * p.tiles;
   const int k_stages = (p.k_blocks + kSlices - 1) / kSlices;
@@ -467,7 +511,6 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
     int64_t issued = 0;
     int stage = 0;
     uint32_t phase = 0;
-    bool ok = true;
     // the loads of K stage ks of a unit: weights, or activations
     auto load = [&](int ks, int st, int e, bool weights, bool acts) {
       uint8_t* dst = smem + st * p.stage_bytes;
@@ -539,6 +582,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
     for (int64_t i = first; i < issued; ++i)
       mbar_wait(&full_bar[i % p.stages], static_cast<uint32_t>((i / p.stages) & 1), p.timeout_ns,
                 p.status);
+    if (!Down && p.K >= 8) mbar_wait(x_bar, 0, p.timeout_ns, p.status);
     return;
   }
 
@@ -675,7 +719,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
                             ((group & 1) * 16 + mrow + 8 * (mat & 1)) * 128);
   int stage = 0, buf = 0, turn = 0;  // turn: the team whose stage it is
   uint32_t phase = 0, buf_phase = 0;
-  bool ok = true;
+  if (!ok) *abort_flag = 1;
   // FP8: the scales of the unit's weight blocks that this warp will meet, those
   // of stage ks in lane ks, for the group's first and last row (a group may
   // straddle two blocks); loaded a unit ahead.
