@@ -158,10 +158,13 @@ __device__ __forceinline__ void others_sync() {
 }
 
 // Up to 32 slots: by one warp, a slot per lane, which has them without a barrier.
+// (The first kernel needs neither the routing weights nor the counts per token.)
+template <bool Down>
 __device__ __forceinline__ void build_route_warp(const Route& r, const LayerParams& p, int lane) {
   int e = lane < p.slots ? __ldg(p.ids + lane) : -1;
-  if (lane < p.slots) r.weight[lane] = p.weights ? __ldg(p.weights + lane) : 1.0f;
-  if (lane < p.tokens) r.valid[lane] = 0;
+  if (Down && lane < p.slots) r.weight[lane] = p.weights ? __ldg(p.weights + lane) : 1.0f;
+  if (Down && lane < p.tokens) r.valid[lane] = 0;
+  __syncwarp();
   if (e >= p.count) e = -1;
   int less = 0, same = 0, before = 0;  // slots of smaller experts, of this one, and of those before
   for (int j = 0; j < p.slots; ++j) {
@@ -184,7 +187,7 @@ __device__ __forceinline__ void build_route_warp(const Route& r, const LayerPara
     if (there) {
       const int t = lane / p.top_k;
       r.token[at] = t;
-      atomicAdd(&r.valid[t], 1);
+      if (Down) atomicAdd(&r.valid[t], 1);
     }
   }
   if (starts) {
@@ -197,13 +200,14 @@ __device__ __forceinline__ void build_route_warp(const Route& r, const LayerPara
 }
 
 // More: by the threads that do not multiply, numbered i.
+template <bool Down>
 __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p, int i) {
   for (int e = i; e < p.count; e += kOtherThreads) r.cnt[e] = 0;
-  for (int t = i; t < p.tokens; t += kOtherThreads) r.valid[t] = 0;
+  for (int t = i; Down && t < p.tokens; t += kOtherThreads) r.valid[t] = 0;
   for (int s = i; s < (p.slots + 3) / 4 * 4; s += kOtherThreads) {
     const int e = s < p.slots ? __ldg(p.ids + s) : -1;
     r.ids[s] = e >= 0 && e < p.count ? e : -1;
-    if (s < p.slots) r.weight[s] = p.weights ? __ldg(p.weights + s) : 1.0f;
+    if (Down && s < p.slots) r.weight[s] = p.weights ? __ldg(p.weights + s) : 1.0f;
   }
   others_sync();
   for (int s = i; s < p.slots; s += kOtherThreads) {
@@ -218,7 +222,7 @@ __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p
                 (4 * k + 3 < s && w.w == e);
       }
       atomicAdd(&r.cnt[e], 1);  // counts: the order does not matter
-      atomicAdd(&r.valid[s / p.top_k], 1);
+      if (Down) atomicAdd(&r.valid[s / p.top_k], 1);
     }
     r.pos[s] = rank;
   }
@@ -483,11 +487,11 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
   // waited for every kernel before it ahead of letting this one start.
   if (!Down) grid_dependency_wait();
   bool ok = true;
-  if (warp == kTmaWarp && !Down && elect_one_lane()) copy_tokens(p, xs, x_bar);
+  if (warp == 0 && !Down && elect_one_lane()) copy_tokens(p, xs, x_bar);
   if (p.slots <= 32) {
-    if (warp == kTmaWarp) build_route_warp(r, p, lane);
+    if (warp == kTmaWarp) build_route_warp<Down>(r, p, lane);
   } else if (warp >= kMmaWarps) {
-    build_route(r, p, static_cast<int>(threadIdx.x) - kMmaWarps * 32);
+    build_route<Down>(r, p, static_cast<int>(threadIdx.x) - kMmaWarps * 32);
   }
   if (!Down && warp < kMmaWarps) ok = convert_tokens<Fmt, kMmaWarps>(p, xs, r, x_bar, warp, lane);
   // the routing and the tokens are there; who loads needs only the first, which
