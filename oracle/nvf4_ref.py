@@ -41,31 +41,25 @@ def quantize(x, given=None):
     x = np.asarray(x, np.float32)
     rows, K = x.shape
     groups = -(-K // GROUP)
-    codes = np.zeros((rows, K), np.uint8)
-    scales = np.zeros((rows, groups), np.uint8)
-    out = np.zeros(rows, np.float32)
-    for i in range(rows):
-        blocks = [x[i, GROUP * j:GROUP * (j + 1)] for j in range(groups)]
-        fine = [bool(np.isfinite(b).all()) for b in blocks]
-        if given is None:
-            r = row_scale(max([float(np.abs(b).max()) for b, f in zip(blocks, fine) if f] or [0.0]))
-        else:
-            r = np.float32(given[i])
-            if not 2.0 ** -100 <= r <= 2.0 ** 100:
-                out[i], scales[i] = r, NAN
-                continue
-        out[i] = r
-        for j, b in enumerate(blocks):
-            if not fine[j]:
-                scales[i, j] = NAN
-                continue
-            with np.errstate(over="ignore"):
-                t = np.abs(b).max() / (np.float32(6.0) * r)
-                s = max(int(fp8_ref.e4m3_codes(t)), 1)
-                u = np.float32(fp8_ref.VALUES[s]) * r
-                codes[i, GROUP * j:GROUP * (j + 1)] = e2m1_codes(b / u)
-            scales[i, j] = s
-    return codes, scales, out
+    full = np.zeros((rows, groups * GROUP), np.float32)
+    full[:, :K] = x
+    v = full.reshape(rows, groups, GROUP)
+    fine = np.isfinite(v).all(2)
+    amax = np.abs(np.where(fine[..., None], v, 0)).max(2)
+    if given is None:
+        r = np.array([row_scale(float(a)) for a in amax.max(1)], np.float32)
+        ok = np.ones(rows, bool)
+    else:
+        r = np.asarray(given, np.float32)
+        ok = (r >= 2.0 ** -100) & (r <= 2.0 ** 100)
+    safe = np.where(ok, r, np.float32(1))[:, None]
+    with np.errstate(over="ignore", invalid="ignore"):
+        scales = np.maximum(fp8_ref.e4m3_codes(amax / (np.float32(6.0) * safe)), 1)
+        u = fp8_ref.VALUES[scales].astype(np.float32) * safe
+        codes = e2m1_codes(v / u[..., None])
+    good = fine & ok[:, None]
+    codes = np.where(good[..., None], codes, 0).astype(np.uint8)
+    return (codes.reshape(rows, -1)[:, :K], np.where(good, scales, NAN).astype(np.uint8), r)
 
 
 def pack(codes):
@@ -84,12 +78,12 @@ def unpack(packed, K):
 
 
 def tiles(scales):
-    """Scale codes [rows, groups] in tiles, one by one."""
+    """Scale codes [rows, groups] in tiles, group by group."""
     rows, groups = scales.shape
     out = np.zeros((-(-rows // 128), -(-groups // 4), 32, 16), np.uint8)
-    for r in range(rows):
-        for g in range(groups):
-            out[r // 128, g // 4, r % 32, 4 * (r % 128 // 32) + g % 4] = scales[r, g]
+    r = np.arange(rows)
+    for g in range(groups):
+        out[r // 128, g // 4, r % 32, 4 * (r % 128 // 32) + g % 4] = scales[:, g]
     return out
 
 

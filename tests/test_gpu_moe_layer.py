@@ -35,10 +35,11 @@ def weights(fmt, count, n, k, rng, pad_rows=0):
         scales = np.stack([p[1] for p in parts])
         return ((gpu(room).view(torch.float8_e4m3fn)[:, :n, :k], gpu(scales)),
                 np.stack([fp8_ref.values(p[0], p[1], 128) for p in parts]))
-    parts = [ref.quantize(m) for m in w]
+    codes, scales, rows = ref.quantize(w.reshape(count * n, k))
+    parts = list(zip(codes.reshape(count, n, k), scales.reshape(count, n, -1)))
     room = np.full((count, n + pad_rows, -(-k // 32) * 16 + 16), 0x77, np.uint8)
-    room[:, :n, :(k + 1) // 2] = np.stack([ref.pack(p[0]) for p in parts])
-    rows = np.stack([p[2] for p in parts]) * rng.uniform(0.6, 1.7, (count, n)).astype(np.float32)
+    room[:, :n, :(k + 1) // 2] = ref.pack(codes).reshape(count, n, -1)
+    rows = rows.reshape(count, n) * rng.uniform(0.6, 1.7, (count, n)).astype(np.float32)
     rows = rows.astype(np.float32)
     return ((gpu(room)[:, :n, :(k + 1) // 2],
              gpu(np.stack([ref.tiles(p[1]) for p in parts])).view(torch.float8_e4m3fn), gpu(rows)),
