@@ -387,6 +387,9 @@ __device__ __forceinline__ uint32_t ld_shared1(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void st_shared1(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -398,8 +401,7 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
 // c += a (16 x 16, weights) . b (16 x 8, activations)
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -424,8 +426,13 @@ __device__ __forceinline__ void scale_pairs(uint32_t word, uint32_t at, uint32_t
   const uint32_t two = __byte_perm(word, 0u, 0x4420u + 0x0011u * at);
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  s[0] = __byte_perm(h, 0u, 0x1010);
-  s[1] = __byte_perm(h, 0u, 0x3232);
+  // (a multiplication takes a half twice without an instruction of its own)
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "mov.b32 %0, {a, a};\n\t"
+      "mov.b32 %1, {b, b};\n\t}"
+      : "=r"(s[0]), "=r"(s[1])
+      : "r"(h));
 }
 
 __device__ __forceinline__ float as_f32(const void* p, int64_t i, int bf16) {
@@ -721,7 +728,8 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
   const uint32_t a_base = smem0 +
       static_cast<uint32_t>(((group >> 1) * kSlices + slice) * S::kBlockW +
                             ((group & 1) * 16 + mrow + 8 * (mat & 1)) * 128);
-  int stage = 0, buf = 0, turn = 0;  // turn: the team whose stage it is
+  // stages go to the teams in turn: `skip` of the unit's come before this team's first
+  int stage = Teams == 1 ? 0 : team, buf = 0, skip = stage;
   uint32_t phase = 0, buf_phase = 0;
   if (!ok) *abort_flag = 1;
   // FP8: the scales of the unit's weight blocks that this warp will meet, those
@@ -740,7 +748,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
   };
   walk.start(blockIdx.x, step, chunks);
   if (units > 0) load_sw(walk, 0);
-  while (walk.tile < p.tiles && units > 0) {
+  while (ok && walk.tile < p.tiles && units > 0) {
     const int tile = walk.tile, n = r.n[walk.u], first = r.first[walk.u];
     // this lane's column of the activations, and its two columns of the sums
     // (past the last: the last)
@@ -760,24 +768,22 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
     const bool second_a = Fmt == kFp8 && (row_g + g) >> 7 != row_g >> 7;
     const bool second_b = Fmt == kFp8 && (row_g + g + 8) >> 7 != row_g >> 7;
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int ks = 0; ks < k_stages; ++ks) {
-      if (Fmt == kFp8 && ks > 0 && (ks & 31) == 0) {  // beyond the 32 that lanes hold
+    int sw_at = 0;
+    for (int ks = skip; ks < k_stages; ks += Teams) {
+      if (Fmt == kFp8 && ks - sw_at >= 32) {  // beyond the 32 that lanes hold
+        sw_at += 32;
         const float keep0 = sw0_next, keep1 = sw1_next;
         UnitWalk now = walk;
         now.tile = tile;
         now.u = walk.u - walk.d_u;
         if (now.u < 0) now.u += walk.chunks;
-        load_sw(now, ks);
+        load_sw(now, sw_at);
         sw0 = sw0_next, sw1 = sw1_next, sw0_next = keep0, sw1_next = keep1;
       }
       const int kb = ks * kSlices + slice;
-      const bool ours = Teams == 1 || turn == team;
-      if (Teams > 1) turn ^= 1;
-      if (ok && ours) {
-        ok = __all_sync(0xffffffffu, mbar_wait_abortable(&full_bar[stage], phase, p.timeout_ns,
-                                                         p.status, abort_flag));
-        if (!ok) *abort_flag = 1;
-      }
+      ok = __all_sync(0xffffffffu, mbar_wait_abortable(&full_bar[stage], phase, p.timeout_ns,
+                                                       p.status, abort_flag));
+      if (!ok) break;
       float sa = 1.0f, sb = 1.0f;
       if (Fmt == kFp8) {
         const float s0 = __shfl_sync(0xffffffffu, sw0, ks & 31);
@@ -785,7 +791,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
         sa = second_a ? s1 : s0;
         sb = second_b ? s1 : s0;
       }
-      if (ok && ours && kb < p.k_blocks) {
+      if (kb < p.k_blocks) {
         const uint32_t at = static_cast<uint32_t>(stage * p.stage_bytes);
         const uint32_t b_at = Down ? b_base + at : b_base + static_cast<uint32_t>(kb * S::kBlockK * 2);
         uint32_t w[4][4];
@@ -832,14 +838,20 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
           const uint32_t sf = smem0 + at +
               static_cast<uint32_t>(S::kW + ((group >> 1) * kSlices + slice) * 2048 +
                                     ((group & 1) * 16 + g) * 16 + (tile & 3) * 4);
+          // (a scale tile past the last is another's: its codes are zeros, NaNs not)
+          if (p.k_tiles - 4 * kb < 4) {
+            for (int mm = p.k_tiles - 4 * kb; mm < 4; ++mm) {
+              st_shared1(sf + mm * 512, 0u);
+              st_shared1(sf + mm * 512 + 128, 0u);
+            }
+            fence_proxy_async_smem();  // before the next copy into this stage
+          }
           float c[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
           for (int mm = 0; mm < 4; ++mm) {
-            // (a scale tile past the last is another's: its codes are zeros, NaNs not)
-            const bool in = 4 * kb + mm < p.k_tiles;
             uint32_t sg[2], sh[2];
-            scale_pairs(in ? ld_shared1(sf + mm * 512) : 0u, q >> 1, sg);
-            scale_pairs(in ? ld_shared1(sf + mm * 512 + 128) : 0u, q >> 1, sh);
+            scale_pairs(ld_shared1(sf + mm * 512), q >> 1, sg);
+            scale_pairs(ld_shared1(sf + mm * 512 + 128), q >> 1, sh);
             uint32_t hv0[2], hv1[2];
             if (Down) {
 #pragma unroll
@@ -875,19 +887,22 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
         }
       }
       __syncwarp();
-      if (lane == 0 && ok && ours) mbar_arrive(&empty_bar[stage]);
-      if (++stage == p.stages) {
-        stage = 0;
+      if (lane == 0) mbar_arrive(&empty_bar[stage]);
+      stage += Teams;
+      if (stage >= p.stages) {
+        stage -= p.stages;
         phase ^= 1;
       }
     }
+    if (Teams > 1) skip = (skip + k_stages) & 1;
     // the slices' sums go to the unit's epilogue warp
-    if (ok) {
+    if (ok)
       ok = __all_sync(0xffffffffu, mbar_wait_abortable(&red_empty[buf], buf_phase ^ 1, p.timeout_ns,
                                                        p.status, abort_flag));
-      if (!ok) *abort_flag = 1;
+    if (!ok) {
+      *abort_flag = 1;
+      break;
     }
-    if (!ok) break;
     float* mine = red + (buf * kMmaWarps + warp) * 4 * 32 + lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i) mine[i * 32] = acc[i];
