@@ -6,7 +6,7 @@
 prompt(): many tokens, activations in 4 bits too: sorted by expert and quantized
 on the way, the experts' two products (the first with GELU), and the way back
 with the routing weights.  decode(): a few tokens, activations in 16 bits, the
-whole layer in two kernels, on the same weights or on 8-bit ones.  The program
+whole layer in three kernels, on the same weights or on 8-bit ones.  The program
 runs both, compares them with plain FP32 torch and prints times.
 """
 

@@ -672,7 +672,7 @@ dg_status dg_gemm_nvf4_grouped(int64_t count, int64_t rows, int64_t N, int64_t K
                                dg_stream_t stream);
 
 /* ------------------------------------------- an expert layer for few tokens
- * The whole layer of a mixture of experts in two launches:
+ * The whole layer of a mixture of experts in three launches:
  *   D[t,:] = sum over j of weights[t,j] * (W2_e h + b2_e),  e = ids[t,j],
  *   h = act(W1_e x_t + b1_e)
  * on weights quantized in 8 bits (E4M3 codes with 128 x 128 FP32 scales, as
@@ -713,8 +713,8 @@ typedef struct {
  * Errors: DG_ERR_INVALID_ARG for sizes, pointers, pitches or strides that break
  * these rules or too little scratch; DG_ERR_UNSUPPORTED for another type, more
  * than 1024 experts, more than 512 slots, more tokens than a CTA's shared
- * memory holds (72 bytes and 2 * (width rounded up to a multiple of 256) for each
- * token, 12 for each expert and 28 for each slot are at most 150 KiB, less 32),
+ * memory holds (68 bytes and 2 * (width rounded up to a multiple of 256) for each
+ * token, 12 for each expert and 24 for each slot are at most 150 KiB, less 16),
  * or SwiGLU on NVF4 weights with hidden not a multiple of 128. */
 int64_t dg_moe_layer_scratch(int64_t tokens, int64_t top_k, int64_t hidden, int64_t out);
 dg_status dg_moe_layer(int64_t tokens, int64_t top_k, int64_t count, int64_t width, int64_t hidden,

@@ -1191,7 +1191,7 @@ _layer_scratch = {}  # sizes -> dg_moe_layer_scratch
 
 def moe_layer(X, ids, weights, up, down, D, activation="gelu", bias_up=None, bias_down=None,
               stream=None):
-    """The expert layer of a few tokens in two kernels: D[t] = sum over j of
+    """The expert layer of a few tokens in three kernels: D[t] = sum over j of
     weights[t, j] * (W2[e] act(W1[e] X[t] + b1[e]) + b2[e]), e = ids[t, j].
 
     X: [tokens, width] float16 or bfloat16, D: [tokens, out] of its type; ids:

@@ -1,10 +1,11 @@
 // A whole mixture-of-experts layer for a few tokens (dg_moe_layer in dg.h) in
-// two kernels:
+// three kernels:
 //   up:    h[s] = act(W1[e] x_t + b1[e])    for each slot s = (t, j), e = ids[s]
-//   down:  y[t] = sum over j of weights[t,j] (W2[e] h[s] + b2[e])
+//   down:  z[s] = W2[e] h[s] + b2[e]
+//   sum:   y[t] = sum over j of weights[t,j] z[t,j]
 //
 // The job is to read the used experts' weights once, at the rate of HBM: 8-bit
-// codes (FP8) or 4-bit codes and their scales (NVF4).  Both kernels are the same
+// codes (FP8) or 4-bit codes and their scales (NVF4).  Up and down are the same
 // machine: a persistent CTA per SM takes units (32 weight rows of one expert, up
 // to 8 of its slots), one thread keeps a ring of loads in flight across units, 8
 // warps multiply with warp-level FP16 MMAs (m16n8k16, weights as the 16-row
@@ -29,10 +30,6 @@
 // sorted order, so that one bulk copy brings a unit's slots of a stage, values
 // and scales.  Few copies matter: a TMA copy costs the issuing thread about 80
 // clocks (with one for each K block and 8 rows, 990 clocks a stage).
-//
-// Slots' sums go to scratch, and whichever warp finishes the last slot of a token
-// (counted by atomics that the results do not depend on) adds them in the order
-// of j.
 #include <algorithm>
 
 #include "convert.cuh"
@@ -108,12 +105,8 @@ struct LayerParams {
   int x_pitch;               // bytes of a token in shared memory
   uint8_t* h;                // [K stage][slot][HRow]
   int h_stages;
-  float* part;               // slots' sums of the second product
-  unsigned* done;            // [tiles][tokens]: slots finished
-  int done_words;
-  const float* weights;
-  uint16_t* D;
-  int64_t ldd;
+  float* part;               // slots' sums of the second product, part_pitch apart
+  int64_t part_pitch;
   int stages, stage_bytes;
   int off_x, off_red, off_route;
   int* status;
@@ -123,10 +116,8 @@ struct LayerParams {
 // The routing in shared memory: slots sorted by expert (stable), cut into
 // chunks of at most `chunk` slots of one expert.
 struct Route {
-  int *pos, *token;          // slot -> sorted place (-1: dropped); sorted place -> token
+  int *pos, *of;             // slot -> sorted place (-1: dropped); sorted place -> token, or slot
   int *expert, *first, *n;   // per chunk
-  float* weight;             // per slot
-  int* valid;                // per token: its slots that are not dropped
   float* fx;                 // per token: what its values are multiplied by
   int* ids;
   int *cnt, *start, *base;   // per expert
@@ -136,13 +127,11 @@ __device__ __forceinline__ Route route_at(int* m, const LayerParams& p) {
   Route r;
   r.ids = m;
   r.pos = r.ids + (p.slots + 3) / 4 * 4;
-  r.token = r.pos + p.slots;
-  r.expert = r.token + p.slots;
+  r.of = r.pos + p.slots;
+  r.expert = r.of + p.slots;
   r.first = r.expert + p.slots;
   r.n = r.first + p.slots;
-  r.weight = reinterpret_cast<float*>(r.n + p.slots);
-  r.valid = r.n + 2 * p.slots;
-  r.fx = reinterpret_cast<float*>(r.valid + p.tokens);
+  r.fx = reinterpret_cast<float*>(r.n + p.slots);
   r.cnt = reinterpret_cast<int*>(r.fx + p.tokens);
   r.start = r.cnt + p.count;
   r.base = r.start + p.count;
@@ -150,7 +139,7 @@ __device__ __forceinline__ Route route_at(int* m, const LayerParams& p) {
   return r;
 }
 int route_bytes(int64_t slots, int64_t tokens, int64_t count) {
-  return static_cast<int>(4 * ((slots + 3) / 4 * 4 + 6 * slots + 2 * tokens + 3 * count + 4));
+  return static_cast<int>(4 * ((slots + 3) / 4 * 4 + 5 * slots + tokens + 3 * count + 1));
 }
 
 __device__ __forceinline__ void others_sync() {
@@ -158,13 +147,10 @@ __device__ __forceinline__ void others_sync() {
 }
 
 // Up to 32 slots: by one warp, a slot per lane, which has them without a barrier.
-// (The first kernel needs neither the routing weights nor the counts per token.)
+// (The first kernel wants sorted places' tokens, the second their slots.)
 template <bool Down>
 __device__ __forceinline__ void build_route_warp(const Route& r, const LayerParams& p, int lane) {
   int e = lane < p.slots ? __ldg(p.ids + lane) : -1;
-  if (Down && lane < p.slots) r.weight[lane] = p.weights ? __ldg(p.weights + lane) : 1.0f;
-  if (Down && lane < p.tokens) r.valid[lane] = 0;
-  __syncwarp();
   if (e >= p.count) e = -1;
   int less = 0, same = 0, before = 0;  // slots of smaller experts, of this one, and of those before
   for (int j = 0; j < p.slots; ++j) {
@@ -184,11 +170,7 @@ __device__ __forceinline__ void build_route_warp(const Route& r, const LayerPara
   }
   if (lane < p.slots) {
     r.pos[lane] = at;
-    if (there) {
-      const int t = lane / p.top_k;
-      r.token[at] = t;
-      if (Down) atomicAdd(&r.valid[t], 1);
-    }
+    if (there) r.of[at] = Down ? lane : lane / p.top_k;
   }
   if (starts) {
     r.expert[k] = e;
@@ -203,11 +185,9 @@ __device__ __forceinline__ void build_route_warp(const Route& r, const LayerPara
 template <bool Down>
 __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p, int i) {
   for (int e = i; e < p.count; e += kOtherThreads) r.cnt[e] = 0;
-  for (int t = i; Down && t < p.tokens; t += kOtherThreads) r.valid[t] = 0;
   for (int s = i; s < (p.slots + 3) / 4 * 4; s += kOtherThreads) {
     const int e = s < p.slots ? __ldg(p.ids + s) : -1;
     r.ids[s] = e >= 0 && e < p.count ? e : -1;
-    if (Down && s < p.slots) r.weight[s] = p.weights ? __ldg(p.weights + s) : 1.0f;
   }
   others_sync();
   for (int s = i; s < p.slots; s += kOtherThreads) {
@@ -222,7 +202,6 @@ __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p
                 (4 * k + 3 < s && w.w == e);
       }
       atomicAdd(&r.cnt[e], 1);  // counts: the order does not matter
-      if (Down) atomicAdd(&r.valid[s / p.top_k], 1);
     }
     r.pos[s] = rank;
   }
@@ -250,7 +229,7 @@ __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p
     if (r.ids[s] >= 0) {
       const int at = r.start[r.ids[s]] + r.pos[s];
       r.pos[s] = at;
-      r.token[at] = s / p.top_k;
+      r.of[at] = Down ? s : s / p.top_k;
     }
   for (int e = i; e < p.count; e += kOtherThreads) {
     const int c = r.cnt[e];
@@ -602,16 +581,6 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
     // The CTA's i-th unit is this warp's where i = mine modulo kEpiWarps; lane =
     // row of the tile.
     const int mine = warp - kEpiWarp;
-    const int first_word = (static_cast<int>(blockIdx.x) * kEpiWarps + mine) * 32 + lane;
-    if (Down) {
-      grid_dependency_wait();
-      // tokens without an expert
-      for (int t = 0; t < p.tokens; ++t)
-        if (r.valid[t] == 0)
-          for (int n = first_word; n < p.rows; n += step * kEpiWarps * 32) p.D[t * p.ldd + n] = 0;
-    } else {
-      for (int i = first_word; i < p.done_words; i += step * kEpiWarps * 32) p.done[i] = 0u;
-    }
     const float* all = red + mine * kMmaWarps * 4 * 32;
     uint32_t phase = 0;
     walk.start(blockIdx.x + mine * step, kEpiWarps * step, chunks);
@@ -646,7 +615,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
         const int ks = tile * kTileRows / H::kK, in_stage = tile * kTileRows % H::kK;
         for (int j = 0; j < n; ++j) {
           const int pos = first + j;
-          const float fx = r.fx[r.token[pos]];
+          const float fx = r.fx[r.of[pos]];
           float v = fmaf(total(0, j), of_row[0] * fx, bias[0]);
           if (Gated) {
             const float up = fmaf(total(1, j), of_row[1] * fx, bias[1]);
@@ -674,44 +643,10 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
       } else {
         for (int j = 0; j < n; ++j) {
           const float v = fmaf(total(0, j), of_row[0], bias[0]);
-          if (there) __stcg(p.part + static_cast<int64_t>(first + j) * p.rows + row, v);
+          if (there) p.part[r.of[first + j] * p.part_pitch + row] = v;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&red_empty[mine]);
-        __threadfence();
-        __syncwarp();
-        // slot j is lane j's to count; a token's last slot to be finished adds
-        // all of them, in order
-        int token = 0;
-        bool last = false;
-        if (lane < n) {
-          token = r.token[first + lane];
-          last = static_cast<int>(atomicAdd(
-                     p.done + static_cast<int64_t>(tile) * p.tokens + token, 1u)) ==
-                 r.valid[token] - 1;
-        }
-        unsigned todo = __ballot_sync(0xffffffffu, last);
-        if (todo) __threadfence();
-        while (todo) {
-          const int tok = __shfl_sync(0xffffffffu, token, __ffs(todo) - 1);
-          todo &= todo - 1;
-          if (!there) continue;
-          float y = 0.0f;
-          for (int j0 = 0; j0 < p.top_k; j0 += 8) {
-            float v[8], w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int s = tok * p.top_k + min(j0 + j, p.top_k - 1);
-              const int at = j0 + j < p.top_k ? r.pos[s] : -1;
-              w[j] = at >= 0 ? r.weight[s] : 0.0f;
-              v[j] = at >= 0 ? __ldcg(p.part + static_cast<int64_t>(at) * p.rows + row) : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y = fmaf(w[j], v[j], y);
-          }
-          p.D[tok * p.ldd + row] =
-              static_cast<uint16_t>(p.bf16 ? BF16::pack(y, 0.0f) : F16::pack(y, 0.0f));
-        }
       }
     }
     return;
@@ -756,7 +691,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
     const uint32_t b_base =
         Down ? smem0 + static_cast<uint32_t>(S::kW + S::kS + col * H::kBytes + slice * S::kBlockK * 2 +
                                              q * 16)
-             : smem_addr(xs) + static_cast<uint32_t>(r.token[first + col] * p.x_pitch + q * 16);
+             : smem_addr(xs) + static_cast<uint32_t>(r.of[first + col] * p.x_pitch + q * 16);
     const uint32_t h_base = smem0 + static_cast<uint32_t>(S::kW + S::kS + H::kScales +
                                                           slice * (S::kBlockK / 32) * 4);
     const uint32_t h0 = h_base + static_cast<uint32_t>(min(2 * q, n - 1) * H::kBytes);
@@ -915,11 +850,67 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
   }
 }
 
+// D[t,:] = the sum over j, in order, of weights[t,j] * part[t top_k + j,:] (choices
+// that are dropped have no part).  A kernel of its own: added by whichever unit of the
+// second product finished a token's last slot, a CTA that was late did the most of it
+// and got later (16 tokens, gated NVF4: the last was at it 30 us after the others).
+constexpr int kSumThreads = 128;
+struct SumParams {
+  const int32_t* ids;
+  const float* weights;
+  int top_k, count, out, bf16;
+  const float* part;
+  int64_t part_pitch;
+  uint16_t* D;
+  int64_t ldd;
+};
+__global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const __grid_constant__ SumParams p) {
+  const int n = (static_cast<int>(blockIdx.x) * kSumThreads + static_cast<int>(threadIdx.x)) * 2;
+  const int s0 = static_cast<int>(blockIdx.y) * p.top_k;
+  // (choices and weights were there before the layer's first kernel)
+  int e[8];
+  float w[8];
+  auto choices = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      e[j] = j0 + j < p.top_k ? __ldg(p.ids + s0 + j0 + j) : -1;
+      w[j] = p.weights && j0 + j < p.top_k ? __ldg(p.weights + s0 + j0 + j) : 1.0f;
+    }
+  };
+  choices(0);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (n >= p.out) return;
+  float2 y = make_float2(0.0f, 0.0f);
+  for (int j0 = 0;;) {
+    float2 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e[j] >= 0 && e[j] < p.count)
+        v[j] = __ldcg(reinterpret_cast<const float2*>(
+            p.part + (s0 + j0 + j) * p.part_pitch + n));
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e[j] >= 0 && e[j] < p.count) {
+        y.x = fmaf(w[j], v[j].x, y.x);
+        y.y = fmaf(w[j], v[j].y, y.y);
+      }
+    if ((j0 += 8) >= p.top_k) break;
+    choices(j0);
+  }
+  const uint32_t d = p.bf16 ? BF16::pack(y.x, y.y) : F16::pack(y.x, y.y);
+  uint16_t* to = p.D + blockIdx.y * p.ldd + n;
+  if (n + 1 < p.out)
+    *reinterpret_cast<uint32_t*>(to) = d;
+  else
+    *to = static_cast<uint16_t>(d);
+}
+
 constexpr int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
 // Where the scratch's parts lie.
 struct LayerScratch {
-  int64_t h, part, done, bytes;
+  int64_t h, part, bytes;
 };
 LayerScratch scratch_of(const MoeLayerArgs& a) {
   LayerScratch s;
@@ -929,8 +920,7 @@ LayerScratch scratch_of(const MoeLayerArgs& a) {
   const int64_t h4 = (a.hidden + HRow<kNvf4>::kK - 1) / HRow<kNvf4>::kK * HRow<kNvf4>::kBytes;
   s.h = 0;
   s.part = round_up(slots * std::max(h8, h4), 16);
-  s.done = s.part + round_up(slots * a.out * 4, 16);
-  s.bytes = s.done + round_up((a.out + kTileRows - 1) / kTileRows * a.tokens * 4, 16);
+  s.bytes = s.part + round_up(slots * round_up(a.out, 2) * 4, 16);
   return s;
 }
 
@@ -1037,6 +1027,17 @@ cudaError_t run_layer(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   return run_phase<Fmt, true, false, 1>(a, p, 0);
 }
 
+cudaError_t run_sum(const MoeLayerArgs& a, const LayerParams& p) {
+  const SumParams q = {p.ids,  a.weights, p.top_k,      p.count,
+                       static_cast<int>(a.out), a.bf16, p.part, p.part_pitch,
+                       static_cast<uint16_t*>(a.D), a.ldd};
+  const dim3 grid(static_cast<unsigned>((a.out + 2 * kSumThreads - 1) / (2 * kSumThreads)),
+                  static_cast<unsigned>(p.tokens));
+  const cudaError_t e = launch_dependent(moe_sum_kernel, grid, dim3(kSumThreads), 0, a.stream, q);
+  count_launches(1);
+  return e;
+}
+
 }  // namespace
 
 int64_t moe_layer_scratch(const MoeLayerArgs& a) { return scratch_of(a).bytes; }
@@ -1067,15 +1068,12 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a) {
   p.x_pitch = static_cast<int>(token_bytes(a));
   p.h = base + s.h;
   p.part = reinterpret_cast<float*>(base + s.part);
-  p.done = reinterpret_cast<unsigned*>(base + s.done);
-  p.done_words = static_cast<int>((a.out + kTileRows - 1) / kTileRows * a.tokens);
-  p.weights = a.weights;
-  p.D = static_cast<uint16_t*>(a.D);
-  p.ldd = a.ldd;
+  p.part_pitch = round_up(a.out, 2);
   p.status = a.status;
   p.timeout_ns = a.timeout_ns;
   const int x_bytes = static_cast<int>(a.tokens * token_bytes(a));
-  return a.nvf4 ? run_layer<kNvf4>(a, p, x_bytes) : run_layer<kFp8>(a, p, x_bytes);
+  const cudaError_t e = a.nvf4 ? run_layer<kNvf4>(a, p, x_bytes) : run_layer<kFp8>(a, p, x_bytes);
+  return e == cudaSuccess ? run_sum(a, p) : e;
 }
 
 }  // namespace dg

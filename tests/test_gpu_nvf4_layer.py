@@ -1,6 +1,6 @@
 """An expert layer on NVF4 weights by both ways: many tokens through the sort, the
 quantizing gather, the grouped products and the way back, each step against the
-oracle on what the step before it gave; a few through the two kernels; and the
+oracle on what the step before it gave; a few through the layer kernels; and the
 example's program for both."""
 
 import importlib.util
