@@ -44,7 +44,6 @@ using namespace fp8;
 
 constexpr int kTeamWarps = 8;  // that share a stage
 constexpr int kEpiWarps = 3;
-constexpr int kOtherThreads = (1 + kEpiWarps) * 32;  // they build the routing
 constexpr int kTileRows = 32;  // weight rows per unit (twice as many where gated)
 constexpr int kMaxChunk = 8;   // slots per unit
 constexpr int kMaxStages = 8;
@@ -64,7 +63,7 @@ template <int Fmt, bool Down, bool Gated, int Teams = 1>
 struct Shape {
   static constexpr int kMmaWarps = Teams * kTeamWarps;
   static constexpr int kTmaWarp = kMmaWarps, kEpiWarp = kMmaWarps + 1;
-  static constexpr int kThreads = kMmaWarps * 32 + kOtherThreads;
+  static constexpr int kThreads = (kMmaWarps + 1 + kEpiWarps) * 32;
   static constexpr int RG = Gated ? 4 : 2;
   static constexpr int kSlices = kTeamWarps / RG;
   static constexpr int kBlockK = Fmt == kFp8 ? 128 : 256;
@@ -89,6 +88,7 @@ struct HRow {
 struct LayerParams {
   const int32_t* ids;
   int tokens, top_k, slots, count, chunk;
+  int inv_chunk, inv_top_k;  // 2^16 / chunk, 2^20 / top_k, rounded up: for quotients of up to 519
   // the phase's product: K values (k_blocks of 128 bytes, full_blocks of them whole,
   // k_tiles scale tiles), `rows` results
   int K, k_blocks, full_blocks, k_tiles, rows, tiles, up0;
@@ -116,40 +116,39 @@ struct LayerParams {
 // The routing in shared memory: slots sorted by expert (stable), cut into
 // chunks of at most `chunk` slots of one expert.
 struct Route {
-  int *pos, *of;             // slot -> sorted place (-1: dropped); sorted place -> token, or slot
+  int* of;                   // sorted place -> token, or slot
   int *expert, *first, *n;   // per chunk
   float* fx;                 // per token: what its values are multiplied by
-  int* ids;
-  int *cnt, *start, *base;   // per expert
+  int *ids, *rank;           // per slot: expert; place among that expert's (-1: dropped)
+  int *cnt, *start;          // per expert: slots; of those before, slots and (<< 16) chunks
   int* chunks;               // their number
 };
 __device__ __forceinline__ Route route_at(int* m, const LayerParams& p) {
   Route r;
   r.ids = m;
-  r.pos = r.ids + (p.slots + 3) / 4 * 4;
-  r.of = r.pos + p.slots;
+  r.rank = r.ids + p.slots;
+  r.of = r.rank + p.slots;
   r.expert = r.of + p.slots;
   r.first = r.expert + p.slots;
   r.n = r.first + p.slots;
   r.fx = reinterpret_cast<float*>(r.n + p.slots);
   r.cnt = reinterpret_cast<int*>(r.fx + p.tokens);
   r.start = r.cnt + p.count;
-  r.base = r.start + p.count;
-  r.chunks = r.base + p.count;
+  r.chunks = r.start + p.count;
   return r;
 }
 int route_bytes(int64_t slots, int64_t tokens, int64_t count) {
-  return static_cast<int>(4 * ((slots + 3) / 4 * 4 + 5 * slots + tokens + 3 * count + 1));
+  return static_cast<int>(4 * (6 * slots + tokens + 2 * count + 1));
 }
 
-__device__ __forceinline__ void others_sync() {
-  asm volatile("bar.sync 2, %0;" ::"n"(kOtherThreads) : "memory");
-}
-
-// Up to 32 slots: by one warp, a slot per lane, which has them without a barrier.
-// (The first kernel wants sorted places' tokens, the second their slots.)
+// The routing is built by the warp that loads: only who multiplies and finishes sums
+// waits at a barrier for it.  What takes the time is the fetches of code that is in no
+// cache yet, so it is short, without a division.  (The first kernel wants sorted places'
+// tokens, the second their slots.)
+//
+// Up to 32 slots: a slot per lane.
 template <bool Down>
-__device__ __forceinline__ void build_route_warp(const Route& r, const LayerParams& p, int lane) {
+__device__ __forceinline__ void build_route_32(const Route& r, const LayerParams& p, int lane) {
   int e = lane < p.slots ? __ldg(p.ids + lane) : -1;
   if (e >= p.count) e = -1;
   int less = 0, same = 0, before = 0;  // slots of smaller experts, of this one, and of those before
@@ -161,17 +160,14 @@ __device__ __forceinline__ void build_route_warp(const Route& r, const LayerPara
   }
   const bool there = e >= 0;
   const int at = there ? less + before : -1;
-  const bool starts = there && before % p.chunk == 0;
+  const bool starts = there && (before * p.inv_chunk >> 16) * p.chunk == before;
   const unsigned all = __ballot_sync(0xffffffffu, starts);
   int k = 0;  // chunks before this slot's
   for (int j = 0; j < p.slots; ++j) {
     const int f = __shfl_sync(0xffffffffu, at, j);
     k += (all >> j & 1u) && f < at;
   }
-  if (lane < p.slots) {
-    r.pos[lane] = at;
-    if (there) r.of[at] = Down ? lane : lane / p.top_k;
-  }
+  if (there) r.of[at] = Down ? lane : lane * p.inv_top_k >> 20;
   if (starts) {
     r.expert[k] = e;
     r.first[k] = at;
@@ -181,65 +177,61 @@ __device__ __forceinline__ void build_route_warp(const Route& r, const LayerPara
   __syncwarp();
 }
 
-// More: by the threads that do not multiply, numbered i.
+// More: 32 slots at a time; a slot's rank is the number of its expert's slots in the
+// blocks before and in the lanes below.
 template <bool Down>
-__device__ __forceinline__ void build_route(const Route& r, const LayerParams& p, int i) {
-  for (int e = i; e < p.count; e += kOtherThreads) r.cnt[e] = 0;
-  for (int s = i; s < (p.slots + 3) / 4 * 4; s += kOtherThreads) {
-    const int e = s < p.slots ? __ldg(p.ids + s) : -1;
-    r.ids[s] = e >= 0 && e < p.count ? e : -1;
+__device__ __forceinline__ void build_route(const Route& r, const LayerParams& p, int lane) {
+#pragma unroll 4
+  for (int s = lane; s < p.slots; s += 32) r.ids[s] = __ldg(p.ids + s);
+#pragma unroll 1
+  for (int e = lane; e < p.count; e += 32) r.cnt[e] = 0;
+  __syncwarp();
+#pragma unroll 1
+  for (int s0 = 0; s0 < p.slots; s0 += 32) {
+    const int s = s0 + lane;
+    int e = s < p.slots ? r.ids[s] : -1;
+    if (e >= p.count) e = -1;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int below = __popc(same & ((1u << lane) - 1u));
+    const int before = e >= 0 ? r.cnt[e] : 0;
+    __syncwarp();
+    if (e >= 0 && below == 0) r.cnt[e] = before + __popc(same);
+    if (s < p.slots) r.rank[s] = e >= 0 ? before + below : -1;
+    __syncwarp();
   }
-  others_sync();
-  for (int s = i; s < p.slots; s += kOtherThreads) {
-    const int e = r.ids[s];
-    int rank = -1;
-    if (e >= 0) {
-      rank = 0;  // slots of this expert before s
-      const int4* v = reinterpret_cast<const int4*>(r.ids);
-      for (int k = 0; k <= s / 4; ++k) {
-        const int4 w = v[k];
-        rank += (4 * k < s && w.x == e) + (4 * k + 1 < s && w.y == e) + (4 * k + 2 < s && w.z == e) +
-                (4 * k + 3 < s && w.w == e);
-      }
-      atomicAdd(&r.cnt[e], 1);  // counts: the order does not matter
-    }
-    r.pos[s] = rank;
-  }
-  others_sync();
-  if (i < 32) {
-    int run = 0, run_c = 0;
-    for (int e0 = 0; e0 < p.count; e0 += 32) {
-      const int e = e0 + i;
-      const int c = e < p.count ? r.cnt[e] : 0, k = (c + p.chunk - 1) / p.chunk;
-      int v = c | k << 16;  // (at most 512 each)
+  int run = 0;  // slots and chunks of the experts before, at most 512 each
+#pragma unroll 1
+  for (int e0 = 0; e0 < p.count; e0 += 32) {
+    const int e = e0 + lane;
+    const int c = e < p.count ? r.cnt[e] : 0;
+    const int own = c | ((c + p.chunk - 1) * p.inv_chunk >> 16) << 16;
+    int v = own;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, v, d);
-        if (i >= d) v += a;
-      }
-      if (e < p.count) r.start[e] = run + (v & 0xFFFF) - c, r.base[e] = run_c + (v >> 16) - k;
-      const int last = __shfl_sync(0xffffffffu, v, 31);
-      run += last & 0xFFFF;
-      run_c += last >> 16;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += a;
     }
-    if (i == 0) *r.chunks = run_c;
+    if (e < p.count) r.start[e] = run + v - own;
+    run += __shfl_sync(0xffffffffu, v, 31);
   }
-  others_sync();
-  for (int s = i; s < p.slots; s += kOtherThreads)
-    if (r.ids[s] >= 0) {
-      const int at = r.start[r.ids[s]] + r.pos[s];
-      r.pos[s] = at;
-      r.of[at] = Down ? s : s / p.top_k;
-    }
-  for (int e = i; e < p.count; e += kOtherThreads) {
-    const int c = r.cnt[e];
-    for (int at = 0, k = r.base[e]; at < c; at += p.chunk, ++k) {
-      r.expert[k] = e;
-      r.first[k] = r.start[e] + at;
-      r.n[k] = min(p.chunk, c - at);
+  if (lane == 0) *r.chunks = run >> 16;
+  __syncwarp();
+#pragma unroll 1
+  for (int s = lane; s < p.slots; s += 32) {
+    const int rank = r.rank[s];
+    if (rank < 0) continue;
+    const int e = r.ids[s], base = r.start[e];
+    const int at = (base & 0xFFFF) + rank;
+    r.of[at] = Down ? s : s * p.inv_top_k >> 20;
+    const int k = rank * p.inv_chunk >> 16;
+    if (k * p.chunk == rank) {
+      const int u = (base >> 16) + k;
+      r.expert[u] = e;
+      r.first[u] = at;
+      r.n[u] = min(p.chunk, r.cnt[e] - rank);
     }
   }
-  others_sync();
+  __syncwarp();
 }
 
 // A CTA's units, chunk by chunk of a tile (neighbours share a tile's place in
@@ -248,9 +240,10 @@ struct UnitWalk {
   int tile, u, chunks, d_tile, d_u;
   __device__ __forceinline__ void start(int first, int step, int chunks_) {
     chunks = max(chunks_, 1);
-    tile = first / chunks;
+    // (exact below 2^21: the quotient of a + 1/2 is half a chunk's part off an integer)
+    tile = static_cast<int>(__fdividef(first + 0.5f, chunks));
     u = first - tile * chunks;
-    d_tile = step / chunks;
+    d_tile = static_cast<int>(__fdividef(step + 0.5f, chunks));
     d_u = step - d_tile * chunks;
   }
   __device__ __forceinline__ void next() {
@@ -475,9 +468,9 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
   bool ok = true;
   if (warp == 0 && !Down && elect_one_lane()) copy_tokens(p, xs, x_bar);
   if (p.slots <= 32) {
-    if (warp == kTmaWarp) build_route_warp<Down>(r, p, lane);
-  } else if (warp >= kMmaWarps) {
-    build_route<Down>(r, p, static_cast<int>(threadIdx.x) - kMmaWarps * 32);
+    if (warp == kTmaWarp) build_route_32<Down>(r, p, lane);
+  } else {
+    if (warp == kTmaWarp) build_route<Down>(r, p, lane);
   }
   if (!Down && warp < kMmaWarps) ok = convert_tokens<Fmt, kMmaWarps>(p, xs, r, x_bar, warp, lane);
   // the routing and the tokens are there; who loads needs only the first, which
@@ -983,14 +976,21 @@ cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
 
   CUtensorMap tw{}, tt{}, ts{};
   const int64_t all_rows = (a.count - 1) * pitch + n_rows;
-  cudaError_t e = tc::encode_map_2d(&tt, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, all_rows, bytes_k,
-                                    w.ld, kTileRows, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
-  tw = ts = tt;  // not used without whole blocks, or by FP8
-  if (p.full_blocks > 0) {
+  cudaError_t e = cudaSuccess;
+  const bool whole = p.full_blocks >= S::kSlices;  // some stages' blocks
+  if (whole) {
     e = weights_map(&tw, w, all_rows, p.full_blocks, S::kSlices);
     if (e != cudaSuccess) return e;
   }
+  if (!whole || p.full_blocks < p.k_blocks || p.k_blocks % S::kSlices != 0) {
+    e = tc::encode_map_2d(&tt, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, all_rows, bytes_k, w.ld,
+                          kTileRows, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+  } else {
+    tt = tw;  // not used
+  }
+  if (!whole) tw = tt;
+  ts = tw;  // not used by FP8
   if (Fmt == kNvf4) {
     e = tc::encode_map_2d(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT32, w.scales,
                           static_cast<int64_t>(p.sf_rows) * p.k_tiles * a.count, 128, 512,
@@ -1062,6 +1062,8 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a) {
   // Slots per unit: as many as there are tokens can meet in one expert (a token
   // that names an expert twice gets a unit more), at most an MMA's columns.
   p.chunk = static_cast<int>(std::min<int64_t>(a.tokens, kMaxChunk));
+  p.inv_chunk = (65536 + p.chunk - 1) / p.chunk;
+  p.inv_top_k = ((1 << 20) + p.top_k - 1) / p.top_k;
   p.bf16 = a.bf16;
   p.X = static_cast<const uint16_t*>(a.X);
   p.ldx = a.ldx;
