@@ -645,14 +645,27 @@ cudaError_t run_nvf4(const Nvf4Args& a) {
 
 }  // namespace
 
+// Which tile.  A stage takes a unit 0.34 us with 256 x 192 (pairs: half as many units),
+// 0.30 with 128 x 128 and 0.29 with 128 x 64 (the scales' copies and the rows of A cost
+// the same for fewer columns), so what counts is the number of rounds of tiles, weighted
+// by that.  In us, pairs / 128 / 64:
+//   16 x 8192 x 8192   19.4 / 13.8 / 13.3      256 x 4096 x 4096   10.8 / 9.2 / 8.5
+//   256 x 8192 x 8192  17.0 / 14.8 / 22.6      1024 x 8192 x 8192  37.6 / 42.7 / 69.5
+//   1024 x 4096 x 4096 16.9 / 14.4 / 23.2      2048 x 4096 x 4096  22.7 / 24.4 / 38.1
+// Experts' row blocks are known on the device only, and a pair's second half is often
+// empty: pairs from 512 rows per expert, of those that the caller makes room for (64
+// experts, 4096 x 2048; 383 rows 119 / 113, 639 rows 185 / 187).
 cudaError_t launch_gemm_nvf4(const Nvf4Args& a) {
   const bool grouped = a.offsets != nullptr;
-  const int64_t rows = grouped ? a.M / std::max<int64_t>(1, a.count) : a.M;
-  if (rows >= 256)
+  auto cost = [&](int64_t row_blocks, int64_t cols, int64_t units, int64_t weight) {
+    return (row_blocks * ((a.N + cols - 1) / cols) + units - 1) / units * weight;
+  };
+  const int64_t blocks = grouped ? a.M / 128 + std::min(a.count, a.M) : (a.M + 127) / 128;
+  const int64_t c128 = cost(blocks, 128, a.sm_count, 30), c64 = cost(blocks, 64, a.sm_count, 29);
+  if (grouped ? a.M >= 512 * a.count
+              : cost((a.M + 255) / 256, 192, a.sm_count / 2, 34) < std::min(c128, c64))
     return grouped ? run_nvf4<true, 192, 4, 2>(a) : run_nvf4<false, 192, 5, 2>(a);
-  const int64_t row_blocks = grouped ? a.M / 128 + std::min(a.count, a.M) : (a.M + 127) / 128;
-  if (row_blocks * ((a.N + 127) / 128) >= a.sm_count)
-    return grouped ? run_nvf4<true, 128, 5, 1>(a) : run_nvf4<false, 128, 5, 1>(a);
+  if (c128 < c64) return grouped ? run_nvf4<true, 128, 5, 1>(a) : run_nvf4<false, 128, 5, 1>(a);
   return grouped ? run_nvf4<true, 64, 6, 1>(a) : run_nvf4<false, 64, 6, 1>(a);
 }
 

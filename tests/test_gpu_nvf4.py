@@ -342,3 +342,52 @@ def test_graph_and_streams(dg):
     dg.gemm_nvf4(*out, *b, d, stream=s)
     s.synchronize()
     check(d, t, err, "f32")
+
+
+# ------------------------------------- enough tiles for pairs of 256 x 192
+@pytest.mark.parametrize("M,N,K,dtype,epilogue", [(1000, 2900, 200, "bf16", "none"),
+                                                  (1024, 2880, 256, "f16", "bias"),
+                                                  (1025, 2881, 777, "f32", "bias_gelu"),
+                                                  (897, 2913, 64, "bf16", "bias_gelu"),
+                                                  (2100, 1500, 1, "f16", "none")])
+def test_pairs(dg, M, N, K, dtype, epilogue):
+    a, av = operand(M, K, 60, pad=16)
+    b, bv = operand(N, K, 61, scale=K ** -0.5)
+    rng = np.random.default_rng(62)
+    d = torch.from_numpy(rng.normal(size=(M, N))).to(TYPES[dtype])
+    bias = torch.from_numpy(rng.normal(size=N)).to(TYPES[dtype])
+    t, err = ref.product(av, bv, 1.25, -0.5, d.double().numpy(),
+                         bias.double().numpy() if "bias" in epilogue else None, "gelu" in epilogue)
+    wide = torch.full((M + 3, N + 5), 3.0, dtype=TYPES[dtype], device="cuda")
+    wide[:M, :N] = d.cuda()
+    check(dg.gemm_nvf4(*a, *b, wide[:M, :N], bias=bias.cuda(), alpha=1.25, beta=-0.5,
+                       epilogue=epilogue), t, err, dtype)
+    assert (wide[:, N:] == 3.0).all() and (wide[M:] == 3.0).all()
+    aligned = torch.empty(M, (N + 7) // 8 * 8, dtype=TYPES[dtype], device="cuda")[:, :N]
+    aligned.copy_(d)
+    dg.gemm_nvf4(*a, *b, aligned, bias=bias.cuda(), alpha=1.25, beta=-0.5, epilogue=epilogue)
+    assert torch.equal(aligned, wide[:M, :N])
+    dg.check_status()
+
+
+def test_pairs_nan_scales_stay_in_their_row(dg):
+    M, N, K = 1000, 2900, 320  # K: five scale tiles, and NaN behind the last
+    a, av = operand(M, K, 63)
+    b, bv = operand(N, K, 64)
+    room = torch.full((b[1].numel() + 4096,), 0x7F, dtype=torch.uint8, device="cuda")
+    room[:b[1].numel()] = b[1].view(torch.uint8).reshape(-1)
+    b = (b[0], room[:b[1].numel()].view(torch.float8_e4m3fn).reshape(b[1].shape), b[2])
+    a[1].view(torch.uint8)[3, 2, 5, 1] = 0x7F  # row 389, block 9
+    b[1].view(torch.uint8)[22, 0, 31, 4] = 0x7F  # row 2879, block 0
+    t, err = ref.product(av, bv)
+    d = dg.gemm_nvf4(*a, *b, torch.zeros(M, N, device="cuda"))
+    nan = torch.isnan(d)
+    assert nan[389].all() and nan[:, 2879].all() and nan.sum() == M + N - 1
+    keep = ~nan.cpu().numpy()
+    assert (np.abs(d.double().cpu().numpy() - t) <= fp8_ref.rounded_bound(t, err, "f32"))[keep].all()
+
+
+@pytest.mark.parametrize("sizes,N,K", [([600, 700, 900], 200, 300), ([1, 1500, 0, 900], 400, 512),
+                                       ([129, 2000], 392, 64)])
+def test_grouped_pairs(dg, sizes, N, K):
+    test_grouped(dg, sizes, N, K)
