@@ -391,3 +391,38 @@ def test_pairs_nan_scales_stay_in_their_row(dg):
                                        ([129, 2000], 392, 64)])
 def test_grouped_pairs(dg, sizes, N, K):
     test_grouped(dg, sizes, N, K)
+
+
+def test_grouped_pairs_of_many_experts(dg):
+    # more experts than a fifth stage leaves room for, and most of the rows in none
+    count, N, K = 250, 40, 48
+    rng = np.random.default_rng(65)
+    sizes = rng.integers(0, 3, count) * 128
+    ends = np.cumsum(np.concatenate([[0], sizes]))
+    rows = 512 * count
+    a, av = operand(rows, K, 66)
+    b, bv = operand(count * N, K, 67)
+    b3 = (b[0].reshape(count, N, -1).contiguous(),
+          gpu(np.stack([ref.tiles(s) for s in untiled(b[1], count * N, K).reshape(count, N, -1)])),
+          b[2].reshape(count, N))
+    room = torch.zeros(count, N, 32, dtype=torch.uint8, device="cuda")
+    room[:, :, :K // 2] = b3[0]
+    d = torch.full((rows, N), 9.0, device="cuda")
+    dg.gemm_nvf4_grouped(*a, room[:, :, :K // 2], b3[1].view(torch.float8_e4m3fn), b3[2],
+                         gpu(ends.astype(np.int32)), d)
+    dg.check_status()
+    bv = bv.reshape(count, N, K)
+    for e in range(count):
+        at = slice(ends[e], ends[e + 1])
+        if ends[e + 1] > ends[e]:
+            t, err = ref.product(av[at], bv[e])
+            check(d[at], t, err, "f32")
+    assert (d[ends[-1]:] == 9.0).all()
+
+
+def untiled(scales, rows, K):
+    """The scale codes [rows, blocks] of tiles (numpy)."""
+    t = scales.view(torch.uint8).cpu().numpy()
+    m, k = t.shape[:2]
+    full = t.reshape(m, k, 32, 4, 4).transpose(0, 3, 2, 1, 4).reshape(m * 128, k * 4)
+    return full[:rows, :-(-K // 16)]
