@@ -18,9 +18,10 @@
 //   warps 4 ..   epilogue, 64 columns x 32 rows each, from one of two
 //                accumulators while the next tile is multiplied.
 //
-// CG = 2: CTA pairs on 256 x BN tiles, half of B's rows each.  An MMA of 128 x
-// 192 x 64 takes about 100 clocks and its operands 5 KB per CTA alone: what
-// bounds large products is the way from L2, and a pair halves B's share.
+// CG = 2: CTA pairs on 256 x BN tiles, half of B's rows each, which halves B's
+// share of the way from L2.  What bounds large products (8192^3 204 us; its MMAs
+// alone, at four times the 16-bit rate, 143): MMAs and scale copies go through one
+// queue (without the copies 173 us), and the operands from L2 alone take 156.
 //
 // Persistent: unit u (a CTA or a pair) takes tiles u, u + units, ...  Experts'
 // rows are read from the device's offsets, multiples of 128 as the scale tiles
