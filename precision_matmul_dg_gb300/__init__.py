@@ -1009,28 +1009,34 @@ def nvf4_buffers(*shape, device="cuda"):
 
 
 def _nvf4_operand(torch, codes, scales, row_scales, what, K=None):
-    """(row stride, matrix stride) of the codes of an NVF4 matrix or stack."""
+    """(row stride, matrix stride, shape) of the codes of an NVF4 matrix or stack."""
     s, shape = codes.stride(), codes.shape
     dim = len(s)
-    rows, width = shape[-2:] if dim in (2, 3) else (0, 0)
-    of = K or 2 * width
-    tiles = ((rows + 127) // 128, (of + 63) // 64, 32, 16)
-    lead = () if dim == 2 else (shape[0],)
+    if dim == 2:
+        rows, width = shape
+        of = K or 2 * width
+        tiles, each = ((rows + 127) // 128, (of + 63) // 64, 32, 16), (rows,)
+    elif dim == 3:
+        count, rows, width = shape
+        of = K or 2 * width
+        tiles = (count, (rows + 127) // 128, (of + 63) // 64, 32, 16)
+        each = (count, rows)
+    else:
+        raise ValueError("%s must be 2-D or 3-D" % what)
     if not (codes.dtype is torch.uint8 and scales.dtype is torch.float8_e4m3fn and
-            row_scales.dtype is torch.float32 and (dim == 2 or dim == 3) and s[-1] == 1 and
-            width == (of + 1) // 2 and scales.shape == lead + tiles and
-            row_scales.shape == lead + (rows,) and scales.is_contiguous() and
+            row_scales.dtype is torch.float32 and s[-1] == 1 and width == (of + 1) // 2 and
+            scales.shape == tiles and row_scales.shape == each and scales.is_contiguous() and
             row_scales.is_contiguous() and codes.is_cuda and scales.is_cuda and
             row_scales.is_cuda):
         # what is wrong
-        _rows(codes, torch.uint8, what, None, dim if dim in (2, 3) else 2)
+        _rows(codes, torch.uint8, what, None, dim)
         if width != (of + 1) // 2:
             raise ValueError("%s must have rows of %d bytes, got %d" % (what, (of + 1) // 2, width))
-        _rows(scales, torch.float8_e4m3fn, "the scales of " + what, lead + tiles, dim + 2)
-        _rows(row_scales, torch.float32, "the row scales of " + what, lead + (rows,), dim - 1)
+        _rows(scales, torch.float8_e4m3fn, "the scales of " + what, tiles, dim + 2)
+        _rows(row_scales, torch.float32, "the row scales of " + what, each, dim - 1)
         if not (scales.is_contiguous() and row_scales.is_contiguous()):
             raise ValueError("the scales of %s must be contiguous" % what)
-    return (s[-2] if rows > 1 else (width + 15) // 16 * 16), s[0]
+    return (s[-2] if rows > 1 else (width + 15) // 16 * 16), s[0], shape
 
 
 def _pitch(stride, rows, width, multiple):
@@ -1046,20 +1052,20 @@ def quantize_nvf4(X, row_scales=None, out=None, stream=None):
     given, its third is not used and may be None."""
     torch = (_FP or _fp())[0]
     code = _float_code(X, "X")
-    dim = X.dim()
+    shape = X.shape
+    dim = len(shape)
     sx = _rows(X, X.dtype, "X", None, dim if dim in (2, 3) else 2)
-    rows, K = X.shape[-2:]
-    codes, scales, found = nvf4_buffers(*X.shape, device=X.device) if out is None else out
+    rows, K = shape[-2], shape[-1]
+    codes, scales, found = nvf4_buffers(*shape, device=X.device) if out is None else out
     if row_scales is not None:
         found = row_scales
-    ldq, stride_q = _nvf4_operand(torch, codes, scales, found, "out", K)
-    if codes.shape[:-1] != X.shape[:-1]:
-        raise ValueError("out is for %s rows, X has %s" % (
-            tuple(codes.shape[:-1]), tuple(X.shape[:-1])))
+    ldq, stride_q, room = _nvf4_operand(torch, codes, scales, found, "out", K)
+    if len(room) != dim or room[-2] != rows or room[0] != shape[0]:
+        raise ValueError("out is for %s rows, X has %s" % (tuple(room[:-1]), tuple(shape[:-1])))
     _check(lib().dg_quantize_nvf4(
-        X.shape[0] if dim == 3 else 1, rows, K, code, X.data_ptr(),
-        _pitch(sx[-2], rows, K, 8), sx[0] if dim == 3 else 0, None if row_scales is None else row_scales.data_ptr(),
-        codes.data_ptr(), ldq, stride_q, scales.data_ptr(),
+        shape[0] if dim == 3 else 1, rows, K, code, X.data_ptr(),
+        _pitch(sx[-2], rows, K, 8), sx[0] if dim == 3 else 0,
+        None if row_scales is None else row_scales.data_ptr(), codes.data_ptr(), ldq, stride_q, scales.data_ptr(),
         found.data_ptr() if row_scales is None else None,
         _stream_of(stream, X, codes, scales, found)))
     return codes, scales, found
@@ -1074,8 +1080,8 @@ def moe_dispatch_nvf4(X, row_slot, top_k, codes, scales, row_scales, stream=None
     tokens, width = X.shape
     rows = row_slot.shape[0]
     _rows(row_slot, torch.int32, "row_slot", None, 1)
-    ldq, _ = _nvf4_operand(torch, codes, scales, row_scales, "codes", width)
-    if codes.shape != (rows, (width + 1) // 2):
+    ldq, _, room = _nvf4_operand(torch, codes, scales, row_scales, "codes", width)
+    if room != (rows, (width + 1) // 2):
         raise ValueError("codes must be [%d, %d]" % (rows, (width + 1) // 2))
     _check(lib().dg_moe_dispatch_nvf4(
         tokens, top_k, width, code, X.data_ptr(), _pitch(sx[0], tokens, width, 8), rows,
@@ -1089,15 +1095,15 @@ def dequantize_nvf4(codes, scales, row_scales, D, stream=None):
     matrix or stack holds."""
     torch = (_FP or _fp())[0]
     dt = _float_code(D, "D", (F16, BF16, F32))
-    dim = D.dim()
+    shape = D.shape
+    dim = len(shape)
     sd = _rows(D, D.dtype, "D", None, dim if dim in (2, 3) else 2)
-    rows, K = D.shape[-2:]
-    ldq, stride_q = _nvf4_operand(torch, codes, scales, row_scales, "codes", K)
-    if codes.shape[:-1] != D.shape[:-1]:
-        raise ValueError("codes have %s rows, D %s" % (
-            tuple(codes.shape[:-1]), tuple(D.shape[:-1])))
+    rows, K = shape[-2], shape[-1]
+    ldq, stride_q, held = _nvf4_operand(torch, codes, scales, row_scales, "codes", K)
+    if len(held) != dim or held[-2] != rows or held[0] != shape[0]:
+        raise ValueError("codes have %s rows, D %s" % (tuple(held[:-1]), tuple(shape[:-1])))
     _check(lib().dg_dequantize_nvf4(
-        D.shape[0] if dim == 3 else 1, rows, K, codes.data_ptr(), ldq, stride_q,
+        shape[0] if dim == 3 else 1, rows, K, codes.data_ptr(), ldq, stride_q,
         scales.data_ptr(), row_scales.data_ptr(), D.data_ptr(), dt, _pitch(sd[-2], rows, K, 1),
         sd[0] if dim == 3 else 0, _stream_of(stream, codes, scales, row_scales, D)))
     return D
@@ -1111,19 +1117,18 @@ def gemm_nvf4(A, scale_a, row_a, B, scale_b, row_b, D, bias=None, alpha=1.0, bet
     bfloat16 or float32; bias: [N] of D's type.
     """
     torch = (_FP or _fp())[0]
-    lda, _ = _nvf4_operand(torch, A, scale_a, row_a, "A")
-    ldb, _ = _nvf4_operand(torch, B, scale_b, row_b, "B")
+    lda, _, of_a = _nvf4_operand(torch, A, scale_a, row_a, "A")
+    ldb, _, of_b = _nvf4_operand(torch, B, scale_b, row_b, "B")
     dt = _float_code(D, "D", (F16, BF16, F32))
     sd = _rows(D, D.dtype, "D")
     M, N = D.shape
-    if A.dim() != 2 or B.dim() != 2 or A.shape[0] != M or B.shape[0] != N or \
-            A.shape[1] != B.shape[1]:
+    if len(of_a) != 2 or len(of_b) != 2 or of_a[0] != M or of_b[0] != N or of_a[1] != of_b[1]:
         raise ValueError("shape mismatch: A %s, B %s, D %s" % tuple(
             tuple(t.shape) for t in (A, B, D)))
     if bias is not None:
         _rows(bias, D.dtype, "bias", (N,), 1)
     _check(lib().dg_gemm_nvf4(
-        M, N, 2 * A.shape[1], A.data_ptr(), lda, scale_a.data_ptr(), row_a.data_ptr(),
+        M, N, 2 * of_a[1], A.data_ptr(), lda, scale_a.data_ptr(), row_a.data_ptr(),
         B.data_ptr(), ldb, scale_b.data_ptr(), row_b.data_ptr(), D.data_ptr(), dt,
         _pitch(sd[0], M, N, 1),
         None if bias is None else bias.data_ptr(), alpha, beta, _epi_code(epilogue),
@@ -1141,22 +1146,21 @@ def gemm_nvf4_grouped(A, scale_a, row_a, B, scale_b, row_b, offsets, D, bias=Non
     D's type.
     """
     torch = (_FP or _fp())[0]
-    lda, _ = _nvf4_operand(torch, A, scale_a, row_a, "A")
-    ldb, stride_b = _nvf4_operand(torch, B, scale_b, row_b, "B")
+    lda, _, of_a = _nvf4_operand(torch, A, scale_a, row_a, "A")
+    ldb, stride_b, of_b = _nvf4_operand(torch, B, scale_b, row_b, "B")
     dt = _float_code(D, "D", (F16, BF16, F32))
     sd = _rows(D, D.dtype, "D")
     rows, N = D.shape
-    if A.dim() != 2 or B.dim() != 3 or A.shape[0] != rows or B.shape[1] != N or \
-            A.shape[1] != B.shape[2]:
+    if len(of_a) != 2 or len(of_b) != 3 or of_a[0] != rows or of_b[1] != N or of_a[1] != of_b[2]:
         raise ValueError("shape mismatch: A %s, B %s, D %s" % tuple(
             tuple(t.shape) for t in (A, B, D)))
-    count = B.shape[0]
+    count = of_b[0]
     _rows(offsets, torch.int32, "offsets", (count + 1,), 1)
     stride_bias = 0
     if bias is not None:
         stride_bias = _rows(bias, D.dtype, "bias", (count, N))[0]
     _check(lib().dg_gemm_nvf4_grouped(
-        count, rows, N, 2 * A.shape[1], A.data_ptr(), lda, scale_a.data_ptr(), row_a.data_ptr(),
+        count, rows, N, 2 * of_a[1], A.data_ptr(), lda, scale_a.data_ptr(), row_a.data_ptr(),
         B.data_ptr(), ldb, stride_b, scale_b.data_ptr(), row_b.data_ptr(), offsets.data_ptr(),
         D.data_ptr(), dt, _pitch(sd[0], rows, N, 1), None if bias is None else bias.data_ptr(),
         stride_bias, alpha, beta, _epi_code(epilogue),
@@ -1165,25 +1169,25 @@ def gemm_nvf4_grouped(A, scale_a, row_a, B, scale_b, row_b, offsets, D, bias=Non
 
 
 def _moe_weights(torch, w, bias, dtype, what):
-    """MoeWeights of one product's weights."""
+    """MoeWeights of one product's weights, and the shape of their codes."""
     codes, scales = w[0], w[1]
     if len(w) == 3:
-        ld, stride = _nvf4_operand(torch, codes, scales, w[2], what)
-        if codes.dim() != 3:
+        ld, stride, shape = _nvf4_operand(torch, codes, scales, w[2], what)
+        if len(shape) != 3:
             raise ValueError("%s must be a stack of matrices" % what)
         m = MoeWeights(codes.data_ptr(), ld, stride, scales.data_ptr(), 0, 0, w[2].data_ptr())
     else:
         s, z = _fp8_operand(torch, codes, scales, what, 3)
-        count, n, k = codes.shape
+        shape = count, n, k = codes.shape
         if scales.shape[0] != count or scales.shape[1] != (n + 127) // 128 or \
                 scales.shape[2] < (k + 127) // 128:
             raise ValueError("shape mismatch: %s %s with %s" % (
                 what, tuple(codes.shape), tuple(scales.shape)))
         m = MoeWeights(codes.data_ptr(), s[1], s[0], scales.data_ptr(), z[1], z[0])
     if bias is not None:
-        m.stride_bias = _rows(bias, dtype, "the bias of " + what, codes.shape[:2])[0]
+        m.stride_bias = _rows(bias, dtype, "the bias of " + what, shape[:2])[0]
         m.bias = bias.data_ptr()
-    return m
+    return m, shape
 
 
 _layer_scratch = {}  # sizes -> dg_moe_layer_scratch
@@ -1207,11 +1211,12 @@ def moe_layer(X, ids, weights, up, down, D, activation="gelu", bias_up=None, bia
     sx = _rows(X, dtype, "X")
     tokens, width = X.shape
     _rows(ids, torch.int32, "ids")
-    top_k = ids.shape[1]
+    of_ids, of_d = ids.shape, D.shape
+    top_k = of_ids[1]
     sd = _rows(D, dtype, "D")
-    out = D.shape[1]
+    out = of_d[1]
     if weights is not None:
-        _rows(weights, torch.float32, "weights", ids.shape)
+        _rows(weights, torch.float32, "weights", of_ids)
         if not weights.is_contiguous():
             raise ValueError("weights must be contiguous")
     if not ids.is_contiguous():
@@ -1222,13 +1227,12 @@ def moe_layer(X, ids, weights, up, down, D, activation="gelu", bias_up=None, bia
     nvf4 = len(up) == 3
     if len(up) != len(down) or len(up) not in (2, 3):
         raise ValueError("up and down are both (codes, scales) or (codes, scales, row scales)")
-    w1 = _moe_weights(torch, up, bias_up, dtype, "up")
-    w2 = _moe_weights(torch, down, bias_down, dtype, "down")
-    count, n1, k1 = up[0].shape
+    w1, (count, n1, k1) = _moe_weights(torch, up, bias_up, dtype, "up")
+    w2, of_down = _moe_weights(torch, down, bias_down, dtype, "down")
     hidden = n1 // 2 if gated else n1
-    if ids.shape[0] != tokens or D.shape[0] != tokens or (gated and n1 % 2) or \
+    if of_ids[0] != tokens or of_d[0] != tokens or (gated and n1 % 2) or \
             k1 != ((width + 1) // 2 if nvf4 else width) or \
-            down[0].shape != (count, out, (hidden + 1) // 2 if nvf4 else hidden):
+            of_down != (count, out, (hidden + 1) // 2 if nvf4 else hidden):
         raise ValueError("shape mismatch: X %s, ids %s, up %s, down %s, D %s" % tuple(
             tuple(t.shape) for t in (X, ids, up[0], down[0], D)))
     if _gpus != 1:

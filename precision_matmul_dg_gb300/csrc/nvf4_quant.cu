@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, Given ? 3 : 4)
         if (d < tpr) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
       if (tpr > 32) {
         if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = most;
-        __syncthreads();
+        // the row's own barrier (with the CTA's, 8191 x 4096 took 0.7 us longer)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (threadIdx.x >> p.log2_tpr)), "r"(tpr) : "memory");
         const int first = (threadIdx.x >> 5) & ~((tpr >> 5) - 1);
         for (int i = 0; i < tpr >> 5; ++i) most = max(most, red[turn][first + i]);
         turn ^= 1;  // (a buffer is written again only after the next barrier)
