@@ -970,7 +970,10 @@ cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   const int fixed = static_cast<int>(round_up(x_bytes, 16)) + S::kRed + 256 + route + 1024;
   constexpr int kMaxSmem = Teams == 1 ? 113 * 1024 : 227 * 1024;
   p.stages = std::min(kMaxStages, (kMaxSmem - fixed) / stage);
-  if (Teams == 1 && p.stages < 3) return run_phase<Fmt, Down, Gated, 2>(a, p, x_bytes);
+  // (FP8's second product has three stages whatever the sizes)
+  if constexpr (Teams == 1 && !(Fmt == kFp8 && Down)) {
+    if (p.stages < 3) return run_phase<Fmt, Down, Gated, 2>(a, p, x_bytes);
+  }
   // two teams: a slot of the ring is one team's, whose waits then see its every phase
   if (Teams == 2) p.stages &= ~1;
   if (p.stages < 2) return cudaErrorInvalidValue;

@@ -287,3 +287,31 @@ def test_largest_tokens_by_width(dg, fmt):
     more = Case(fmt, fits + 2, 1, 4, width, 64, 40, "bf16", seed=14)
     with pytest.raises(dg.DgError, match="shared memory"):
         more.run(dg)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tokens,top_k,count,width,hidden,out,dtype,gated", [
+    (5, 2, 3, 8500, 128, 48, "bf16", True),
+    (1, 2, 3, 17000, 40, 24, "f16", False),
+    (2, 2, 3, 64, 17000, 40, "bf16", False),
+    (9, 1, 2, 72, 16900, 33, "f16", False),
+])
+def test_long_rows(dg, fmt, tokens, top_k, count, width, hidden, out, dtype, gated):
+    # more stages of K than a lane each holds the weight scales of
+    c = Case(fmt, tokens, top_k, count, width, hidden, out, dtype, gated, seed=hidden)
+    c.run(dg)
+    dg.check_status()
+    c.check()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tokens,top_k", [(1, 512), (240, 2), (33, 1), (16, 2), (11, 3), (170, 3)])
+def test_slots(dg, fmt, tokens, top_k):
+    # up to 32 slots and more, of one expert and of many
+    rng = np.random.default_rng(tokens)
+    for count in (1, 3, 40):
+        ids = rng.integers(-1 if count > 1 else 0, count, (tokens, top_k))
+        c = Case(fmt, tokens, top_k, count, 40, 64, 24, "f16", ids=ids, seed=count)
+        c.run(dg)
+        c.check()
+    dg.check_status()

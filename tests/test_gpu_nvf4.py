@@ -426,3 +426,26 @@ def untiled(scales, rows, K):
     m, k = t.shape[:2]
     full = t.reshape(m, k, 32, 4, 4).transpose(0, 3, 2, 1, 4).reshape(m * 128, k * 4)
     return full[:rows, :-(-K // 16)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("offset,pitch", [(0, 104), (1, 104), (0, 101), (3, 107)])
+def test_reading_back_into_any_rows(dg, dtype, offset, pitch):
+    rows, K = 131, 100
+    (codes, scales, r), _ = operand(rows, K, 68)
+    # the formula's steps, each rounded to FP32: code * (scale * row scale)
+    one = np.ones(rows, np.float32)
+    packed = codes.cpu().numpy()
+    plain = np.stack([packed & 15, packed >> 4], -1).reshape(rows, K)
+    of_block = untiled(scales, rows, K)
+    code = ref.values(plain, np.full_like(of_block, 0x38), one).astype(np.float32)
+    scale = ref.values(np.full_like(plain, 2), of_block, one).astype(np.float32)
+    v = code * (scale * r.cpu().numpy()[:, None])
+    assert v.dtype == np.float32
+    room = torch.full((rows * pitch + 8,), 7.0, dtype=TYPES[dtype], device="cuda")
+    d = room[offset:].as_strided((rows, K), (pitch, 1), room.storage_offset() + offset)
+    dg.dequantize_nvf4(codes, scales, r, d)
+    assert torch.equal(d.cpu(), torch.from_numpy(v).to(TYPES[dtype]))
+    outside = torch.ones(rows * pitch + 8, dtype=torch.bool)
+    outside.as_strided((rows, K), (pitch, 1), offset)[:] = False
+    assert (room.cpu()[outside] == 7.0).all()
