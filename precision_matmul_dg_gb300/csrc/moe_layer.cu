@@ -125,7 +125,7 @@ struct Route {
   int *expert, *first, *n;   // per chunk
   float* fx;                 // per token: what its values are multiplied by
   int *ids, *rank;           // per slot: expert; place among that expert's (-1: dropped)
-  int *cnt, *start;          // per expert: slots; of those before, slots and (<< 16) chunks
+  int *cnt, *seen, *start;   // per expert: its slots, twice; those of the experts before
   int* chunks;               // their number
 };
 __device__ __forceinline__ Route route_at(int* m, const LayerParams& p) {
@@ -138,12 +138,13 @@ __device__ __forceinline__ Route route_at(int* m, const LayerParams& p) {
   r.n = r.first + p.slots;
   r.fx = reinterpret_cast<float*>(r.n + p.slots);
   r.cnt = reinterpret_cast<int*>(r.fx + p.tokens);
-  r.start = r.cnt + p.count;
+  r.seen = r.cnt + p.count;
+  r.start = r.seen + p.count;
   r.chunks = r.start + p.count;
   return r;
 }
 int route_bytes(int64_t slots, int64_t tokens, int64_t count) {
-  return static_cast<int>(4 * (6 * slots + tokens + 2 * count + 1));
+  return static_cast<int>(4 * (6 * slots + tokens + 3 * count + 1));
 }
 
 // The routing is built by the warp that loads: only who multiplies and finishes sums
@@ -182,29 +183,20 @@ __device__ __forceinline__ void build_route_32(const Route& r, const LayerParams
   __syncwarp();
 }
 
-// More: 32 slots at a time; a slot's rank is the number of its expert's slots in the
-// blocks before and in the lanes below.
-template <bool Down>
-__device__ __forceinline__ void build_route(const Route& r, const LayerParams& p, int lane) {
-#pragma unroll 4
-  for (int s = lane; s < p.slots; s += 32) r.ids[s] = __ldg(p.ids + s);
+// More: the warp that loads counts the experts' slots and cuts them into chunks, and
+// goes on; another puts the slots in their places, 32 at a time.  A slot's rank is the
+// number of its expert's slots in the blocks before and in the lanes below.
+__device__ __forceinline__ void count_route(const Route& r, const LayerParams& p, int lane) {
 #pragma unroll 1
   for (int e = lane; e < p.count; e += 32) r.cnt[e] = 0;
   __syncwarp();
-#pragma unroll 1
-  for (int s0 = 0; s0 < p.slots; s0 += 32) {
-    const int s = s0 + lane;
-    int e = s < p.slots ? r.ids[s] : -1;
-    if (e >= p.count) e = -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const int below = __popc(same & ((1u << lane) - 1u));
-    const int before = e >= 0 ? r.cnt[e] : 0;
-    __syncwarp();
-    if (e >= 0 && below == 0) r.cnt[e] = before + __popc(same);
-    if (s < p.slots) r.rank[s] = e >= 0 ? before + below : -1;
-    __syncwarp();
+#pragma unroll 4
+  for (int s = lane; s < p.slots; s += 32) {
+    const int e = __ldg(p.ids + s);
+    if (e >= 0 && e < p.count) atomicAdd(&r.cnt[e], 1);  // counts: the order does not matter
   }
-  int run = 0;  // slots and chunks of the experts before, at most 512 each
+  __syncwarp();
+  int run = 0;  // slots and (<< 16) chunks of the experts before, at most 512 each
 #pragma unroll 1
   for (int e0 = 0; e0 < p.count; e0 += 32) {
     const int e = e0 + lane;
@@ -216,27 +208,44 @@ __device__ __forceinline__ void build_route(const Route& r, const LayerParams& p
       const int a = __shfl_up_sync(0xffffffffu, v, d);
       if (lane >= d) v += a;
     }
-    if (e < p.count) r.start[e] = run + v - own;
+    int at = (run + v - own) & 0xFFFF, u = (run + v - own) >> 16;
+    if (e < p.count) r.start[e] = at;
+#pragma unroll 1
+    for (int left = c; left > 0; left -= p.chunk, at += p.chunk, ++u) {
+      r.expert[u] = e;
+      r.first[u] = at;
+      r.n[u] = min(p.chunk, left);
+    }
     run += __shfl_sync(0xffffffffu, v, 31);
   }
   if (lane == 0) *r.chunks = run >> 16;
   __syncwarp();
+  asm volatile("bar.arrive 2, 64;" ::: "memory");
+}
+template <bool Down>
+__device__ __forceinline__ void place_route(const Route& r, const LayerParams& p, int lane) {
+#pragma unroll 4
+  for (int s = lane; s < p.slots; s += 32) r.ids[s] = __ldg(p.ids + s);
 #pragma unroll 1
-  for (int s = lane; s < p.slots; s += 32) {
-    const int rank = r.rank[s];
-    if (rank < 0) continue;
-    const int e = r.ids[s], base = r.start[e];
-    const int at = (base & 0xFFFF) + rank;
-    r.of[at] = Down ? s : s * p.inv_top_k >> 20;
-    const int k = rank * p.inv_chunk >> 16;
-    if (k * p.chunk == rank) {
-      const int u = (base >> 16) + k;
-      r.expert[u] = e;
-      r.first[u] = at;
-      r.n[u] = min(p.chunk, r.cnt[e] - rank);
-    }
-  }
+  for (int e = lane; e < p.count; e += 32) r.seen[e] = 0;
   __syncwarp();
+#pragma unroll 1
+  for (int s0 = 0; s0 < p.slots; s0 += 32) {
+    const int s = s0 + lane;
+    int e = s < p.slots ? r.ids[s] : -1;
+    if (e >= p.count) e = -1;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int below = __popc(same & ((1u << lane) - 1u));
+    const int before = e >= 0 ? r.seen[e] : 0;
+    __syncwarp();
+    if (e >= 0 && below == 0) r.seen[e] = before + __popc(same);
+    if (s < p.slots) r.rank[s] = e >= 0 ? before + below : -1;
+    __syncwarp();
+  }
+  asm volatile("bar.sync 2, 64;" ::: "memory");
+#pragma unroll 1
+  for (int s = lane; s < p.slots; s += 32)
+    if (r.rank[s] >= 0) r.of[r.start[r.ids[s]] + r.rank[s]] = Down ? s : s * p.inv_top_k >> 20;
 }
 
 // A CTA's units, chunk by chunk of a tile (neighbours share a tile's place in
@@ -475,7 +484,8 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
   if (p.slots <= 32) {
     if (warp == kTmaWarp) build_route_32<Down>(r, p, lane);
   } else {
-    if (warp == kTmaWarp) build_route<Down>(r, p, lane);
+    if (warp == kTmaWarp) count_route(r, p, lane);
+    if (warp == kEpiWarp) place_route<Down>(r, p, lane);
   }
   if (!Down && warp < kMmaWarps) ok = convert_tokens<Fmt, kMmaWarps>(p, xs, r, x_bar, warp, lane);
   // the routing and the tokens are there; who loads needs only the first, which
