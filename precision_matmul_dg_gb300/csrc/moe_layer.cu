@@ -31,10 +31,10 @@
 // and scales.  Few copies matter: a TMA copy costs the issuing thread about 80
 // clocks (with one for each K block and 8 rows, 990 clocks a stage).
 //
-// Measured, experts of 2048 x 2048, SwiGLU: 8 tokens, FP8, 454 MB of weights in 79.6
-// us (6.0 and 5.5 TB/s in the two products, HBM); 16 tokens, NVF4, 335 MB in 75.9 us
+// Measured, experts of 2048 x 2048, SwiGLU: 8 tokens, FP8, 454 MB of weights in 77
+// us (6.0 and 5.5 TB/s in the two products, HBM); 16 tokens, NVF4, 335 MB in 72.8 us
 // (5.5 and 4.8 TB/s, instructions: 315 for 16 rows x 256 values).  One token, 8 experts
-// of 4096 x 2048, GELU: FP8 29.1 us, NVF4 22.5, of which the kernels' starts are 6.
+// of 4096 x 2048, GELU: FP8 27.7 us, NVF4 22.1, of which the kernels' starts are 6.
 #include <algorithm>
 
 #include "convert.cuh"
@@ -52,6 +52,7 @@ constexpr int kEpiWarps = 3;
 constexpr int kTileRows = 32;  // weight rows per unit (twice as many where gated)
 constexpr int kMaxChunk = 8;   // slots per unit
 constexpr int kMaxStages = 8;
+constexpr int64_t kNextBytes = 48 * 1024;  // a CTA's part of what goes to L2 ahead
 
 enum : int { kFp8 = 0, kNvf4 = 1 };
 
@@ -112,6 +113,12 @@ struct LayerParams {
   int h_stages;
   float* part;               // slots' sums of the second product, part_pitch apart
   int64_t part_pitch;
+  // the first kernel's: the weights of the second, to bring into L2
+  const uint8_t* next_w;
+  int64_t next_ld, next_stride;
+  const uint8_t* next_sf;
+  int64_t next_sf_stride;    // bytes from one expert's scale tiles to the next's
+  int next_bytes, next_rows, next_k_tiles;
   int stages, stage_bytes;
   int off_x, off_red, off_route;
   int* status;
@@ -430,6 +437,34 @@ __device__ __forceinline__ float silu(float g) {
   return __fdividef(g, 1.0f + ex2_approx(-kLog2e * g));
 }
 
+__device__ __forceinline__ void prefetch_l2(const uint8_t* at, uint32_t bytes) {
+  if (bytes > 0)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
+// The second product's first weights into L2, by the thread whose last loads have
+// landed: HBM would wait for the second kernel until the first one's last sums are
+// done and its own first loads are out.  (One token, FP8 27.7 us, was 29.2; with 128
+// KB a CTA 29.0, for NVF4 later than without; before the last loads have landed 28.1.)
+template <int Fmt>
+__device__ __forceinline__ void prefetch_next(const LayerParams& p, const Route& r, int chunks,
+                                              int step) {
+  const int tiles = (p.next_rows + kTileRows - 1) / kTileRows;
+  int64_t left = kNextBytes;
+  UnitWalk walk{};
+  walk.start(blockIdx.x, step, chunks);
+  for (; walk.tile < tiles && left > 0; walk.next()) {
+    const int e = r.expert[walk.u], row = walk.tile * kTileRows;
+    const int64_t bytes = (min(kTileRows, p.next_rows - row) - 1) * p.next_ld + p.next_bytes;
+    prefetch_l2(p.next_w + e * p.next_stride + row * p.next_ld,
+                static_cast<uint32_t>(min(bytes, left)) & ~15u);
+    if (Fmt == kNvf4)  // a quarter of the tiles of 128 rows
+      prefetch_l2(p.next_sf + e * p.next_sf_stride +
+                      ((walk.tile >> 2) * 4 + (walk.tile & 3)) * static_cast<int64_t>(p.next_k_tiles) * 128,
+                  static_cast<uint32_t>(p.next_k_tiles) * 128);
+    left -= bytes;
+  }
+}
+
 // Down: the second product (its activations come with the ring's stages).
 template <int Fmt, bool Down, bool Gated, int Teams>
 __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Teams == 1 ? 2 : 1)
@@ -580,6 +615,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
     for (int64_t i = first; i < issued; ++i)
       mbar_wait(&full_bar[i % p.stages], static_cast<uint32_t>((i / p.stages) & 1), p.timeout_ns,
                 p.status);
+    if (!Down && ok && chunks > 0) prefetch_next<Fmt>(p, r, chunks, step);
     if (!Down && p.K >= 8) mbar_wait(x_bar, 0, p.timeout_ns, p.status);
     return;
   }
@@ -1037,6 +1073,14 @@ cudaError_t run_layer(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   p.K = static_cast<int>(a.width);
   p.rows = static_cast<int>(a.hidden);
   p.up0 = static_cast<int>(a.hidden);
+  p.next_w = static_cast<const uint8_t*>(a.down.codes);
+  p.next_ld = a.down.ld;
+  p.next_stride = a.down.stride;
+  p.next_bytes = static_cast<int>(Fmt == kFp8 ? a.hidden : (a.hidden + 1) / 2);
+  p.next_rows = static_cast<int>(a.out);
+  p.next_k_tiles = static_cast<int>((a.hidden + 63) / 64);
+  p.next_sf = static_cast<const uint8_t*>(a.down.scales);
+  p.next_sf_stride = (a.out + 127) / 128 * p.next_k_tiles * 512;
   const cudaError_t e = a.gated ? run_phase<Fmt, false, true, 1>(a, p, x_bytes)
                                 : run_phase<Fmt, false, false, 1>(a, p, x_bytes);
   if (e != cudaSuccess) return e;

@@ -105,6 +105,8 @@ class Case:
     (32, 4, 8, 136, 160, 72, "bf16", False),
     (4, 8, 16, 2048, 256, 2048, "bf16", True),
     (1, 8, 64, 2048, 128, 96, "f16", False),
+    (2, 1, 3, 9, 8, 1, "bf16", False),
+    (3, 2, 3, 1, 1, 33, "f16", False),
 ])
 def test_layer(dg, fmt, tokens, top_k, count, width, hidden, out, dtype, gated):
     c = Case(fmt, tokens, top_k, count, width, hidden, out, dtype, gated, seed=tokens + width)
