@@ -159,7 +159,8 @@ int route_bytes(int64_t slots, int64_t tokens, int64_t count) {
 // cache yet, so it is short, without a division.  (The first kernel wants sorted places'
 // tokens, the second their slots.)
 //
-// Up to 32 slots: a slot per lane.
+// Up to 32 slots: a slot per lane (in the form below one token of 8 choices took 0.4 us
+// longer in each product).
 template <bool Down>
 __device__ __forceinline__ void build_route_32(const Route& r, const LayerParams& p, int lane) {
   int e = lane < p.slots ? __ldg(p.ids + lane) : -1;
