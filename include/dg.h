@@ -678,10 +678,11 @@ dg_status dg_gemm_nvf4_grouped(int64_t count, int64_t rows, int64_t N, int64_t K
  * on weights quantized in 8 bits (E4M3 codes with 128 x 128 FP32 scales, as
  * dg_gemm_fp8_grouped's B) or 4 bits (NVF4 stacks).  X is not quantized: it is
  * exact (but for values below 2^-31 of their row's largest, which may lose
- * bits), sums are FP32, and h is rounded once, to 11 bits (FP16 times a power of
- * two for each 32 of its values).  Infinities and NaNs propagate.  The used
- * experts' weights are read once for up to 8 slots each.  For a decoding step;
- * many tokens are faster through dg_moe_sort and the grouped products.
+ * bits), sums are FP32, and h is held in 22 bits (two FP16 values times a power
+ * of two for each 32 of them).  Infinities and NaNs propagate.  The used
+ * experts' weights are read once for up to 8 slots each (W1) and 4 (W2).  For a
+ * decoding step; many tokens are faster through dg_moe_sort and the grouped
+ * products.
  */
 typedef enum { DG_MOE_FP8 = 0, DG_MOE_NVF4 = 1 } dg_moe_format;
 /* GELU: W1 has `hidden` rows.  SwiGLU: W1 has 2 * hidden rows, gate first;

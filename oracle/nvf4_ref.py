@@ -133,8 +133,8 @@ def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
 
     A sum of K products errs by at most (K + 200) 2^-23 of the sum of magnitudes
     (truncated FP32 additions, the slices' sums and the scales a few more), a value
-    of x by 2^-39 of its row's largest, one of h by 2^-11 of itself and 2^-39 of the
-    largest of 32 around it.  GELU's and SiLU's slopes are at most 1.13, and they
+    of x by 2^-39 of its row's largest, one of h (two FP16 values, the second what the
+    first leaves) by 2^-22 of itself and 2^-39 of the largest of 32 around it.  GELU's and SiLU's slopes are at most 1.13, and they
     are evaluated to 2e-6."""
     tokens, top_k = ids.shape
     count, out = down.shape[0], down.shape[1]
@@ -169,7 +169,7 @@ def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
                 h = fp8_ref.gelu(h)
             pad = np.zeros(-len(h) % 32)
             around = np.repeat(np.concatenate([np.abs(h) + err, pad]).reshape(-1, 32).max(1), 32)
-            err = err + 2.0 ** -11 * (np.abs(h) + err) + 2.0 ** -39 * around[:len(h)]
+            err = err + 2.0 ** -22 * (np.abs(h) + err) + 2.0 ** -39 * around[:len(h)]
             v, ev = product(down[e], h, err, None if bias_down is None else bias_down[e])
             w = 1.0 if weights is None else float(weights[t, j])
             y[t] += w * v

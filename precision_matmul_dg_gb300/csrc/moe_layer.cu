@@ -7,7 +7,7 @@
 // The job is to read the used experts' weights once, at the rate of HBM: 8-bit
 // codes (FP8) or 4-bit codes and their scales (NVF4).  Up and down are the same
 // machine: a persistent CTA per SM takes units (32 weight rows of one expert, up
-// to 8 of its slots), one thread keeps a ring of loads in flight across units, 8
+// to 8 of its slots, 4 in down), one thread keeps a ring of loads in flight across units, 8
 // warps multiply with warp-level FP16 MMAs (m16n8k16, weights as the 16-row
 // operand, slots as the 8 columns), and 3 warps take the units' sums in turn and
 // finish them.
@@ -17,8 +17,10 @@
 // codes as they are, want the activations in three parts, and 4-bit codes' two
 // blocks in columns of their own: 1340 clocks a stage of NVF4 against the 780 that
 // HBM needs for it.)  Activations are FP16 times a power of two: x exactly, h
-// rounded once, each 32 of its values with a power of their own, so that h has
-// FP32's range.
+// as two FP16 values (22 bits) in two of the MMA's columns, each 32 of its values with
+// a power of their own, so that h has FP32's range.  (With 11 bits its rounding is as
+// large as that of an FP16 result; 16 tokens NVF4 72.8 us then, as units of the second
+// product held eight slots.)
 //
 // What a lane needs for 32 values of K is then 16 bytes: in a 16-byte piece of a
 // weight row as ldmatrix hands it out, lane q of a row's four has 4 (FP8) or 8
@@ -32,9 +34,9 @@
 // clocks (with one for each K block and 8 rows, 990 clocks a stage).
 //
 // Measured, experts of 2048 x 2048, SwiGLU: 8 tokens, FP8, 454 MB of weights in 77
-// us (6.0 and 5.5 TB/s in the two products, HBM); 16 tokens, NVF4, 335 MB in 72.8 us
+// us (6.0 and 5.5 TB/s in the two products, HBM); 16 tokens, NVF4, 335 MB in 76.5 us
 // (5.5 and 4.8 TB/s, instructions: 315 for 16 rows x 256 values).  One token, 8 experts
-// of 4096 x 2048, GELU: FP8 27.7 us, NVF4 22.1, of which the kernels' starts are 6.
+// of 4096 x 2048, GELU: FP8 27.3 us, NVF4 22.3, of which the kernels' starts are 6.
 #include <algorithm>
 
 #include "convert.cuh"
@@ -51,6 +53,7 @@ constexpr int kTeamWarps = 8;  // that share a stage
 constexpr int kEpiWarps = 3;
 constexpr int kTileRows = 32;  // weight rows per unit (twice as many where gated)
 constexpr int kMaxChunk = 8;   // slots per unit
+constexpr int kMaxChunkH = 4;  // in the second product: two columns each
 constexpr int kMaxStages = 8;
 constexpr int64_t kNextBytes = 48 * 1024;  // a CTA's part of what goes to L2 ahead
 
@@ -79,14 +82,14 @@ struct Shape {
   static constexpr int kRed = kEpiWarps * kMmaWarps * 4 * 32 * 4;
   static constexpr int kBars = (2 * kMaxStages + 2 * kEpiWarps + 1) * 8 + 8;
 };
-// A slot's share of a stage of the second product: FP16 values, then a scale for
-// each 32 of them.  Rows are 64 bytes apart in their banks: two rows' 64-byte
-// reads do not meet.
+// A slot's share of a stage of the second product: FP16 values, what is left of
+// them as FP16, then a scale for each 32 of them.  Rows are 64 bytes apart in their
+// banks: two rows' 64-byte reads do not meet.
 template <int Fmt>
 struct HRow {
   static constexpr int kK =
       Shape<Fmt, true, false>::kSlices * Shape<Fmt, true, false>::kBlockK;
-  static constexpr int kScales = 2 * kK;
+  static constexpr int kRest = 2 * kK, kScales = 4 * kK;
   static constexpr int kBytes = kScales + kK / 32 * 4 + (Fmt == kNvf4 ? 64 : 0);
   static_assert(kBytes % 128 == 64, "banks");
 };
@@ -674,12 +677,17 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
           float inv;
           const float f = half_factor(__uint_as_float(most), inv);
           uint8_t* to = p.h + (static_cast<int64_t>(ks) * p.slots + pos) * H::kBytes;
-          reinterpret_cast<uint16_t*>(to)[in_stage + place_of<Fmt>(lane)] =
-              static_cast<uint16_t>(F16::pack(v * f, 0.0f));
+          // the value and what is left of it (of infinities and NaNs nothing)
+          const uint32_t hi = F16::pack(v * f, 0.0f) & 0xFFFFu;
+          const float rest = (hi & 0x7FFFu) < F16::kInf ? fmaf(v, f, -F16::one(hi)) : 0.0f;
+          uint16_t* at = reinterpret_cast<uint16_t*>(to) + in_stage + place_of<Fmt>(lane);
+          at[0] = static_cast<uint16_t>(hi);
+          at[H::kRest / 2] = static_cast<uint16_t>(F16::pack(rest, 0.0f));
           if (lane == 0) reinterpret_cast<float*>(to + H::kScales)[in_stage / 32] = inv;
           if (tile == p.tiles - 1)  // zeros to the end of the last stage
             for (int i = in_stage + 32; i < H::kK; i += 32) {
               reinterpret_cast<uint16_t*>(to)[i + lane] = 0;
+              reinterpret_cast<uint16_t*>(to)[H::kRest / 2 + i + lane] = 0;
               if (lane == 0) reinterpret_cast<float*>(to + H::kScales)[i / 32] = 0.0f;
             }
         }
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
         if (lane == 0) mbar_arrive(&red_empty[mine]);
       } else {
         for (int j = 0; j < n; ++j) {
-          const float v = fmaf(total(0, j), of_row[0], bias[0]);
+          const float v = fmaf(total(0, j) + total(0, j + kMaxChunkH), of_row[0], bias[0]);
           if (there) p.part[r.of[first + j] * p.part_pitch + row] = v;
         }
         __syncwarp();
@@ -731,16 +739,16 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
   while (ok && walk.tile < p.tiles && units > 0) {
     const int tile = walk.tile, n = r.n[walk.u], first = r.first[walk.u];
     // this lane's column of the activations, and its two columns of the sums
-    // (past the last: the last)
-    const int col = min(g, n - 1);
+    // (past the last: the last); of h, what is left in columns 4 ..
+    const int col = min(Down ? g & 3 : g, n - 1);
     const uint32_t b_base =
-        Down ? smem0 + static_cast<uint32_t>(S::kW + S::kS + col * H::kBytes + slice * S::kBlockK * 2 +
-                                             q * 16)
+        Down ? smem0 + static_cast<uint32_t>(S::kW + S::kS + col * H::kBytes + (g >> 2) * H::kRest +
+                                             slice * S::kBlockK * 2 + q * 16)
              : smem_addr(xs) + static_cast<uint32_t>(r.of[first + col] * p.x_pitch + q * 16);
     const uint32_t h_base = smem0 + static_cast<uint32_t>(S::kW + S::kS + H::kScales +
                                                           slice * (S::kBlockK / 32) * 4);
-    const uint32_t h0 = h_base + static_cast<uint32_t>(min(2 * q, n - 1) * H::kBytes);
-    const uint32_t h1 = h_base + static_cast<uint32_t>(min(2 * q + 1, n - 1) * H::kBytes);
+    const uint32_t h0 = h_base + static_cast<uint32_t>(min(2 * q & 3, n - 1) * H::kBytes);
+    const uint32_t h1 = h_base + static_cast<uint32_t>(min((2 * q + 1) & 3, n - 1) * H::kBytes);
     sw0 = sw0_next, sw1 = sw1_next;
     walk.next();
     load_sw(walk, 0);
@@ -996,6 +1004,10 @@ cudaError_t run_phase(const MoeLayerArgs& a, LayerParams p, int x_bytes) {
   const MoeWeights& w = Down ? a.down : a.up;
   const int64_t n_rows = Down ? a.out : a.hidden * (Gated ? 2 : 1);
   const int64_t bytes_k = Fmt == kFp8 ? p.K : (p.K + 1) / 2;
+  // Slots per unit: as many as there are tokens can meet in one expert (a token
+  // that names an expert twice gets a unit more), at most an MMA's columns.
+  p.chunk = static_cast<int>(std::min<int64_t>(a.tokens, Down ? kMaxChunkH : kMaxChunk));
+  p.inv_chunk = (65536 + p.chunk - 1) / p.chunk;
   p.k_blocks = static_cast<int>((bytes_k + 127) / 128);
   p.full_blocks = static_cast<int>(bytes_k / 128);
   p.k_tiles = static_cast<int>((p.K + 63) / 64);
@@ -1122,10 +1134,6 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a) {
   p.top_k = static_cast<int>(a.top_k);
   p.slots = static_cast<int>(a.tokens * a.top_k);
   p.count = static_cast<int>(a.count);
-  // Slots per unit: as many as there are tokens can meet in one expert (a token
-  // that names an expert twice gets a unit more), at most an MMA's columns.
-  p.chunk = static_cast<int>(std::min<int64_t>(a.tokens, kMaxChunk));
-  p.inv_chunk = (65536 + p.chunk - 1) / p.chunk;
   p.inv_top_k = ((1 << 20) + p.top_k - 1) / p.top_k;
   p.bf16 = a.bf16;
   p.X = static_cast<const uint16_t*>(a.X);
