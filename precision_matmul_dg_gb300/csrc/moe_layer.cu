@@ -113,7 +113,6 @@ struct LayerParams {
   int64_t ldx;
   int x_pitch;               // bytes of a token in shared memory
   uint8_t* h;                // [K stage][slot][HRow]
-  int h_stages;
   float* part;               // slots' sums of the second product, part_pitch apart
   int64_t part_pitch;
   // the first kernel's: the weights of the second, to bring into L2
