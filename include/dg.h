@@ -647,9 +647,11 @@ dg_status dg_dequantize_nvf4(int64_t count, int64_t rows, int64_t K, const void 
                              dg_dtype dtype_d, int64_t ldd, int64_t stride_d, dg_stream_t stream);
 
 /* D = epilogue(alpha * A.B^T + beta * D) for NVF4 A (M x K) and B (N x K), with
- * FP32 sums over all of K on the block-scaled MMA.  D, bias and epilogues as
- * dg_gemm_fp8; K is at least 1.  M == 0 or N == 0 is a no-op.  Results are
- * bit-stable; nothing is allocated. */
+ * FP32 sums over all of K on the block-scaled MMA.  alpha times a row scale of A
+ * is one FP32 product; what the row scales of B make of it may lie anywhere: only
+ * a result beyond FP32 overflows.  D, bias and epilogues as dg_gemm_fp8; K is at
+ * least 1.  M == 0 or N == 0 is a no-op.  Results are bit-stable; nothing is
+ * allocated. */
 dg_status dg_gemm_nvf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
                        const void *scale_a, const float *row_a, const void *B, int64_t ldb,
                        const void *scale_b, const float *row_b, void *D, dg_dtype dtype_d,

@@ -122,6 +122,24 @@ __device__ __forceinline__ bool next_tile(N4Walk& w, const N4Params& p, int unit
   return true;
 }
 
+// A row's factor s (alpha times its scale) as s1 g, s1 between 2^-104 and 2^65 and g a power
+// of two, 1 unless s is outside [2^-100, 2^65).  A nonzero sum of codes times scales is
+// between 2^-20 and 2^53 in magnitude, so sum * s1 is in FP32's normal range, and
+// sum * s1 * (a column's scale) leaves it only where the result does too: g then moves it
+// further out.
+__device__ __forceinline__ float row_factor(float s, float& g) {
+  const uint32_t b = __float_as_uint(s) & 0x7FFFFFFFu, e = b >> 23;
+  g = 1.0f;
+  if (e > 191 && e < 255) {  // to 2^64 .. 2^65
+    g = __uint_as_float((e - 191 + 127) << 23);
+    s = __uint_as_float((__float_as_uint(s) & 0x807FFFFFu) | 191u << 23);
+  } else if (e < 27 && b != 0) {  // below 2^-100, subnormal ones too
+    g = 0x1p-45f;
+    s *= 0x1p45f;
+  }
+  return s;
+}
+
 template <bool Grouped, int BN, int Stages, int CG>
 __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
     gemm_nvf4_kernel(const __grid_constant__ CUtensorMap tmap_a,
@@ -399,7 +417,9 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
       const N4Tile now = tile;
       const int col0 = now.n0 + first;
       const int row = min(now.row0 + in_tile + lane, p.M - 1);
-      const float s = p.alpha * row_next;
+      float g;
+      const float s = row_factor(p.alpha * row_next, g);
+      const bool far = __any_sync(0xffffffffu, g != 1.0f);
       __syncwarp();  // the last tile's have been read
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -447,6 +467,11 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
                                            __uint_as_float(x[2 * i + 3])),
                                s2),
                           make_float2(k.z, k.w));
+        }
+        if (far) {
+          const float2 g2 = make_float2(g, g);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], g2);
         }
         if (p.beta != 0.0f) {
           const int64_t z = p.dtype_d == DG_F32 ? 4 : 2;
