@@ -440,6 +440,16 @@ __device__ __forceinline__ float silu(float g) {
   return __fdividef(g, 1.0f + ex2_approx(-kLog2e * g));
 }
 
+// t * row * power + bias, one rounding: the power of two goes to the row's scale, or, where
+// that leaves FP32's normal range, to t (NVF4's, between 2^-34 and 2^60 where it is not
+// zero), which comes back into range with the row's scale if the result is in it.  (FP8 has
+// no row scale, and a power alone is in range.)
+__device__ __forceinline__ float scaled_sum(float t, float row, float power, float bias) {
+  const float s = row * power;
+  const bool in = (fabsf(s) >= 0x1p-126f && fabsf(s) <= 0x1.fffffep127f) || row == 0.0f;
+  return fmaf(in ? t : t * power, in ? s : row, bias);
+}
+
 __device__ __forceinline__ void prefetch_l2(const uint8_t* at, uint32_t bytes) {
   if (bytes > 0)
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
@@ -663,9 +673,9 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
         for (int j = 0; j < n; ++j) {
           const int pos = first + j;
           const float fx = r.fx[r.of[pos]];
-          float v = fmaf(total(0, j), of_row[0] * fx, bias[0]);
+          float v = scaled_sum(total(0, j), of_row[0], fx, bias[0]);
           if (Gated) {
-            const float up = fmaf(total(1, j), of_row[1] * fx, bias[1]);
+            const float up = scaled_sum(total(1, j), of_row[1], fx, bias[1]);
             v = silu(v) * up;
           } else {
             v = gelu2(make_float2(v, v)).x;

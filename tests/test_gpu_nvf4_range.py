@@ -1,11 +1,12 @@
-"""NVF4 products where factors of a result lie beyond FP32's range and their product does
-not."""
+"""NVF4 products and the expert layer where factors of a result lie beyond FP32's range and
+their product does not."""
 
 import numpy as np
 import pytest
 import torch
 
 from oracle import fp8_ref, nvf4_ref as ref
+from test_gpu_moe_layer import Case
 from test_gpu_nvf4 import TYPES, check, dg, gpu, operand  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -72,3 +73,33 @@ def test_experts_row_scales_that_cancel(dg, pairs):  # noqa: F811
         t, err = ref.product(av[at], parts[e][1])
         assert check_finite(d[at], t, err, "f32") > 0.3 * t.size
     dg.check_status()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_layer_of_tiny_tokens(dg, gated):  # noqa: F811
+    """Tokens near 2^-117 and row scales of W1 far below one: a row's scale times the power of
+    two that a token is held with is below FP32's normal range, the hidden values are not (all
+    products have one sign, so they are large against their factors)."""
+    c = Case("nvf4", 3, 2, 4, 512, 128, 64, "bf16", gated=False, seed=8)
+    c.gated = gated
+    if gated:
+        c = Case("nvf4", 3, 2, 4, 512, 128, 64, "bf16", gated=True, seed=8)
+    tiny = 2.0 ** -117
+    x = np.abs(c.x64) + 1.0
+    c.x.copy_(torch.from_numpy(x * tiny).to(c.x.dtype))
+    c.x64 = c.x.double().cpu().numpy()
+    c.up[0].bitwise_and_(0x77)  # W1's codes without their signs
+    c.up64 = np.abs(c.up64)
+    low = 2.0 ** -9
+    rows = slice(128, None) if gated else slice(None)
+    if gated:
+        # the gates are 2^10 and more times their own scales: SiLU is their argument
+        c.up[2][:, :128].mul_(2.0 ** 126)
+        c.up64[:, :128] *= 2.0 ** 126
+    c.up[2][:, rows].mul_(low)
+    c.up64[:, rows] *= low
+    lift = 2.0 ** 100
+    c.down[2].mul_(lift)
+    c.down64 = c.down64 * lift
+    c.run(dg)
+    c.check()
