@@ -1036,7 +1036,9 @@ def _nvf4_operand(torch, codes, scales, row_scales, what, K=None):
         _rows(row_scales, torch.float32, "the row scales of " + what, each, dim - 1)
         if not (scales.is_contiguous() and row_scales.is_contiguous()):
             raise ValueError("the scales of %s must be contiguous" % what)
-    return (s[-2] if rows > 1 else (width + 15) // 16 * 16), s[0], shape
+    # (of one row, whose stride torch leaves open: in a stack, the next matrix's)
+    return (s[-2] if rows > 1 else s[0] if dim == 3 and count > 1 else
+            (width + 15) // 16 * 16), s[0], shape
 
 
 def _pitch(stride, rows, width, multiple):
@@ -1183,7 +1185,8 @@ def _moe_weights(torch, w, bias, dtype, what):
                 scales.shape[2] < (k + 127) // 128:
             raise ValueError("shape mismatch: %s %s with %s" % (
                 what, tuple(codes.shape), tuple(scales.shape)))
-        m = MoeWeights(codes.data_ptr(), s[1], s[0], scales.data_ptr(), z[1], z[0])
+        ld = s[1] if n > 1 else s[0] if count > 1 else -(-k // 16) * 16
+        m = MoeWeights(codes.data_ptr(), ld, s[0], scales.data_ptr(), z[1], z[0])
     if bias is not None:
         m.stride_bias = _rows(bias, dtype, "the bias of " + what, shape[:2])[0]
         m.bias = bias.data_ptr()
