@@ -717,7 +717,7 @@ typedef struct {
  * these rules or too little scratch; DG_ERR_UNSUPPORTED for another type, more
  * than 1024 experts, more than 512 slots, more tokens than a CTA's shared
  * memory holds (68 bytes and 2 * (width rounded up to a multiple of 256) for each
- * token, 12 for each expert and 24 for each slot are at most 150 KiB, less 16),
+ * token, 12 for each expert and 24 for each slot are at most 150 KiB, less 4),
  * or SwiGLU on NVF4 weights with hidden not a multiple of 128. */
 int64_t dg_moe_layer_scratch(int64_t tokens, int64_t top_k, int64_t hidden, int64_t out);
 dg_status dg_moe_layer(int64_t tokens, int64_t top_k, int64_t count, int64_t width, int64_t hidden,
