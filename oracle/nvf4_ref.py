@@ -125,17 +125,32 @@ def silu(g):
         return g / (1.0 + np.exp(-g))
 
 
+def chain(K):
+    """Roundings (or truncations) to 24 bits that a term of the layer's sums of K products
+    passes, and those that the sum's other terms pass beside it, at most.
+
+    The products are taken by MMAs of 16 with an accumulator: an exact product of two
+    FP16 values, then 16 of them and the accumulator aligned to the largest, added and
+    normalised, 18 truncations.  A term passes up to eight of them (256 values of K in
+    4 bits, which two accumulators share; 2 for each 32 values, whose halves lie in both),
+    then FP32 additions: of the accumulators, times scales, into the sum of the blocks that
+    a warp meets, which are every second at least (up to 5 for each 512 values: in 8
+    bits, one for each of the four powers of h in a block and one for the block), up to
+    eight warps' sums, h's two values' sums, and the row's scale.  Additions of zeros, past
+    K, are exact."""
+    return 18 * min(8, 2 * -(-K // 32)) + 5 * -(-K // 512) + 10
+
+
 def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
     """(y, bound) of the expert layer on values: x [tokens, width], up [count,
     hidden or 2 hidden, width], down [count, out, hidden]; the bound is of an
     FP32 computation with x and h held as include/dg.h says, before the last
     rounding.
 
-    A sum of K products errs by at most (K + 200) 2^-23 of the sum of magnitudes
-    (truncated FP32 additions, the slices' sums and the scales a few more), a value
-    of x by 2^-39 of its row's largest, one of h (two FP16 values, the second what the
-    first leaves) by 2^-22 of itself and 2^-39 of the largest of 32 around it.  GELU's and SiLU's slopes are at most 1.13, and they
-    are evaluated to 2e-6."""
+    A product errs by chain(K) roundings of 2^-23 of the sum of magnitudes, a value of x
+    by 2^-39 of its row's largest, one of h (two FP16 values, the second what the first
+    leaves) by 2^-22 of itself and 2^-39 of the largest of 32 around it.  GELU's and
+    SiLU's slopes are at most 1.13, and they are evaluated to 2e-6."""
     tokens, top_k = ids.shape
     count, out = down.shape[0], down.shape[1]
     u = 2.0 ** -23
@@ -144,7 +159,7 @@ def layer(x, ids, weights, up, down, gated=False, bias_up=None, bias_down=None):
     def product(W, v, verr, bias):
         t = W @ v
         mags = np.abs(W) @ np.abs(v)
-        err = mags * (len(v) + 200) * u + np.abs(W) @ verr
+        err = mags * chain(len(v)) * u + np.abs(W) @ verr
         if bias is not None:
             t = t + bias
             err = err + (np.abs(t) + np.abs(bias)) * u
