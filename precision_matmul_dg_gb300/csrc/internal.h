@@ -35,6 +35,13 @@ enum : int {
 // drains.  Every kernel launched this way executes griddepcontrol.wait
 // before its first global-memory access, which waits for that kernel to
 // complete and its memory to be visible.
+//   One exception: the second and later kernels of one call may read, ahead of
+// their wait, inputs of the call that none of its kernels writes, where every
+// CTA of the kernel before signals (griddepcontrol.launch_dependents) only
+// behind its own wait: then all kernels before the call have completed.  (The
+// expert layer: choices, routing weights, W2 with its scales and biases.)
+// Every such kernel still waits before it ends, so that the next one's wait
+// covers the whole call.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t stream, Args&&... args) {

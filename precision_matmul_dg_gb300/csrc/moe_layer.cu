@@ -621,6 +621,8 @@ __global__ void __launch_bounds__(Shape<Fmt, Down, Gated, Teams>::kThreads, Team
         }
       }
     }
+    // (behind this kernel's wait, never ahead of it: the next kernel reads inputs of the
+    // call before its own)
     grid_launch_dependents();
     if (!ok) *abort_flag = 1;
     // the copies land before the CTA goes away, whoever gave up
@@ -940,6 +942,7 @@ __global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const __grid_const
     }
   };
   choices(0);
+  // (this order: the next call's kernels take it that all before this one have completed)
   grid_dependency_wait();
   grid_launch_dependents();
   if (n >= p.out) return;
