@@ -942,7 +942,6 @@ __global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const __grid_const
     }
   };
   choices(0);
-  // (this order: the next call's kernels take it that all before this one have completed)
   grid_dependency_wait();
   grid_launch_dependents();
   if (n >= p.out) return;
