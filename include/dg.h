@@ -495,7 +495,10 @@ dg_status dg_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A, int64_t ld
  *   128 blocks: ceil(N / 128) rows of lds_b), bias_e = bias + e * stride_bias;
  *   stride_b is a multiple of ldb and at least N * ldb.  Rows outside every
  *   segment are neither read nor written.  Offsets are taken as clamped to
- *   [0, rows]; an end before its start is an empty segment.
+ *   [0, rows]; an end before its start is an empty segment.  Where segments
+ *   overlap so far that they are more than 2^30 tiles (8 rows by 16 columns or
+ *   more), those behind are left out and DG_ERR_INVALID_ARG is recorded in the
+ *   status word.
  *   count is at most 1024.  Other rules as dg_gemm_fp8. */
 dg_status dg_gemm_fp8_grouped(int64_t count, int64_t rows, int64_t N, int64_t K, const void *A,
                               int64_t lda, const float *scale_a, int64_t lds_a, const void *B,
@@ -664,7 +667,8 @@ dg_status dg_gemm_nvf4(int64_t M, int64_t N, int64_t K, const void *A, int64_t l
  * device array of count + 1 int32, each a multiple of 128 (dg_moe_sort with
  * align 128) or `rows`: one that is not is rounded down to it and
  * DG_ERR_INVALID_ARG is recorded in the status word.  Rows outside every
- * segment are neither read nor written. */
+ * segment are not written, and what they hold does not matter (a tile may load
+ * some of them). */
 dg_status dg_gemm_nvf4_grouped(int64_t count, int64_t rows, int64_t N, int64_t K, const void *A,
                                int64_t lda, const void *scale_a, const float *row_a, const void *B,
                                int64_t ldb, int64_t stride_b, const void *scale_b,

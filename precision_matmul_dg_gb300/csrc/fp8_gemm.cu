@@ -61,6 +61,7 @@
 #include "epilogue.cuh"
 #include "fp8.cuh"
 #include "out_box.cuh"
+#include "segments.cuh"
 #include "tc_common.cuh"
 
 namespace dg {
@@ -357,22 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (odd && blockIdx.x == 0) atomicExch(p.status, static_cast<int>(DG_ERR_INVALID_ARG));
     __syncthreads();
-    if (Mode == Fp8Mode::kRows && warp == 0) {
-      int run = 0;
-      if (lane == 0) pre[0] = 0;
-      for (int e0 = 0; e0 < p.count; e0 += 32) {
-        const int e = e0 + lane;
-        int v = 0;
-        if (e < p.count) v = (max(off[e + 1] - off[e], 0) + kRowsPerCta - 1) / kRowsPerCta;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, v, d);
-          if (lane >= d) v += u;
-        }
-        if (e < p.count) pre[e + 1] = run + v;
-        run += __shfl_sync(0xffffffffu, v, 31);
-      }
-    }
+    if (Mode == Fp8Mode::kRows && warp == 0)
+      count_row_blocks(off, pre, p.count, kRowsPerCta, p.n_blocks, blockIdx.x == 0, p.status, lane);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -899,7 +886,7 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
   const int64_t most = Mode == Fp8Mode::kRows
                            ? (a.M / kRowsPerCta + std::min(a.count, a.M)) * p.n_blocks
                            : tiles;
-  if (most > (1 << 30)) return cudaErrorInvalidConfiguration;  // tile numbers are 32-bit
+  if (most > kMaxTiles) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(
       Split ? most * split : std::max<int64_t>(1, std::min<int64_t>(most, a.sm_count))));

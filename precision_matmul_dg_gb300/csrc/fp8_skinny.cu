@@ -30,6 +30,7 @@
 
 #include "epilogue.cuh"
 #include "fp8.cuh"
+#include "segments.cuh"
 #include "tc_common.cuh"
 
 namespace dg {
@@ -167,22 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = threadIdx.x; e <= p.count; e += kThreads)
       off[e] = min(max(__ldg(p.offsets + e), 0), p.M);
     __syncthreads();
-    if (warp == 0) {
-      int run = 0;
-      if (lane == 0) pre[0] = 0;
-      for (int e0 = 0; e0 < p.count; e0 += 32) {
-        const int e = e0 + lane;
-        int v = 0;
-        if (e < p.count) v = (max(off[e + 1] - off[e], 0) + 8 * NT - 1) / (8 * NT);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, v, d);
-          if (lane >= d) v += u;
-        }
-        if (e < p.count) pre[e + 1] = run + v;
-        run += __shfl_sync(0xffffffffu, v, 31);
-      }
-    }
+    if (warp == 0)
+      count_row_blocks(off, pre, p.count, 8 * NT, p.tiles_n, blockIdx.x == 0, p.status, lane);
   }
   __syncthreads();
   SkinnyWalk walk{static_cast<int>(blockIdx.x), 0};
@@ -385,7 +372,7 @@ cudaError_t run_skinny(const Fp8Args& a, SkinnyParams p) {
   if (e != cudaSuccess) return e;
   const int64_t chunks = p.offsets ? a.M / (8 * NT) + std::min(a.count, a.M)
                                    : (a.M + 8 * NT - 1) / (8 * NT);
-  if (chunks * p.tiles_n > (1 << 30)) return cudaErrorInvalidConfiguration;  // 32-bit tile numbers
+  if (chunks * p.tiles_n > kMaxTiles) return cudaErrorInvalidConfiguration;
   const int64_t ctas = std::min<int64_t>(chunks * p.tiles_n, a.sm_count);
   e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads),
                        static_cast<size_t>(L::bytes(p.offsets ? a.count : 0)), a.stream, ta, tb, p);

@@ -31,6 +31,7 @@
 #include "epilogue.cuh"
 #include "fp8.cuh"
 #include "out_box.cuh"
+#include "segments.cuh"
 #include "tc_common.cuh"
 
 namespace dg {
@@ -216,22 +217,8 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
     }
     if (odd && blockIdx.x == 0) atomicExch(p.status, static_cast<int>(DG_ERR_INVALID_ARG));
     __syncthreads();
-    if (warp == 3) {
-      int run = 0;
-      if (lane == 0) pre[0] = 0;
-      for (int e0 = 0; e0 < p.count; e0 += 32) {
-        const int e = e0 + lane;
-        int v = 0;
-        if (e < p.count) v = (max(off[e + 1] - off[e], 0) + 128 * CG - 1) / (128 * CG);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, v, d);
-          if (lane >= d) v += u;
-        }
-        if (e < p.count) pre[e + 1] = run + v;
-        run += __shfl_sync(0xffffffffu, v, 31);
-      }
-    }
+    if (warp == 3)
+      count_row_blocks(off, pre, p.count, 128 * CG, p.n_blocks, blockIdx.x == 0, p.status, lane);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -632,7 +619,7 @@ cudaError_t run_nvf4(const Nvf4Args& a) {
   static int max_units[64] = {};
   const int64_t most =
       Grouped ? (a.M / (128 * CG) + std::min(a.count, a.M)) * p.n_blocks : tiles;
-  if (most > (1 << 30)) return cudaErrorInvalidConfiguration;  // tile numbers are 32-bit
+  if (most > kMaxTiles) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3((4 + L::kEpiWarps) * 32);
   cfg.dynamicSmemBytes = static_cast<size_t>(L::bytes(p.count));
