@@ -87,6 +87,7 @@ struct F8Params {
   int group_m, count;
   int b_rows;  // rows of B's map from one expert to the next
   const int32_t* offsets;
+  uint32_t most_blocks;  // experts: row blocks whose tiles a walk takes
   const float* sa;
   int64_t lds_a;
   const float* sb;
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (odd && blockIdx.x == 0) atomicExch(p.status, static_cast<int>(DG_ERR_INVALID_ARG));
     __syncthreads();
     if (Mode == Fp8Mode::kRows && warp == 0)
-      count_row_blocks(off, pre, p.count, kRowsPerCta, p.n_blocks, blockIdx.x == 0, p.status, lane);
+      count_row_blocks(off, pre, p.count, kRowsPerCta, p.most_blocks, blockIdx.x == 0, p.status, lane);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -813,6 +814,7 @@ cudaError_t run_fp8(const Fp8Args& a, int split = 1) {
   p.N = static_cast<int>(a.N);
   p.m_blocks = static_cast<int>((a.M + kRowsPerCta - 1) / kRowsPerCta);
   p.n_blocks = static_cast<int>((a.N + BN - 1) / BN);
+  p.most_blocks = static_cast<uint32_t>(kMaxTiles / p.n_blocks);
   p.k_blocks = static_cast<int>((a.K + kBlock - 1) / kBlock);
   p.k_rows = static_cast<int>(a.K);
   const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_blocks *

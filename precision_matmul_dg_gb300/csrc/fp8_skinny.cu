@@ -47,6 +47,7 @@ struct SkinnyParams {
   const float* sb;
   int64_t lds_b, stride_sb;
   const int32_t* offsets;  // NULL: one product over M rows
+  uint32_t most_blocks;  // experts: row blocks whose tiles a walk takes
   void* D;
   int64_t ldd;
   const void* bias;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       off[e] = min(max(__ldg(p.offsets + e), 0), p.M);
     __syncthreads();
     if (warp == 0)
-      count_row_blocks(off, pre, p.count, 8 * NT, p.tiles_n, blockIdx.x == 0, p.status, lane);
+      count_row_blocks(off, pre, p.count, 8 * NT, p.most_blocks, blockIdx.x == 0, p.status, lane);
   }
   __syncthreads();
   SkinnyWalk walk{static_cast<int>(blockIdx.x), 0};
@@ -346,6 +347,7 @@ template <int NT, int RG>
 cudaError_t run_skinny(const Fp8Args& a, SkinnyParams p) {
   using L = SkinnySmem<NT, RG>;
   p.tiles_n = static_cast<int>((a.N + 16 * RG - 1) / (16 * RG));
+  p.most_blocks = static_cast<uint32_t>(kMaxTiles / p.tiles_n);
   const int64_t stage_k = L::kStageBlocks * kBlock;
   p.k_stages = static_cast<int>((a.K + stage_k - 1) / stage_k);
   CUtensorMap ta{}, tb{};

@@ -27,7 +27,6 @@
 // rows are read from the device's offsets, multiples of 128 as the scale tiles
 // are; a row tile may run into the next expert's rows (loaded, never stored).
 #include <algorithm>
-#include <type_traits>
 
 #include "epilogue.cuh"
 #include "fp8.cuh"
@@ -52,6 +51,7 @@ struct N4Params {
   int b_rows;           // rows of B's map from one expert to the next
   int sfa_rows, sfb_rows;  // scale tile rows (128 rows each) of A, of one B
   const int32_t* offsets;
+  uint32_t most_blocks;  // experts: row blocks whose tiles a walk takes
   const float *row_a, *row_b;
   void* D;
   int64_t ldd, stride_d;
@@ -124,17 +124,18 @@ __device__ __forceinline__ bool next_tile(N4Walk& w, const N4Params& p, int unit
   return true;
 }
 
-// A row's factor s (alpha times its scale) as s1 g, s1 between 2^-104 and 2^65 and g a power
-// of two, 1 unless s is outside [2^-100, 2^65).  A nonzero sum of codes times scales is
-// between 2^-20 and 2^53 in magnitude, so sum * s1 is in FP32's normal range, and
-// sum * s1 * (a column's scale) leaves it only where the result does too: g then moves it
-// further out.
-//   Tiles that have such a row take a copy of the epilogue of their own (with a test of g in
-// the one epilogue 32768 x 4096 x 2048 with bias and GELU took 148 us instead of 142).
+// A warp's 64 columns of an accumulator times its rows' factors s (alpha times a row scale)
+// and the columns' scales `col`, in place: what the epilogue does on its way, for tiles with
+// a row whose s is outside [2^-100, 2^65).  Such an s is s1 g, s1 between 2^-104 and 2^65
+// and g a power of two: a nonzero sum of codes times scales is between 2^-20 and 2^53 in
+// magnitude, so sum * s1 is in FP32's normal range, and sum * s1 * (a column's scale) leaves
+// it only where the result does too: g then moves it further out.
+//   Ahead of the epilogue, which is as it was: 32768 x 4096 x 2048 with bias and GELU 141.6
+// us, with g in the epilogue 147.6, with a copy of it 143.4.
 constexpr uint32_t kNearExp = 127 - 100, kFarExp = 127 + 64;
-__device__ __forceinline__ float row_factor(float s, float& g) {
+__device__ __forceinline__ void scale_far(uint32_t taddr, float s, const float* col) {
   const uint32_t e = __float_as_uint(s) >> 23 & 0xFFu;
-  g = 1.0f;
+  float g = 1.0f;
   if (e > kFarExp && e < 255) {  // to 2^64 .. 2^65
     g = __uint_as_float((e - kFarExp + 127) << 23);
     s = __uint_as_float((__float_as_uint(s) & 0x807FFFFFu) | kFarExp << 23);
@@ -142,7 +143,18 @@ __device__ __forceinline__ float row_factor(float s, float& g) {
     g = 0x1p-45f;
     s *= 0x1p45f;
   }
-  return s;
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 32) {
+    uint32_t x[32];
+    tmem_ld_32cols(taddr + static_cast<uint32_t>(c), x);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      x[i] = __float_as_uint(__uint_as_float(x[i]) * s * col[c + i] * g);
+    tc::tmem_st_32cols(taddr + static_cast<uint32_t>(c), x);
+  }
+  tc::tc_wait_st();
+  __syncwarp();  // `col` has been read
 }
 
 template <bool Grouped, int BN, int Stages, int CG>
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
     if (odd && blockIdx.x == 0) atomicExch(p.status, static_cast<int>(DG_ERR_INVALID_ARG));
     __syncthreads();
     if (warp == 3)
-      count_row_blocks(off, pre, p.count, 128 * CG, p.n_blocks, blockIdx.x == 0, p.status, lane);
+      count_row_blocks(off, pre, p.count, 128 * CG, p.most_blocks, blockIdx.x == 0, p.status, lane);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -408,8 +420,8 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
       const N4Tile now = tile;
       const int col0 = now.n0 + first;
       const int row = min(now.row0 + in_tile + lane, p.M - 1);
-      const float s = p.alpha * row_next;
-      // (see row_factor: zero, infinite and NaN factors go that way too)
+      float s = p.alpha * row_next;
+      // (see scale_far: zero, infinite and NaN factors go that way too)
       const bool far = __any_sync(
           0xffffffffu, (__float_as_uint(s) >> 23 & 0xFFu) - kNearExp > kFarExp - kNearExp);
       __syncwarp();  // the last tile's have been read
@@ -429,102 +441,94 @@ __global__ void __launch_bounds__((4 + 4 * (BN / 64)) * 32, 1)
                            static_cast<uint32_t>(acc * BN + first);
       const bool stored = now.rows > in_tile && col0 < p.N;
       const int64_t drow = static_cast<int64_t>(row) * p.ldd;
-      auto columns = [&](auto far_rows, float s1, float g) {
-        constexpr bool Far = decltype(far_rows)::value;
+      if (far) {
+        scale_far(src, s, col);
+        s = 1.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) col[32 * i + lane] = 1.0f;
+        __syncwarp();
+      }
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t x[32];
-          tmem_ld_32cols(src + static_cast<uint32_t>(c), x);
-          tc_wait_ld();
-          if (c == 32) {  // all of the warp's columns are in registers
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-              // (a cluster-scope release would wait for the warp's stores: there is
-              // nothing in memory to release)
-              if (CG == 2)
-                mbar_arrive_remote(empty0 + static_cast<uint32_t>(acc * 8));
-              else
-                mbar_arrive(&tmem_empty[acc]);
-            }
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t x[32];
+        tmem_ld_32cols(src + static_cast<uint32_t>(c), x);
+        tc_wait_ld();
+        if (c == 32) {  // all of the warp's columns are in registers
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            // (a cluster-scope release would wait for the warp's stores: there is
+            // nothing in memory to release)
+            if (CG == 2)
+              mbar_arrive_remote(empty0 + static_cast<uint32_t>(acc * 8));
+            else
+              mbar_arrive(&tmem_empty[acc]);
           }
-          if (!stored || col0 + c >= p.N) continue;
-          float2 v[16];
-          const float2 s2 = make_float2(s1, s1);
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float4 k = *reinterpret_cast<const float4*>(col + c + 2 * i);
-            v[i] = mul2(mul2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
-                             s2),
-                        make_float2(k.x, k.y));
-            v[i + 1] = mul2(mul2(make_float2(__uint_as_float(x[2 * i + 2]),
-                                             __uint_as_float(x[2 * i + 3])),
-                                 s2),
-                            make_float2(k.z, k.w));
-          }
-          if (Far) {
-            const float2 g2 = make_float2(g, g);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], g2);
-          }
-          if (p.beta != 0.0f) {
-            const int64_t z = p.dtype_d == DG_F32 ? 4 : 2;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float t[16];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) t[2 * i] = v[8 * h + i].x, t[2 * i + 1] = v[8 * h + i].y;
-              add16(t, p.beta,
-                    static_cast<const uint8_t*>(p.D) + (drow + col0 + c + 16 * h) * z, p.dtype_d,
-                    p.N - (col0 + c + 16 * h));
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[8 * h + i] = make_float2(t[2 * i], t[2 * i + 1]);
-            }
-          }
-          if (p.flags & kEpiBias) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 k = *reinterpret_cast<const float2*>(col + 64 + c + 2 * i);
-              v[i] = make_float2(v[i].x + k.x, v[i].y + k.y);
-            }
-          }
-          if (p.flags & kEpiGelu) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = gelu2(v[i]);
-          }
-          if (c == 0 || box_cols == 32) {
-            if (lane == 0) bulk_wait_group_read<0>();  // the box's last store has read it
-            __syncwarp();
-          }
-          if (p.dtype_d == DG_F32) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4*>(box + box_offset(lane, q)) =
-                  make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
-          } else if (p.dtype_d == DG_BF16) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(box + box_offset(lane, c / 8 + q)) =
-                  pack8<BF16>(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(box + box_offset(lane, c / 8 + q)) =
-                  pack8<F16>(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          }
-          // the box is full, or ends with D
-          if (box_cols == 32)
-            send_box(&tmap_d, box, p, now, in_tile, col0 + c, 8, 0, lane);
-          else if (c == 32 || col0 + 32 >= p.N)
-            send_box(&tmap_d, box, p, now, in_tile, col0, c == 32 ? 8 : 4, 0, lane);
         }
-      };
-      if (!far) {
-        columns(std::false_type{}, s, 1.0f);
-      } else {
-        float g;
-        const float s1 = row_factor(s, g);
-        columns(std::true_type{}, s1, g);
+        if (!stored || col0 + c >= p.N) continue;
+        float2 v[16];
+        const float2 s2 = make_float2(s, s);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float4 k = *reinterpret_cast<const float4*>(col + c + 2 * i);
+          v[i] = mul2(mul2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                           s2),
+                      make_float2(k.x, k.y));
+          v[i + 1] = mul2(mul2(make_float2(__uint_as_float(x[2 * i + 2]),
+                                           __uint_as_float(x[2 * i + 3])),
+                               s2),
+                          make_float2(k.z, k.w));
+        }
+        if (p.beta != 0.0f) {
+          const int64_t z = p.dtype_d == DG_F32 ? 4 : 2;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[2 * i] = v[8 * h + i].x, t[2 * i + 1] = v[8 * h + i].y;
+            add16(t, p.beta,
+                  static_cast<const uint8_t*>(p.D) + (drow + col0 + c + 16 * h) * z, p.dtype_d,
+                  p.N - (col0 + c + 16 * h));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * h + i] = make_float2(t[2 * i], t[2 * i + 1]);
+          }
+        }
+        if (p.flags & kEpiBias) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 k = *reinterpret_cast<const float2*>(col + 64 + c + 2 * i);
+            v[i] = make_float2(v[i].x + k.x, v[i].y + k.y);
+          }
+        }
+        if (p.flags & kEpiGelu) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = gelu2(v[i]);
+        }
+        if (c == 0 || box_cols == 32) {
+          if (lane == 0) bulk_wait_group_read<0>();  // the box's last store has read it
+          __syncwarp();
+        }
+        if (p.dtype_d == DG_F32) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(box + box_offset(lane, q)) =
+                make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+        } else if (p.dtype_d == DG_BF16) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(box + box_offset(lane, c / 8 + q)) =
+                pack8<BF16>(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(box + box_offset(lane, c / 8 + q)) =
+                pack8<F16>(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+        // the box is full, or ends with D
+        if (box_cols == 32)
+          send_box(&tmap_d, box, p, now, in_tile, col0 + c, 8, 0, lane);
+        else if (c == 32 || col0 + 32 >= p.N)
+          send_box(&tmap_d, box, p, now, in_tile, col0, c == 32 ? 8 : 4, 0, lane);
       }
       if (++acc == 2) {
         acc = 0;
@@ -583,6 +587,7 @@ cudaError_t run_nvf4(const Nvf4Args& a) {
   p.N = static_cast<int>(a.N);
   p.m_blocks = static_cast<int>((a.M + 128 * CG - 1) / (128 * CG));
   p.n_blocks = static_cast<int>((a.N + BN - 1) / BN);
+  p.most_blocks = static_cast<uint32_t>(kMaxTiles / p.n_blocks);
   p.k_blocks = static_cast<int>((a.K + kStageK - 1) / kStageK);
   p.k_tiles = static_cast<int>((a.K + 63) / 64);
   const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_blocks;

@@ -16,12 +16,12 @@ constexpr int kMaxTiles = 1 << 30;  // tile numbers are 32-bit, and a walk steps
 // Segments in order have at most one part-filled block each, and the host has checked that
 // those make no more than kMaxTiles tiles.  Offsets that go back and forth make segments
 // that overlap, up to count / 2 times all rows (512 experts, 8192 rows in blocks of 8 and
-// 4096 tiles of columns: 2^31 tiles): the count stops at kMaxTiles, what lies behind it is
-// not computed, and `report` records it in the status word.
+// 4096 tiles of columns: 2^31 tiles): the count stops at `most` row blocks, kMaxTiles by the
+// tiles of columns, what lies behind it is not computed, and `report` records it in the
+// status word.
 __device__ __forceinline__ void count_row_blocks(const int* off, int* pre, int count, int rows,
-                                                 int col_tiles, bool report, int* status,
+                                                 uint32_t most, bool report, int* status,
                                                  int lane) {
-  const uint32_t most = static_cast<uint32_t>(kMaxTiles / col_tiles);
   uint32_t run = 0;
   bool over = false;
   if (lane == 0) pre[0] = 0;
