@@ -612,8 +612,10 @@ dg_status dg_moe_combine_backward(int64_t tokens, int64_t top_k, int64_t width, 
  *     line l of a tile (16 bytes) holds the scales of its rows l, 32 + l,
  *     64 + l and 96 + l, four bytes each.  Bytes of rows and blocks that are
  *     not there are 0 (in an operand: any E4M3 code but NaN's).
- *   Stacks of matrices: codes `stride` bytes apart, scales and row scales
- *     (rows FP32 each) one matrix after another.
+ *   Stacks of matrices: codes `stride` bytes apart, at least rows times the
+ *     pitch; scales and row scales (rows FP32 each) one matrix after another.
+ *     A stack that is quantized has its matrices at least rows * ldx elements
+ *     apart, one that is read back at least (rows - 1) * ldd + K.
  */
 
 /* Quantization of `count` matrices X (rows x K, FP16 or BF16; row pitch ldx and
@@ -685,7 +687,10 @@ dg_status dg_gemm_nvf4_grouped(int64_t count, int64_t rows, int64_t N, int64_t K
  * dg_gemm_fp8_grouped's B) or 4 bits (NVF4 stacks).  X is not quantized: it is
  * exact (but for values below 2^-31 of their row's largest, which may lose
  * bits), sums are FP32, and h is held in 22 bits (two FP16 values times a power
- * of two for each 32 of them).  Infinities and NaNs propagate.  The used
+ * of two for each 32 of them; fewer bits below 2^-122).  Infinities and NaNs
+ * propagate.  What scales a whole sum comes behind it: W2's sums are of h times
+ * codes (and times NVF4's block scales), and stay in FP32's range where
+ * 2688 * hidden * |h| (FP8: 2^16 * |h|) does.  The used
  * experts' weights are read once for up to 8 slots each (W1) and 4 (W2).  For a
  * decoding step; many tokens are faster through dg_moe_sort and the grouped
  * products.

@@ -34,9 +34,10 @@
 // clocks (with one for each K block and 8 rows, 990 clocks a stage).
 //
 // Measured, experts of 2048 x 2048, SwiGLU: 8 tokens, FP8, 454 MB of weights in 77
-// us (6.0 and 5.5 TB/s in the two products, HBM); 16 tokens, NVF4, 335 MB in 76.5 us
-// (5.5 and 4.8 TB/s, instructions: 315 for 16 rows x 256 values).  One token, 8 experts
-// of 4096 x 2048, GELU: FP8 27.3 us, NVF4 22.3, of which the kernels' starts are 6.
+// us (5.9 TB/s; 6.2 and 5.7 in the two products by themselves: HBM); 16 tokens, NVF4, 335
+// MB in 76.5 us (4.4 TB/s; 5.1 and 3.6: instructions, and h's two columns in the second).
+// One token, 8 experts of 4096 x 2048, GELU: FP8 27.5 us, NVF4 22.6, of which the
+// kernels' starts are 6.
 #include <algorithm>
 
 #include "convert.cuh"
@@ -454,10 +455,13 @@ __device__ __forceinline__ void prefetch_l2(const uint8_t* at, uint32_t bytes) {
   if (bytes > 0)
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
 }
-// The second product's first weights into L2, by the thread whose last loads have
+// Weights of the second product into L2, by the thread whose last loads have
 // landed: HBM would wait for the second kernel until the first one's last sums are
 // done and its own first loads are out.  (One token, FP8 27.7 us, was 29.2; with 128
 // KB a CTA 29.0, for NVF4 later than without; before the last loads have landed 28.1.)
+// They are the second kernel's first where its chunks and grid are the first one's: up
+// to four slots an expert, as with one token.  Else they are others that it reads: it
+// cuts an expert's slots by four, the first by eight.
 template <int Fmt>
 __device__ __forceinline__ void prefetch_next(const LayerParams& p, const Route& r, int chunks,
                                               int step) {

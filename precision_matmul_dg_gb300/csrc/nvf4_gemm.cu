@@ -687,9 +687,11 @@ cudaError_t run_nvf4(const Nvf4Args& a) {
 //   16 x 8192 x 8192   19.4 / 13.8 / 13.3      256 x 4096 x 4096   10.8 / 9.2 / 8.5
 //   256 x 8192 x 8192  17.0 / 14.8 / 22.6      1024 x 8192 x 8192  37.6 / 42.7 / 69.5
 //   1024 x 4096 x 4096 16.9 / 14.4 / 23.2      2048 x 4096 x 4096  22.7 / 24.4 / 38.1
-// Experts' row blocks are known on the device only, and a pair's second half is often
-// empty: pairs from 512 rows per expert, of those that the caller makes room for (64
-// experts, 4096 x 2048; 383 rows 119 / 113, 639 rows 185 / 187).
+// Experts' row blocks are known on the device only, and a pair's second half may be
+// empty: pairs from 512 rows per expert, of those that the caller makes room for.  64
+// experts, 4096 x 2048, GELU, us, pairs / 128: all experts of 256 rows 87 / 96, 384 146 /
+// 135, 512 150 / 175, 640 207 / 214, 1024 276 / 336; rows spread by half to either side,
+// room for 312 each 112 / 113, 472 156 / 162, 578 176 / 194, 678 203 / 227, 1048 299 / 342.
 cudaError_t launch_gemm_nvf4(const Nvf4Args& a) {
   const bool grouped = a.offsets != nullptr;
   auto cost = [&](int64_t row_blocks, int64_t cols, int64_t units, int64_t weight) {
@@ -698,8 +700,8 @@ cudaError_t launch_gemm_nvf4(const Nvf4Args& a) {
   const int64_t blocks = grouped ? a.M / 128 + std::min(a.count, a.M) : (a.M + 127) / 128;
   const int64_t c128 = cost(blocks, 128, a.sm_count, 30), c64 = cost(blocks, 64, a.sm_count, 29);
   if (grouped && a.M >= 512 * a.count) {
-    // a fifth stage where the experts' table leaves room (up to 239 of them; 64 experts,
-    // 639 rows each, GELU: 179.5 us, with four 188.4)
+    // a fifth stage where the experts' table leaves room (up to 239 of them; 4096 tokens,
+    // 8 of 64 experts, GELU: 179.5 us, with four 188.4)
     return N4Smem<192, 5, 2>::bytes(a.count) <= 227 * 1024 ? run_nvf4<true, 192, 5, 2>(a)
                                                           : run_nvf4<true, 192, 4, 2>(a);
   }
